@@ -17,6 +17,9 @@
  *   awq_fold_norm, awq_fold_linear  divide the operation that produces X by
  *                      s, so the scaled weights need no run-time division
  *   awq_w4a16_matmul   a consumer of the packed layout: Y = X·Ŵᵀ
+ *   awq_w4a16_lora_matmul, awq_w4a16_lora_backward  low-rank adapters of many
+ *                      requests beside a packed layer, and their gradient
+ *   awq_act_pack8, awq_act_unpack8  activation checkpoints in 8 bits
  *
  * Sources (page titles and sections):
  *   "AWQ and Activation-Aware Scaling", section "Scaling instead of
@@ -389,6 +392,73 @@ awq_status awq_w4a16_matmul(const void* X, awq_dtype dtype, int64_t T, int64_t N
                             const uint16_t* scales, int32_t group_size, void* Y, void* ws,
                             size_t ws_bytes, void* stream);
 
+/* Low-rank adapters beside a packed 4-bit layer. Each token row t of X [T, K]
+ * belongs to a request, whose adapter is a = ids[t] of L loaded ones; the
+ * packed layer (arguments as for awq_w4a16_matmul) is shared and frozen:
+ *   h_t = A_a·x_t,   y_t = Ŵ·x_t + scaling_a·B_a·h_t.
+ * A [L, r, K] and B [L, N, r] in X's type (bf16 or fp16), scaling [L] f32,
+ * ids [T] int32. An id outside [0, L) means no adapter (y_t = Ŵ·x_t, h_t =
+ * 0); ids may come in any order. r is a multiple of 8, 8..128 (pad shorter
+ * adapters with zeros); 1 <= L <= 4096. A, B, scaling and ids stay on the
+ * device: nothing is read back.
+ * Y [T, N] in X's type. For training, optionally (NULL = not wanted):
+ * H [T, r] f32 receives the h_t, and x8_codes [T, K] int8 with x8_steps
+ * [T, K/128] f32 the 8-bit checkpoint of X that awq_act_pack8 would write
+ * (both or neither).
+ * Sums are float32 and each output is rounded once; an adapter's NaN or
+ * infinity reaches its own tokens only. N a multiple of 8, K of 128, both
+ * and T within awq_w4a16_matmul's limits. X, qweight, qzeros, scales, A, B,
+ * Y, H, x8_codes and ws 16-byte aligned, scaling, ids and x8_steps 4-byte.
+ * Outputs may not overlap inputs. ws: at least
+ * awq_w4a16_lora_workspace_bytes(T, N, K, L, r, dtype) bytes (0 = invalid
+ * sizes). Does not synchronise. */
+size_t awq_w4a16_lora_workspace_bytes(int64_t T, int64_t N, int64_t K, int32_t L, int32_t r,
+                                      awq_dtype dtype);
+awq_status awq_w4a16_lora_matmul(const void* X, awq_dtype dtype, int64_t T, int64_t N, int64_t K,
+                                 const int32_t* qweight, const int32_t* qzeros,
+                                 const uint16_t* scales, int32_t group_size, const void* A,
+                                 const void* B, const float* scaling, const int32_t* ids,
+                                 int32_t L, int32_t r, void* Y, float* H, int8_t* x8_codes,
+                                 float* x8_steps, void* ws, size_t ws_bytes, void* stream);
+
+/* The gradient of awq_w4a16_lora_matmul for a loss whose gradient with
+ * respect to Y is dY [T, N] (in the adapters' type):
+ *   g_t = scaling_a·B_aᵀ·dy_t,   dx_t = Ŵᵀ·dy_t + A_aᵀ·g_t,
+ *   dA_a = Σ_{t: ids[t] = a} g_t·x_tᵀ,  dB_a = Σ_{t: ids[t] = a} scaling_a·dy_t·h_tᵀ.
+ * H [T, r] f32 is what the forward pass wrote (rows of tokens without an
+ * adapter are not read). X is the forward pass's input in dY's type with
+ * x8_steps NULL, or the int8 codes of its checkpoint with their steps; it is
+ * read for dA only. dX [T, K] (NULL = not wanted: neither the packed layer
+ * nor A is read then), dA [L, r, K] and dB [L, N, r] are overwritten, in dY's type,
+ * each value summed in float32 and rounded once; an adapter without tokens
+ * gets zeros. Sums run in an order that the arguments fix: equal calls give
+ * equal bits. Alignment as above (dX, dA, dB 16-byte); ws: at least
+ * awq_w4a16_lora_backward_workspace_bytes(T, N, K, L, r, dtype) bytes. N
+ * also below 2^22. Does not synchronise. */
+size_t awq_w4a16_lora_backward_workspace_bytes(int64_t T, int64_t N, int64_t K, int32_t L,
+                                               int32_t r, awq_dtype dtype);
+awq_status awq_w4a16_lora_backward(const void* dY, const void* X, const float* x8_steps,
+                                   const float* H, awq_dtype dtype, int64_t T, int64_t N,
+                                   int64_t K, const int32_t* qweight, const int32_t* qzeros,
+                                   const uint16_t* scales, int32_t group_size, const void* A,
+                                   const void* B, const float* scaling, const int32_t* ids,
+                                   int32_t L, int32_t r, void* dX, void* dA, void* dB, void* ws,
+                                   size_t ws_bytes, void* stream);
+
+/* Activation checkpoints in 8 bits: one step per token and 128 channels,
+ * IEEE float32 with one rounding per operation,
+ *   m = max(max |x|, 2^-100);  step = m / 127;  code = rint(x·(127 / m)),
+ * codes [T, K] int8 in -127..127 and steps [T, K/128] f32. A block that
+ * holds a NaN or an infinity gets the step NaN and codes 0, so that all of
+ * it comes back as NaN. awq_act_unpack8 writes x^ = code·step, one float32
+ * product rounded once to `dtype`. X [T, K] bf16, f16 or f32, K a multiple
+ * of 128, at most 2^34 elements; X and codes 16-byte aligned, steps 4-byte.
+ * Neither synchronises. */
+awq_status awq_act_pack8(const void* X, awq_dtype dtype, int64_t T, int64_t K, int8_t* codes,
+                         float* steps, void* stream);
+awq_status awq_act_unpack8(const int8_t* codes, const float* steps, awq_dtype dtype, int64_t T,
+                           int64_t K, void* X, void* stream);
+
 /* Message for the last non-OK status returned on the calling thread. */
 const char* awq_last_error(void);
 
@@ -399,10 +469,12 @@ const char* awq_last_error(void);
  * Kinds: 0 stats, 1 scale table, 2 transform (quantise/dequantise
  * candidates), 3 search GEMM, 4 reductions, 5 pack, 6 fold, 7 W4A16
  * dequantisation, 8 W4A16 GEMM or GEMV, 9 W4A16 GEMV reduction, 10 Gram
- * matrix build (transpose + G), 11 Gram-path candidate GEMM. */
+ * matrix build (transpose + G), 11 Gram-path candidate GEMM, 12 low-rank
+ * adapter calls (all kernels of a call as one), 13 8-bit checkpoints. */
 enum { AWQ_K_STATS = 0, AWQ_K_SCALE = 1, AWQ_K_TRANSFORM = 2, AWQ_K_GEMM = 3, AWQ_K_REDUCE = 4,
        AWQ_K_PACK = 5, AWQ_K_FOLD = 6, AWQ_K_DEQUANT = 7, AWQ_K_W4A16 = 8,
-       AWQ_K_W4A16_REDUCE = 9, AWQ_K_GRAM_BUILD = 10, AWQ_K_GRAM_SEARCH = 11, AWQ_K_COUNT = 12 };
+       AWQ_K_W4A16_REDUCE = 9, AWQ_K_GRAM_BUILD = 10, AWQ_K_GRAM_SEARCH = 11, AWQ_K_LORA = 12,
+       AWQ_K_ACT8 = 13, AWQ_K_COUNT = 14 };
 void awq_profile_enable(int on);
 void awq_profile_reset(void);
 awq_status awq_profile_read(int kind, double* total_ms, int64_t* launches);

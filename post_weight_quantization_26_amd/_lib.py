@@ -27,7 +27,7 @@ AWQ_SEARCH_SPLIT_E = 1
 AWQ_SEARCH_FUSED = 2
 KERNEL_KINDS = {"stats": 0, "scale": 1, "transform": 2, "gemm": 3, "reduce": 4, "pack": 5,
                 "fold": 6, "dequant": 7, "w4a16": 8, "w4a16_reduce": 9, "gram_build": 10,
-                "gram_search": 11}
+                "gram_search": 11, "lora": 12, "act8": 13}
 
 
 class QConfig(ctypes.Structure):
@@ -93,6 +93,18 @@ SIGNATURES = {
                                         c_i32, c_vp, c_vp, c_sz, c_vp]),
     "awq_w3a16_matmul": (ctypes.c_int, [c_vp, ctypes.c_int, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp,
                                         c_i32, c_vp, c_vp, c_sz, c_vp]),
+    "awq_w4a16_lora_workspace_bytes": (c_sz, [c_i64, c_i64, c_i64, c_i32, c_i32, ctypes.c_int]),
+    "awq_w4a16_lora_matmul": (ctypes.c_int, [c_vp, ctypes.c_int, c_i64, c_i64, c_i64, c_vp, c_vp,
+                                             c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_i32, c_i32,
+                                             c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "awq_w4a16_lora_backward_workspace_bytes": (c_sz, [c_i64, c_i64, c_i64, c_i32, c_i32,
+                                                       ctypes.c_int]),
+    "awq_w4a16_lora_backward": (ctypes.c_int, [c_vp, c_vp, c_vp, c_vp, ctypes.c_int, c_i64, c_i64,
+                                               c_i64, c_vp, c_vp, c_vp, c_i32, c_vp, c_vp, c_vp,
+                                               c_vp, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_sz,
+                                               c_vp]),
+    "awq_act_pack8": (ctypes.c_int, [c_vp, ctypes.c_int, c_i64, c_i64, c_vp, c_vp, c_vp]),
+    "awq_act_unpack8": (ctypes.c_int, [c_vp, c_vp, ctypes.c_int, c_i64, c_i64, c_vp, c_vp]),
     "awq_last_error": (ctypes.c_char_p, []),
     "awq_profile_enable": (None, [ctypes.c_int]),
     "awq_profile_reset": (None, []),

@@ -7,6 +7,7 @@ in section 9 (zero point on, group 128, 4 bits).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional, Sequence
 
@@ -381,6 +382,171 @@ def w4a16_matmul(X: torch.Tensor, qweight: torch.Tensor, qzeros: torch.Tensor,
     L.check(fn(_ptr(X), _dtype(X), T, N, K, _ptr(qweight), _ptr(qzeros), _ptr(scales), int(group),
                _ptr(Y), _ptr(ws), ws.numel(), _stream()))
     return Y
+
+
+def _on_device_of(t: torch.Tensor):
+    """Makes t's GPU the current one, so that the stream and the kernels are its."""
+    if t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
+
+
+def _same_device(t: torch.Tensor, **others) -> None:
+    for name, o in others.items():
+        if o is not None and o.device != t.device:
+            raise ValueError(f"{name} is on {o.device}, not on {t.device}")
+
+
+def _out(t: Optional[torch.Tensor], shape, dtype, like: torch.Tensor, name: str) -> torch.Tensor:
+    """The caller's output buffer, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _dev(t, name)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {tuple(shape)} {dtype}")
+    return t
+
+
+def w4a16_lora_workspace_bytes(T: int, N: int, K: int, L_: int, r: int,
+                               dtype: torch.dtype) -> int:
+    """Workspace of w4a16_lora_matmul for L_ adapters of rank r."""
+    return int(L.lib().awq_w4a16_lora_workspace_bytes(T, N, K, L_, r, _DT[dtype]))
+
+
+def w4a16_lora_backward_workspace_bytes(T: int, N: int, K: int, L_: int, r: int,
+                                        dtype: torch.dtype) -> int:
+    """Workspace of w4a16_lora_backward for L_ adapters of rank r."""
+    return int(L.lib().awq_w4a16_lora_backward_workspace_bytes(T, N, K, L_, r, _DT[dtype]))
+
+
+def _lora_args(V: torch.Tensor, V_cols: str, qweight, qzeros, scales, A, B, scaling, ids,
+               group: int):
+    """Checks what the forward and the backward call share; (T, N, K, L, r)."""
+    for t, name in ((V, V_cols), (qweight, "qweight"), (qzeros, "qzeros"), (scales, "scales"),
+                    (A, "A"), (B, "B"), (scaling, "scaling"), (ids, "ids")):
+        _dev(t, name)
+    _same_device(V, qweight=qweight, qzeros=qzeros, scales=scales, A=A, B=B, scaling=scaling,
+                 ids=ids)
+    if V.dim() != 2 or qweight.dim() != 2 or scales.dim() != 2 or A.dim() != 3:
+        raise ValueError(f"{V_cols}, qweight and scales must have 2 dimensions, A 3")
+    T, K, N = V.shape[0], qweight.shape[0], scales.shape[1]
+    n, r = A.shape[0], A.shape[1]
+    if qweight.shape[1] * 8 != N or qzeros.shape != (K // group, N // 8) or \
+            scales.shape[0] != K // group or V.shape[1] != (K if V_cols == "X" else N):
+        raise ValueError(f"packed layer shapes do not match {V_cols} and the group size")
+    if qweight.dtype != torch.int32 or qzeros.dtype != torch.int32 or \
+            scales.dtype != torch.float16:
+        raise ValueError("qweight and qzeros must be int32, scales float16")
+    if A.shape != (n, r, K) or B.shape != (n, N, r) or scaling.shape != (n,) or ids.shape != (T,):
+        raise ValueError("adapters must be A [L, r, K], B [L, N, r], scaling [L], ids [T]")
+    if A.dtype != V.dtype or B.dtype != V.dtype:
+        raise ValueError(f"A and B must share {V_cols}'s dtype")
+    if scaling.dtype != torch.float32 or ids.dtype != torch.int32:
+        raise ValueError("scaling must be float32 and ids int32")
+    return T, N, K, n, r
+
+
+def w4a16_lora_matmul(X: torch.Tensor, qweight: torch.Tensor, qzeros: torch.Tensor,
+                      scales: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                      scaling: torch.Tensor, ids: torch.Tensor, group: int = DEFAULT_GROUP,
+                      ws: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                      h: Optional[torch.Tensor] = None, x8=None) -> torch.Tensor:
+    """Low-rank adapters of many requests beside a packed 4-bit layer:
+    Y[t] = Ŵ·x_t + scaling[a]·B[a]·(A[a]·x_t) with a = ids[t]; an id outside
+    [0, L) means no adapter. X [T, K] and the layer as in w4a16_matmul, A
+    [L, r, K] and B [L, N, r] in X's dtype, scaling [L] float32, ids [T]
+    int32. For training: ``h`` [T, r] float32 receives A[a]·x_t and ``x8`` =
+    (codes, steps) the checkpoint of X that act_pack8 would make, both for
+    w4a16_lora_backward. Returns Y [T, N] in X's dtype."""
+    T, N, K, n, r = _lora_args(X, "X", qweight, qzeros, scales, A, B, scaling, ids, group)
+    Y = _out(out, (T, N), X.dtype, X, "out")
+    codes = steps = None
+    if h is not None:
+        _out(h, (T, r), torch.float32, X, "h")
+    if x8 is not None:
+        codes = _out(x8[0], (T, K), torch.int8, X, "x8 codes")
+        steps = _out(x8[1], (T, K // 128), torch.float32, X, "x8 steps")
+    _same_device(X, out=Y, h=h, codes=codes, steps=steps, ws=ws)
+    with _on_device_of(X):
+        if ws is None:
+            ws = _workspace(ws, w4a16_lora_workspace_bytes(T, N, K, n, r, X.dtype), X.device)
+        L.check(L.lib().awq_w4a16_lora_matmul(
+            _ptr(X), _dtype(X), T, N, K, _ptr(qweight), _ptr(qzeros), _ptr(scales), int(group),
+            _ptr(A), _ptr(B), _ptr(scaling), _ptr(ids), n, r, _ptr(Y), _ptr(h), _ptr(codes),
+            _ptr(steps), _ptr(ws), ws.numel() * ws.element_size(), _stream()))
+    return Y
+
+
+def w4a16_lora_backward(dY: torch.Tensor, X, h: torch.Tensor, qweight: torch.Tensor,
+                        qzeros: torch.Tensor, scales: torch.Tensor, A: torch.Tensor,
+                        B: torch.Tensor, scaling: torch.Tensor, ids: torch.Tensor,
+                        group: int = DEFAULT_GROUP, ws: Optional[torch.Tensor] = None, out=None,
+                        want_dx: bool = True):
+    """The gradient of w4a16_lora_matmul: (dX [T, K], dA [L, r, K], dB
+    [L, N, r]) in dY's dtype from dY [T, N], the ``h`` that the forward call
+    wrote and X, its input or that input's checkpoint (codes, steps). dX is
+    None with want_dx False. ``out`` = (dX, dA, dB) gives the buffers."""
+    T, N, K, n, r = _lora_args(dY, "dY", qweight, qzeros, scales, A, B, scaling, ids, group)
+    steps = None
+    if isinstance(X, (tuple, list)):
+        X, steps = X
+        _dev(steps, "steps")
+        if X.dtype != torch.int8 or steps.dtype != torch.float32 or steps.shape != (T, K // 128):
+            raise ValueError("a checkpoint is (codes [T, K] int8, steps [T, K / 128] float32)")
+    elif X.dtype != dY.dtype:
+        raise ValueError("X must share dY's dtype or be a checkpoint")
+    _dev(X, "X")
+    if X.shape != (T, K):
+        raise ValueError("X must be [T, K]")
+    _dev(h, "h")
+    _out(h, (T, r), torch.float32, dY, "h")
+    dX, dA, dB = out if out is not None else (None, None, None)
+    dX = _out(dX, (T, K), dY.dtype, dY, "dX") if want_dx else None
+    dA = _out(dA, (n, r, K), dY.dtype, dY, "dA")
+    dB = _out(dB, (n, N, r), dY.dtype, dY, "dB")
+    _same_device(dY, X=X, steps=steps, h=h, dX=dX, dA=dA, dB=dB, ws=ws)
+    with _on_device_of(dY):
+        if ws is None:
+            ws = _workspace(ws, w4a16_lora_backward_workspace_bytes(T, N, K, n, r, dY.dtype),
+                            dY.device)
+        L.check(L.lib().awq_w4a16_lora_backward(
+            _ptr(dY), _ptr(X), _ptr(steps), _ptr(h), _dtype(dY), T, N, K, _ptr(qweight),
+            _ptr(qzeros), _ptr(scales), int(group), _ptr(A), _ptr(B), _ptr(scaling), _ptr(ids),
+            n, r, _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel() * ws.element_size(),
+            _stream()))
+    return dX, dA, dB
+
+
+def act_pack8(X: torch.Tensor, out=None):
+    """An 8-bit checkpoint of activations X [T, K] (bf16, float16 or float32,
+    K a multiple of 128): (codes [T, K] int8, steps [T, K / 128] float32)
+    with x ≈ code·step, step = max |x| / 127 over a token's 128 channels."""
+    _dev(X, "X")
+    T, K = X.shape
+    codes, steps = out if out is not None else (None, None)
+    codes = _out(codes, (T, K), torch.int8, X, "codes")
+    steps = _out(steps, (T, K // 128), torch.float32, X, "steps")
+    _same_device(X, codes=codes, steps=steps)
+    with _on_device_of(X):
+        L.check(L.lib().awq_act_pack8(_ptr(X), _dtype(X), T, K, _ptr(codes), _ptr(steps),
+                                      _stream()))
+    return codes, steps
+
+
+def act_unpack8(codes: torch.Tensor, steps: torch.Tensor, dtype: torch.dtype,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The activations that a checkpoint of act_pack8 stands for, code·step
+    rounded once to ``dtype``."""
+    _dev(codes, "codes"), _dev(steps, "steps")
+    T, K = codes.shape
+    if codes.dtype != torch.int8 or steps.dtype != torch.float32 or steps.shape != (T, K // 128):
+        raise ValueError("a checkpoint is (codes [T, K] int8, steps [T, K / 128] float32)")
+    X = _out(out, (T, K), dtype, codes, "out")
+    _same_device(codes, steps=steps, out=X)
+    with _on_device_of(codes):
+        L.check(L.lib().awq_act_unpack8(_ptr(codes), _ptr(steps), _dtype(X), T, K, _ptr(X),
+                                        _stream()))
+    return X
 
 
 def profile_enable(on: bool = True) -> None:

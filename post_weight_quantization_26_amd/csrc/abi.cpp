@@ -8,6 +8,7 @@
 #include <vector>
 
 #include "awq_internal.h"
+#include "lora.h"
 
 namespace awq {
 // Launchers (HIP translation units).
@@ -743,6 +744,83 @@ extern "C" awq_status awq_w3a16_matmul(const void* X, awq_dtype dtype, int64_t T
                                            static_cast<uint16_t*>(Y), st);
                 }),
           "w3a16 gemm");
+  return AWQ_OK;
+}
+
+extern "C" awq_status awq_w4a16_lora_matmul(
+    const void* X, awq_dtype dtype, int64_t T, int64_t N, int64_t K, const int32_t* qweight,
+    const int32_t* qzeros, const uint16_t* scales, int32_t group_size, const void* A,
+    const void* B, const float* scaling, const int32_t* ids, int32_t L, int32_t r, void* Y,
+    float* H, int8_t* x8_codes, float* x8_steps, void* ws, size_t ws_bytes, void* stream) {
+  awq_status st_ = check_lora(X, dtype, T, N, K, qweight, qzeros, scales, group_size, A, B,
+                              scaling, ids, L, r, Y, H, x8_codes, x8_steps, ws, ws_bytes);
+  if (st_ != AWQ_OK) return st_;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const LoraLayout l = lora_layout(T, N, K, L, r);
+  LoraForward p{};
+  p.X = static_cast<const uint16_t*>(X);
+  p.T = T;
+  p.w = {qweight, qzeros, scales, N, K, group_size};
+  p.s = {static_cast<const uint16_t*>(A), static_cast<const uint16_t*>(B), scaling, ids, L, r};
+  p.Y = static_cast<uint16_t*>(Y);
+  p.H = H ? H : at<float>(ws, l.h);
+  p.f16 = dtype == AWQ_F16;
+  AWQ_HIP(timed(AWQ_K_LORA, st, [&] { return launch_lora_forward(p, st); }), "lora_matmul");
+  if (x8_codes)
+    AWQ_HIP(timed(AWQ_K_ACT8, st,
+                  [&] { return launch_act_pack8(X, dt(dtype), T, K, x8_codes, x8_steps, st); }),
+            "lora_matmul checkpoint");
+  return AWQ_OK;
+}
+
+extern "C" awq_status awq_w4a16_lora_backward(
+    const void* dY, const void* X, const float* x8_steps, const float* H, awq_dtype dtype,
+    int64_t T, int64_t N, int64_t K, const int32_t* qweight, const int32_t* qzeros,
+    const uint16_t* scales, int32_t group_size, const void* A, const void* B,
+    const float* scaling, const int32_t* ids, int32_t L, int32_t r, void* dX, void* dA, void* dB,
+    void* ws, size_t ws_bytes, void* stream) {
+  awq_status st_ = check_lora_backward(dY, X, x8_steps, H, dtype, T, N, K, qweight, qzeros,
+                                       scales, group_size, A, B, scaling, ids, L, r, dX, dA, dB,
+                                       ws, ws_bytes);
+  if (st_ != AWQ_OK) return st_;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const LoraLayout l = lora_backward_layout(T, N, K, L, r);
+  LoraBackward p{};
+  p.dY = static_cast<const uint16_t*>(dY);
+  p.X = X;
+  p.steps = x8_steps;
+  p.H = H;
+  p.T = T;
+  p.w = {qweight, qzeros, scales, N, K, group_size};
+  p.s = {static_cast<const uint16_t*>(A), static_cast<const uint16_t*>(B), scaling, ids, L, r};
+  p.G = at<float>(ws, l.h);
+  p.dX = static_cast<uint16_t*>(dX);
+  p.dA = static_cast<uint16_t*>(dA);
+  p.dB = static_cast<uint16_t*>(dB);
+  p.f16 = dtype == AWQ_F16;
+  AWQ_HIP(timed(AWQ_K_LORA, st, [&] { return launch_lora_backward(p, st); }), "lora_backward");
+  return AWQ_OK;
+}
+
+extern "C" awq_status awq_act_pack8(const void* X, awq_dtype dtype, int64_t T, int64_t K,
+                                    int8_t* codes, float* steps, void* stream) {
+  awq_status st_ = check_act8("act_pack8", X, dtype, T, K, codes, steps);
+  if (st_ != AWQ_OK) return st_;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  AWQ_HIP(timed(AWQ_K_ACT8, st,
+                [&] { return launch_act_pack8(X, dt(dtype), T, K, codes, steps, st); }),
+          "act_pack8");
+  return AWQ_OK;
+}
+
+extern "C" awq_status awq_act_unpack8(const int8_t* codes, const float* steps, awq_dtype dtype,
+                                      int64_t T, int64_t K, void* X, void* stream) {
+  awq_status st_ = check_act8("act_unpack8", X, dtype, T, K, codes, steps);
+  if (st_ != AWQ_OK) return st_;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  AWQ_HIP(timed(AWQ_K_ACT8, st,
+                [&] { return launch_act_unpack8(codes, steps, dt(dtype), T, K, X, st); }),
+          "act_unpack8");
   return AWQ_OK;
 }
 

@@ -203,6 +203,32 @@ awq_status check_w4a16(const void* X, awq_dtype d, int64_t T, int64_t N, int64_t
                        const int32_t* qweight, const int32_t* qzeros, const uint16_t* scales,
                        int32_t group, const void* Y, const void* ws, size_t ws_bytes);
 
+// Low-rank adapters: byte offsets of the regions of a call's workspace.
+constexpr int kLoraMaxRank = 128;
+constexpr int kLoraMaxAdapters = 4096;
+struct LoraLayout {
+  size_t h;       // [T, r] f32: H (forward) or G (backward)
+  size_t total;
+};
+LoraLayout lora_layout(int64_t T, int64_t N, int64_t K, int32_t L, int32_t r);
+LoraLayout lora_backward_layout(int64_t T, int64_t N, int64_t K, int32_t L, int32_t r);
+bool lora_sizes_ok(int64_t T, int64_t N, int64_t K, int32_t L, int32_t r, awq_dtype d);
+awq_status check_lora(const void* X, awq_dtype d, int64_t T, int64_t N, int64_t K,
+                      const int32_t* qweight, const int32_t* qzeros, const uint16_t* scales,
+                      int32_t group, const void* A, const void* B, const float* scaling,
+                      const int32_t* ids, int32_t L, int32_t r, const void* Y, const float* H,
+                      const void* x8_codes, const float* x8_steps, const void* ws,
+                      size_t ws_bytes);
+awq_status check_lora_backward(const void* dY, const void* X, const float* x8_steps,
+                               const float* H, awq_dtype d, int64_t T, int64_t N, int64_t K,
+                               const int32_t* qweight, const int32_t* qzeros,
+                               const uint16_t* scales, int32_t group, const void* A,
+                               const void* B, const float* scaling, const int32_t* ids,
+                               int32_t L, int32_t r, const void* dX, const void* dA,
+                               const void* dB, const void* ws, size_t ws_bytes);
+awq_status check_act8(const char* name, const void* X, awq_dtype d, int64_t T, int64_t K,
+                      const void* codes, const float* steps);
+
 awq_status set_error(awq_status st, const char* fmt, ...);
 
 }  // namespace awq

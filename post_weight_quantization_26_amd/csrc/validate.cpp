@@ -482,7 +482,150 @@ awq_status check_w3a16(const void* X, awq_dtype d, int64_t T, int64_t N, int64_t
   return AWQ_OK;
 }
 
+// ---------------------------------------------------------------------------
+// low-rank adapters and 8-bit checkpoints
+// ---------------------------------------------------------------------------
+
+bool lora_sizes_ok(int64_t T, int64_t N, int64_t K, int32_t L, int32_t r, awq_dtype d) {
+  return T >= 1 && N >= 1 && K >= 1 && T <= kMaxDim && N <= kMaxDim && K <= kMaxDim &&
+         (d == AWQ_BF16 || d == AWQ_F16) && N % 8 == 0 && K % kTileK == 0 && L >= 1 &&
+         L <= kLoraMaxAdapters && r >= 8 && r <= kLoraMaxRank && r % 8 == 0;
+}
+
+LoraLayout lora_layout(int64_t T, int64_t, int64_t, int32_t, int32_t r) {
+  LoraLayout l{};
+  l.h = 0;
+  l.total = align_up(size_t(T) * size_t(r) * 4);
+  return l;
+}
+
+LoraLayout lora_backward_layout(int64_t T, int64_t, int64_t, int32_t, int32_t r) {
+  LoraLayout l{};
+  l.h = 0;
+  l.total = align_up(size_t(T) * size_t(r) * 4);
+  return l;
+}
+
+// What the forward and the backward call share: the layer, the adapters and
+// the sizes. V is X or dY.
+static awq_status check_lora_common(const char* name, const void* V, awq_dtype d, int64_t T,
+                                    int64_t N, int64_t K, const int32_t* qweight,
+                                    const int32_t* qzeros, const uint16_t* scales, int32_t group,
+                                    const void* A, const void* B, const float* scaling,
+                                    const int32_t* ids, int32_t L, int32_t r) {
+  if (!V || !qweight || !qzeros || !scales || !A || !B || !scaling || !ids)
+    return set_error(AWQ_E_INVALID, "%s: NULL pointer argument", name);
+  if (!dtype_ok(d)) return set_error(AWQ_E_INVALID, "%s: unknown dtype %d", name, int(d));
+  if (d == AWQ_F32)
+    return set_error(AWQ_E_UNSUPPORTED, "%s: activations must be bf16 or fp16", name);
+  if (T < 1 || N < 1 || K < 1 || T > kMaxDim || N > kMaxDim || K > kMaxDim || L < 1 || r < 1)
+    return set_error(AWQ_E_INVALID, "%s: bad shape T=%lld N=%lld K=%lld L=%d r=%d", name,
+                     (long long)T, (long long)N, (long long)K, int(L), int(r));
+  if (group != 32 && group != 64 && group != 128)
+    return set_error(AWQ_E_UNSUPPORTED, "%s: group_size %d (32, 64 or 128)", name, group);
+  if (N % 8)
+    return set_error(AWQ_E_INVALID, "%s: N=%lld not a multiple of 8", name, (long long)N);
+  if (K % kTileK)
+    return set_error(AWQ_E_INVALID, "%s: K=%lld not a multiple of 128", name, (long long)K);
+  if (r % 8 || r > kLoraMaxRank)
+    return set_error(AWQ_E_UNSUPPORTED, "%s: rank %d (a multiple of 8 up to %d)", name, int(r),
+                     kLoraMaxRank);
+  if (L > kLoraMaxAdapters)
+    return set_error(AWQ_E_UNSUPPORTED, "%s: %d adapters (at most %d)", name, int(L),
+                     kLoraMaxAdapters);
+  if (!tile_rows_fit(K) || N * K > kMaxMatrixElems)
+    return set_error(AWQ_E_UNSUPPORTED,
+                     "%s: K=%lld, N=%lld exceed the 32-bit offsets (512 * K must stay below "
+                     "2^31, N*K at most 2^34)", name, (long long)K, (long long)N);
+  if (!grid_fits(search_gemm_blocks(T, std::max(N, K), AWQ_BF16), 256) || !grid_fits(T, 256))
+    return set_error(AWQ_E_UNSUPPORTED, "%s: T=%lld x N=%lld exceed the GEMM's grid", name,
+                     (long long)T, (long long)N);
+  if (!aligned16(V) || !aligned16(qweight) || !aligned16(qzeros) || !aligned16(scales) ||
+      !aligned16(A) || !aligned16(B) || !aligned4(scaling) || !aligned4(ids))
+    return set_error(AWQ_E_INVALID,
+                     "%s: the layer, the adapters and the activations must be 16-byte aligned, "
+                     "scaling and ids 4", name);
+  return AWQ_OK;
+}
+
+awq_status check_lora(const void* X, awq_dtype d, int64_t T, int64_t N, int64_t K,
+                      const int32_t* qweight, const int32_t* qzeros, const uint16_t* scales,
+                      int32_t group, const void* A, const void* B, const float* scaling,
+                      const int32_t* ids, int32_t L, int32_t r, const void* Y, const float* H,
+                      const void* x8_codes, const float* x8_steps, const void* ws,
+                      size_t ws_bytes) {
+  const char* name = "w4a16_lora_matmul";
+  if (!Y) return set_error(AWQ_E_INVALID, "%s: NULL pointer argument", name);
+  const awq_status st = check_lora_common(name, X, d, T, N, K, qweight, qzeros, scales, group, A,
+                                          B, scaling, ids, L, r);
+  if (st != AWQ_OK) return st;
+  if (!x8_codes != !x8_steps)
+    return set_error(AWQ_E_INVALID, "%s: a checkpoint needs both codes and steps", name);
+  if (!aligned16(Y) || !aligned16(H) || !aligned16(x8_codes) || !aligned4(x8_steps))
+    return set_error(AWQ_E_INVALID, "%s: Y, H and codes must be 16-byte aligned, steps 4", name);
+  const size_t need = lora_layout(T, N, K, L, r).total;
+  if (!ws || !aligned16(ws) || ws_bytes < need)
+    return set_error(AWQ_E_WORKSPACE, "%s: workspace needs %zu bytes (16-byte aligned)", name,
+                     need);
+  return AWQ_OK;
+}
+
+awq_status check_lora_backward(const void* dY, const void* X, const float* x8_steps,
+                               const float* H, awq_dtype d, int64_t T, int64_t N, int64_t K,
+                               const int32_t* qweight, const int32_t* qzeros,
+                               const uint16_t* scales, int32_t group, const void* A,
+                               const void* B, const float* scaling, const int32_t* ids,
+                               int32_t L, int32_t r, const void* dX, const void* dA,
+                               const void* dB, const void* ws, size_t ws_bytes) {
+  const char* name = "w4a16_lora_backward";
+  if (!X || !H || !dA || !dB) return set_error(AWQ_E_INVALID, "%s: NULL pointer argument", name);
+  const awq_status st = check_lora_common(name, dY, d, T, N, K, qweight, qzeros, scales, group, A,
+                                          B, scaling, ids, L, r);
+  if (st != AWQ_OK) return st;
+  if (!tile_rows_fit(N))
+    return set_error(AWQ_E_UNSUPPORTED, "%s: N=%lld exceeds the 32-bit offsets (512 * N must "
+                     "stay below 2^31)", name, (long long)N);
+  if (!aligned16(X) || !aligned16(H) || !aligned4(x8_steps) || !aligned16(dX) ||
+      !aligned16(dA) || !aligned16(dB))
+    return set_error(AWQ_E_INVALID,
+                     "%s: X, H and the gradients must be 16-byte aligned, steps 4", name);
+  const size_t need = lora_backward_layout(T, N, K, L, r).total;
+  if (!ws || !aligned16(ws) || ws_bytes < need)
+    return set_error(AWQ_E_WORKSPACE, "%s: workspace needs %zu bytes (16-byte aligned)", name,
+                     need);
+  return AWQ_OK;
+}
+
+awq_status check_act8(const char* name, const void* X, awq_dtype d, int64_t T, int64_t K,
+                      const void* codes, const float* steps) {
+  if (!X || !codes || !steps) return set_error(AWQ_E_INVALID, "%s: NULL pointer argument", name);
+  if (!dtype_ok(d)) return set_error(AWQ_E_INVALID, "%s: unknown dtype %d", name, int(d));
+  if (T < 1 || K < 1 || T > kMaxDim || K > kMaxDim)
+    return set_error(AWQ_E_INVALID, "%s: bad shape T=%lld K=%lld", name, (long long)T,
+                     (long long)K);
+  if (K % kTileK)
+    return set_error(AWQ_E_INVALID, "%s: K=%lld not a multiple of 128", name, (long long)K);
+  if (T * K > kMaxMatrixElems)
+    return set_error(AWQ_E_UNSUPPORTED, "%s: T*K=%lld exceeds 2^34", name, (long long)(T * K));
+  if (!aligned16(X) || !aligned16(codes) || !aligned4(steps))
+    return set_error(AWQ_E_INVALID, "%s: X and codes must be 16-byte aligned, steps 4", name);
+  return AWQ_OK;
+}
+
 }  // namespace awq
+
+extern "C" size_t awq_w4a16_lora_workspace_bytes(int64_t T, int64_t N, int64_t K, int32_t L,
+                                                 int32_t r, awq_dtype dtype) {
+  using namespace awq;
+  return lora_sizes_ok(T, N, K, L, r, dtype) ? lora_layout(T, N, K, L, r).total : 0;
+}
+
+extern "C" size_t awq_w4a16_lora_backward_workspace_bytes(int64_t T, int64_t N, int64_t K,
+                                                          int32_t L, int32_t r,
+                                                          awq_dtype dtype) {
+  using namespace awq;
+  return lora_sizes_ok(T, N, K, L, r, dtype) ? lora_backward_layout(T, N, K, L, r).total : 0;
+}
 
 extern "C" size_t awq_w4a16_workspace_bytes(int64_t T, int64_t N, int64_t K, awq_dtype dtype) {
   using namespace awq;

@@ -1,0 +1,446 @@
+"""GPU: low-rank adapters beside a packed layer, their gradient, and the 8-bit
+checkpoints between them, against float64 (lora_reference.py).
+
+Bounds, per output element (u = half a step of the 16-bit type, LOW = what two
+16-bit halves lose, γ_n = float32 sums of n products):
+  * H: γ_K·Σ|x||A|.
+  * Y: the shared product as in test_gpu_w4a16.py — γ_{K+4}·Σ|x|(32 + q + z)·s
+    for T <= 16 (exact Ŵ), (u + γ_K)·Σ|x||ŵ| above (Ŵ rounded once to the
+    16-bit type) — plus (LOW + γ_{K+r+4})·c·Σ|B||A||x| for the adapter, plus u·|Y|
+    for the output's rounding.
+  * dX: (u + γ_N)·Σ|dy||ŵ| + (LOW + γ_{N+r+4})·Σ|A||g| + u·|dX|.
+  * dA, dB: (LOW + γ_{N+T+4})·Σ|g||x| and (LOW + γ_{T+4})·Σ|c dy||h|, + u·|·|;
+    |g| stands for c·Σ|dy||B|.
+  * every output: + tiny, the smallest normal of its type.
+The checkpoint is equal bit for bit.
+"""
+import numpy as np
+import pytest
+import torch
+
+import lora_reference as R
+import oracle as O
+from test_gpu_parity import to_dev
+from test_gpu_w4a16 import _dec, _enc, packed_layer
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def api():
+    if not torch.cuda.is_available():
+        raise RuntimeError("GPU tests need a GPU")
+    from post_weight_quantization_26_amd import api as A
+    return A
+
+
+TD = {"bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to("cuda:0")
+
+
+def make_ids(T, L, kind, rng):
+    if kind == "none":
+        return np.full(T, -1, np.int32)
+    if kind == "one":
+        return np.full(T, L - 1, np.int32)
+    if kind == "tokens":                   # any adapter or none, and ids no adapter has
+        ids = rng.integers(-1, L, T).astype(np.int32)
+        odd = rng.random(T) < 0.1
+        ids[odd] = rng.choice(np.array([-7, L, L + 3, 2 ** 31 - 1, -2 ** 31], np.int32), odd.sum())
+        return ids
+    cuts = np.sort(rng.integers(0, T, min(T, 2 * L)))   # runs of tokens
+    run = np.searchsorted(cuts, np.arange(T), side="right")
+    return rng.integers(-1, L, len(cuts) + 1).astype(np.int32)[run]
+
+
+class Problem:
+    """One layer, adapters, tokens; float64 values and device tensors."""
+
+    def __init__(self, T, N, K, r, L, dtype, group=128, kind="runs", seed=0, layer=None):
+        rng = np.random.default_rng(seed)
+        self.T, self.N, self.K, self.r, self.L, self.dtype, self.group = T, N, K, r, L, dtype, group
+        self.qw, self.qz, self.sc = layer if layer else packed_layer(N, K, group, seed % 7)
+        self.w = O.dequantize_packed(self.qw, self.qz, self.sc, N, 4, group)
+        enc = lambda a: _enc(a.astype(np.float32), dtype)
+        self.Xb = enc(rng.standard_normal((T, K)) * np.exp(0.5 * rng.standard_normal(K)))
+        self.Ab = enc(rng.standard_normal((L, r, K)) / np.sqrt(K))
+        self.Bb = enc(rng.standard_normal((L, N, r)) * 0.1)
+        self.dYb = enc(rng.standard_normal((T, N)) * 0.05)
+        self.c = (rng.random(L) * 2 - 0.5).astype(np.float32)
+        self.ids = make_ids(T, L, kind, rng)
+        self.x, self.A, self.B, self.dy = (
+            _dec(b, dtype).astype(np.float64).reshape(b.shape)
+            for b in (self.Xb, self.Ab, self.Bb, self.dYb))
+
+    def td(self, bits):
+        return to_dev(bits.reshape(-1, bits.shape[-1]), self.dtype).view(bits.shape)
+
+    def layer(self):
+        return dev(self.qw), dev(self.qz), dev(self.sc).view(torch.float16)
+
+    def lora(self):
+        return self.td(self.Ab), self.td(self.Bb), dev(self.c), dev(self.ids)
+
+
+def f64(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+def worst(got, want, bound):
+    assert got.shape == want.shape and np.isfinite(got).all()
+    return float((np.abs(got - want) / bound).max())
+
+
+def check_forward(api, p, save=True):
+    X = p.td(p.Xb)
+    h = x8 = None
+    if save:
+        h = torch.full((p.T, p.r), 7.0, device="cuda:0")
+        x8 = (torch.full((p.T, p.K), 9, dtype=torch.int8, device="cuda:0"),
+              torch.full((p.T, p.K // 128), 9.0, device="cuda:0"))
+    Y = api.w4a16_lora_matmul(X, *p.layer(), *p.lora(), group=p.group, h=h, x8=x8)
+    torch.cuda.synchronize()
+    y, hr, mh, ml, mw = R.forward(p.x, p.w, p.A, p.B, p.c.astype(np.float64), p.ids)
+    u, tiny = R.UOUT[p.dtype], R.TINY[p.dtype]
+    if p.T <= 16:
+        base = R.gamma(p.K + 4) * R.decode_magnitude(p.x, p.qw, p.qz, p.sc, p.N, p.group)
+    else:
+        base = (u + R.gamma(p.K)) * mw
+    bound = base + (R.LOW[p.dtype] + R.gamma(p.K + p.r + 4)) * ml + u * np.abs(y) + tiny
+    e = worst(f64(Y), y, bound)
+    print(f"lora T={p.T} N={p.N} K={p.K} r={p.r} L={p.L} {p.dtype}: Y {e:.3f} of the bound",
+          flush=True)
+    assert e <= 1.0
+    if save:
+        assert worst(f64(h), hr, R.gamma(p.K) * mh + 2.0 ** -126) <= 1.0
+        codes, steps = R.pack8(_dec(p.Xb, p.dtype).astype(np.float32).reshape(p.T, p.K))
+        assert np.array_equal(x8[0].cpu().numpy(), codes)
+        assert np.array_equal(x8[1].cpu().numpy().view(np.uint32), steps.view(np.uint32))
+
+
+# T: single tokens, one full and one ragged row tile, several; N = 264 is no
+# multiple of 16, 1048 of 32; K = 128 is the least, 1152 leaves waves idle.
+@pytest.mark.parametrize("T,N,K,r,L,dtype,group,kind", [
+    (1, 264, 384, 8, 1, "bf16", 128, "one"),
+    (1, 272, 1152, 16, 3, "f16", 128, "one"),
+    (1, 4096, 4096, 16, 4, "bf16", 128, "one"),
+    (2, 512, 128, 128, 2, "bf16", 32, "tokens"),
+    (7, 1048, 1152, 24, 9, "f16", 64, "tokens"),
+    (16, 272, 512, 64, 40, "bf16", 128, "tokens"),
+    (16, 264, 384, 40, 5, "f16", 32, "tokens"),
+    (16, 512, 2048, 16, 5, "bf16", 128, "none"),
+    (17, 264, 384, 8, 2, "f16", 128, "tokens"),
+    (33, 1048, 1152, 16, 33, "bf16", 64, "tokens"),
+    (64, 512, 512, 32, 48, "bf16", 128, "tokens"),
+    (64, 1040, 2176, 128, 4, "f16", 32, "runs"),
+    (65, 512, 128, 56, 3, "bf16", 128, "one"),
+    (130, 520, 640, 72, 70, "f16", 64, "tokens"),
+    (200, 1048, 1152, 8, 6, "bf16", 128, "runs"),
+    (256, 1048, 384, 104, 7, "f16", 128, "tokens"),
+    (257, 264, 384, 16, 3, "bf16", 32, "runs"),
+    (300, 1032, 1152, 64, 1, "f16", 128, "one"),
+    (300, 512, 512, 128, 300, "bf16", 128, "tokens"),
+    (777, 520, 640, 40, 5, "bf16", 64, "runs"),
+    (1030, 1048, 1152, 88, 4, "f16", 128, "runs"),
+    (1100, 512, 512, 32, 9, "bf16", 128, "none"),
+])
+def test_forward(api, T, N, K, r, L, dtype, group, kind):
+    check_forward(api, Problem(T, N, K, r, L, dtype, group, kind, seed=T + N))
+
+
+def backward_args(p, x8):
+    if x8:
+        codes, steps = R.pack8(_dec(p.Xb, p.dtype).astype(np.float32).reshape(p.T, p.K))
+        x = codes.astype(np.float64) * np.repeat(steps.astype(np.float64), 128, axis=1)
+        return (dev(codes), dev(steps)), x
+    return p.td(p.Xb), p.x
+
+
+def check_backward(api, p, x8=False, want_dx=True):
+    rng = np.random.default_rng(p.T)
+    h32 = rng.standard_normal((p.T, p.r)).astype(np.float32)
+    X, x = backward_args(p, x8)
+    dX, dA, dB = api.w4a16_lora_backward(p.td(p.dYb), X, dev(h32), *p.layer(), *p.lora(),
+                                         group=p.group, want_dx=want_dx)
+    torch.cuda.synchronize()
+    dx, da, db, mw, mgx, mA, mB = R.backward(p.dy, x, h32.astype(np.float64), p.w, p.A, p.B,
+                                             p.c.astype(np.float64), p.ids)
+    u, tiny, low = R.UOUT[p.dtype], R.TINY[p.dtype], R.LOW[p.dtype]
+    e = [0.0]
+    if want_dx:
+        e[0] = worst(f64(dX), dx, (u + R.gamma(p.N)) * mw +
+                     (low + R.gamma(p.N + p.r + 4)) * mgx + u * np.abs(dx) + tiny)
+    else:
+        assert dX is None
+    e.append(worst(f64(dA), da, (low + R.gamma(p.N + p.T + 4)) * mA + u * np.abs(da) + tiny))
+    e.append(worst(f64(dB), db, (low + R.gamma(p.T + 4)) * mB + u * np.abs(db) + tiny))
+    print(f"lora backward T={p.T} N={p.N} K={p.K} r={p.r} L={p.L} {p.dtype} x8={x8}: dX, dA, dB "
+          f"{e[0]:.3f} {e[1]:.3f} {e[2]:.3f} of the bounds", flush=True)
+    assert max(e) <= 1.0
+    for a in range(p.L):                    # adapters without tokens: zeros
+        if not (p.ids == a).any():
+            assert not f64(dA[a]).any() and not f64(dB[a]).any()
+
+
+@pytest.mark.parametrize("T,N,K,r,L,dtype,group,kind,x8", [
+    (1, 264, 384, 8, 2, "bf16", 128, "one", False),
+    (1, 512, 128, 16, 1, "f16", 32, "one", True),
+    (3, 272, 512, 24, 3, "f16", 128, "tokens", True),
+    (16, 1048, 1152, 128, 2, "bf16", 64, "tokens", False),
+    (40, 512, 512, 16, 5, "bf16", 128, "none", True),
+    (96, 512, 512, 8, 2, "f16", 128, "runs", False),
+    (130, 520, 640, 40, 70, "bf16", 128, "tokens", True),
+    (255, 264, 384, 72, 3, "f16", 64, "runs", False),
+    (300, 1048, 1152, 32, 4, "bf16", 32, "runs", True),
+    (513, 1032, 640, 64, 1, "f16", 128, "one", True),
+    (777, 520, 1152, 56, 5, "bf16", 128, "runs", False),
+    (1100, 512, 512, 104, 3, "f16", 128, "tokens", True),
+])
+def test_backward(api, T, N, K, r, L, dtype, group, kind, x8):
+    check_backward(api, Problem(T, N, K, r, L, dtype, group, kind, seed=T + N), x8)
+
+
+def test_backward_without_dx(api):
+    p = Problem(300, 264, 384, 16, 3, "bf16", seed=5)
+    check_backward(api, p, want_dx=False)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_gradients_against_differences(api, dtype):
+    """L = Σ dY·Y is linear in A (B fixed), in B and in x: central differences
+    of the float64 forward pass with steps D are exact, and must equal the
+    kernels' gradient times D within the gradient's own rounding."""
+    p = Problem(150, 272, 384, 16, 3, dtype, seed=11)
+    c = p.c.astype(np.float64)
+    _, h, _, _, _ = R.forward(p.x, p.w, p.A, p.B, c, p.ids)
+    h32 = h.astype(np.float32)
+    dX, dA, dB = api.w4a16_lora_backward(p.td(p.dYb), p.td(p.Xb), dev(h32), *p.layer(), *p.lora())
+    torch.cuda.synchronize()
+    rng = np.random.default_rng(12)
+    loss = lambda x, A, B: float((p.dy * R.forward(x, p.w, A, B, c, p.ids)[0]).sum())
+    dx, da, db, mw, mgx, mA, mB = R.backward(p.dy, p.x, h, p.w, p.A, p.B, c, p.ids)
+    u, low, tiny = R.UOUT[dtype], R.LOW[dtype], R.TINY[dtype]
+    bounds = {"x": (u + R.gamma(p.N)) * mw + (low + R.gamma(p.N + p.r + 4)) * mgx + u * np.abs(dx),
+              "A": (low + R.gamma(p.N + p.T + 4)) * mA + u * np.abs(da),
+              "B": (low + R.gamma(p.T + 4) + R.U32) * mB + u * np.abs(db)}
+    for name, grad, v in (("x", dX, p.x), ("A", dA, p.A), ("B", dB, p.B)):
+        D = rng.standard_normal(v.shape)
+        up = {"x": p.x, "A": p.A, "B": p.B, name: v + D}
+        dn = {"x": p.x, "A": p.A, "B": p.B, name: v - D}
+        diff = (loss(**up) - loss(**dn)) / 2
+        got = float((f64(grad) * D).sum())
+        allow = float(((bounds[name] + tiny) * np.abs(D)).sum()) + 1e-9 * abs(diff)
+        assert abs(got - diff) <= allow, (name, got, diff, allow)
+
+
+def test_a_broken_adapter_reaches_its_own_tokens_only(api):
+    """NaN and infinities in one adapter, one token's activations or one
+    token's gradient leave everybody else's results as they were, bit for bit."""
+    for T, dtype in ((12, "bf16"), (50, "f16"), (200, "bf16"), (700, "f16")):
+        p = Problem(T, 520, 640, 16, 4, dtype, kind="tokens", seed=T)
+        p.ids[:4] = [0, 1, 2, 3]
+        A, B, c, ids = p.lora()
+        X, dY, h = p.td(p.Xb), p.td(p.dYb), dev(np.ones((T, 16), np.float32))
+        lay = p.layer()
+        run = lambda: (api.w4a16_lora_matmul(X, *lay, A, B, c, ids, h=h),
+                       *api.w4a16_lora_backward(dY, X, h, *lay, A, B, c, ids))
+        y0, dx0, da0, db0 = [t.clone() for t in run()]
+        A[1, 3, 5], A[1, 0, 0], B[1, 7, 2], B[1, 100, 0] = (float("nan"), float("inf"),
+                                                             float("nan"), float("-inf"))
+        y, dx, da, db = run()
+        torch.cuda.synchronize()
+        other = torch.from_numpy(p.ids != 1).to("cuda:0")
+        for got, want in ((y, y0), (dx, dx0)):
+            assert torch.equal(got[other].view(torch.int16), want[other].view(torch.int16))
+            assert not torch.isfinite(got[~other]).all()
+        for a in (0, 2, 3):
+            assert torch.equal(da[a], da0[a]) and torch.equal(db[a], db0[a])
+        # a token's own NaN: its row, and its adapter's gradient
+        A, B, c, ids = p.lora()
+        X[2, 9] = float("nan")
+        dY[2, 8] = float("inf")
+        y, dx, da, db = run()
+        torch.cuda.synchronize()
+        keep = torch.arange(T, device="cuda:0") != 2
+        assert torch.equal(y[keep].view(torch.int16), y0[keep].view(torch.int16))
+        assert torch.equal(dx[keep].view(torch.int16), dx0[keep].view(torch.int16))
+        assert torch.isnan(y[2]).all()
+        for a in (0, 1, 3):
+            assert torch.equal(da[a], da0[a]) and torch.equal(db[a], db0[a])
+
+
+def test_values_past_fp16_in_the_low_rank_product(api):
+    """H = A·x leaves fp16's range (above 65504, or far below its least
+    subnormal) while Y does not; the same for G and dX."""
+    for scale in (2.0 ** 14, 2.0 ** -12):
+        for T in (5, 40, 300):
+            p = Problem(T, 272, 384, 16, 3, "f16", kind="tokens", seed=3 * T)
+            p.Ab = _enc((p.A * scale).astype(np.float32), "f16")
+            p.Bb = _enc((p.B / scale).astype(np.float32), "f16")
+            p.A = _dec(p.Ab, "f16").astype(np.float64).reshape(p.A.shape)
+            p.B = _dec(p.Bb, "f16").astype(np.float64).reshape(p.B.shape)
+            check_forward(api, p)
+            check_backward(api, p)
+
+
+def test_results_repeat_and_stay_in_their_rows(api):
+    """Equal calls give equal bits; rows behind the outputs stay untouched."""
+    for T in (3, 60, 500):
+        p = Problem(T, 520, 384, 24, 6, "bf16", kind="tokens", seed=T)
+        X, dY = p.td(p.Xb), p.td(p.dYb)
+        lay, lora = p.layer(), p.lora()
+        full = lambda rows, cols, dt: torch.full((rows, cols), 3.0, device="cuda:0").to(dt)
+        Yb, dXb = full(T + 8, p.N, X.dtype), full(T + 8, p.K, X.dtype)
+        hb = full(T + 8, p.r, torch.float32)
+        cb, sb = full(T + 8, p.K, torch.int8), full(T + 8, p.K // 128, torch.float32)
+        dAb, dBb = full(6 * 24 + 8, p.K, X.dtype), full(6 * p.N + 8, 24, X.dtype)
+        first = None
+        for _ in range(3):
+            api.w4a16_lora_matmul(X, *lay, *lora, out=Yb[:T], h=hb[:T], x8=(cb[:T], sb[:T]))
+            api.w4a16_lora_backward(dY, (cb[:T], sb[:T]), hb[:T], *lay, *lora,
+                                    out=(dXb[:T], dAb[:144].view(6, 24, p.K),
+                                         dBb[:6 * p.N].view(6, p.N, 24)))
+            torch.cuda.synchronize()
+            now = [t.clone() for t in (Yb, dXb, hb, cb, sb, dAb, dBb)]
+            for t in now[:5]:
+                assert (t[T:] == 3).all()
+            assert (now[5][144:] == 3).all() and (now[6][6 * p.N:] == 3).all()
+            if first is None:
+                first = now
+            for a, b in zip(first, now):
+                assert torch.equal(a, b)
+
+
+def test_other_stream_and_two_at_once(api):
+    """Two calls on two streams with their own workspaces, and a captured graph
+    replayed between eager calls, all give the plain call's bits."""
+    ps = [Problem(T, 520, 640, 16, 3, "bf16", kind="tokens", seed=T) for T in (9, 70, 600)]
+    jobs = []
+    for p in ps:
+        X, dY, h = p.td(p.Xb), p.td(p.dYb), torch.empty(p.T, p.r, device="cuda:0")
+        lay, lora = p.layer(), p.lora()
+
+        def run(X=X, dY=dY, h=h, lay=lay, lora=lora, ws=None, wb=None):
+            Y = api.w4a16_lora_matmul(X, *lay, *lora, h=h, ws=ws)
+            return (Y, *api.w4a16_lora_backward(dY, X, h, *lay, *lora, ws=wb))
+        jobs.append((p, run))
+    want = [[t.clone() for t in run()] for _, run in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    got = []
+    for (_, run), s in zip(jobs, streams):
+        with torch.cuda.stream(s):
+            got.append(run())
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(a, b) for a, b in zip(w, g))
+    for (p, run), w in zip(jobs, want):
+        need = (api.w4a16_lora_workspace_bytes(p.T, p.N, p.K, p.L, p.r, torch.bfloat16),
+                api.w4a16_lora_backward_workspace_bytes(p.T, p.N, p.K, p.L, p.r, torch.bfloat16))
+        ws, wb = (torch.empty(n, dtype=torch.uint8, device="cuda:0") for n in need)
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            run(ws=ws, wb=wb)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = run(ws=ws, wb=wb)
+        for _ in range(3):
+            for t in out:
+                t.zero_()
+            ws.fill_(255)
+            wb.fill_(255)
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(w, out))
+            eager = run()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(w, eager))
+
+
+def test_search_pack_then_train_adapters(api):
+    """A layer searched and packed here, two adapters trained over it for a few
+    steps from 8-bit checkpoints: every step's gradients against float64 from
+    the same adapters, and an adapter that no token uses stays as it is."""
+    from post_weight_quantization_26_amd import synth
+    T, N, K, r, L = 320, 256, 384, 16, 3
+    Xb, Wb = synth.make_custom(T, N, K, "bf16", seed=21)
+    X, W = to_dev(Xb, "bf16"), to_dev(Wb, "bf16")
+    abar = api.act_stats(X)
+    res = api.search_scale(X, W, abar, synth.alpha_grid(5))
+    qw, qz, sc = api.quantize_pack(W, res["s_best"])
+    Xf = (X.float() / res["s_best"]).to(torch.bfloat16)
+    p = Problem(T, N, K, r, L, "bf16", seed=22,
+                layer=(qw.cpu().numpy(), qz.cpu().numpy(), sc.cpu().numpy().view(np.uint16)))
+    p.Xb = Xf.view(torch.int16).cpu().numpy().view(np.uint16)
+    p.x = _dec(p.Xb, "bf16").astype(np.float64)
+    p.ids = np.where(np.arange(T) < 200, 0, 2).astype(np.int32)
+    A, B, c, ids = p.lora()
+    B.zero_()
+    target = torch.randn(T, N, device="cuda:0") * 0.1
+    h = torch.empty(T, r, device="cuda:0")
+    x8 = api.act_pack8(Xf)
+    A1 = A[1].clone()
+    for step in range(3):
+        Y = api.w4a16_lora_matmul(Xf, qw, qz, sc, A, B, c, ids, h=h, x8=x8)
+        dY = ((Y.float() - target) / T).to(torch.bfloat16)
+        dX, dA, dB = api.w4a16_lora_backward(dY, x8, h, qw, qz, sc, A, B, c, ids)
+        x = f64(x8[0]) * np.repeat(f64(x8[1]), 128, axis=1)
+        dx, da, db, mw, mgx, mA, mB = R.backward(f64(dY), x, f64(h), p.w, f64(A), f64(B),
+                                                 p.c.astype(np.float64), p.ids)
+        u, low, tiny = R.UOUT["bf16"], R.LOW["bf16"], R.TINY["bf16"]
+        assert worst(f64(dX), dx, (u + R.gamma(N)) * mw + (low + R.gamma(N + r + 4)) * mgx +
+                     u * np.abs(dx) + tiny) <= 1
+        assert worst(f64(dA), da, (low + R.gamma(N + T + 4)) * mA + u * np.abs(da) + tiny) <= 1
+        assert worst(f64(dB), db, (low + R.gamma(T + 4)) * mB + u * np.abs(db) + tiny) <= 1
+        A -= (0.5 * dA.float()).to(A.dtype)
+        B -= (0.5 * dB.float()).to(B.dtype)
+    assert torch.equal(A[1], A1) and not B[1].any() and B[0].any() and B[2].any()
+
+
+# ------------------------------------------------------------- checkpoints
+
+def special_rows(T, K, rng):
+    """Blocks at the edges: zeros, the least numbers, ties, NaN, infinities."""
+    x = (rng.standard_normal((T, K)) * np.exp(3 * rng.standard_normal((T, 1)))).astype(np.float32)
+    kinds = [0.0, 2.0 ** -120, 2.0 ** -133, np.nan, np.inf, -np.inf, 3.0e38, 6.0e4]
+    for t in range(T):
+        b = rng.integers(0, K // 128) * 128
+        kind = kinds[t % len(kinds)]
+        if kind == 0.0 or abs(kind) in (2.0 ** -120, 2.0 ** -133):
+            x[t, b:b + 128] = kind
+        else:
+            x[t, b + rng.integers(0, 128)] = kind
+        if t % 5 == 0:                      # x·(127/127) falls on .5
+            x[t, :128] = rng.integers(-126, 126, 128) + np.float32(0.5)
+            x[t, 0] = 127
+    return x
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T,K", [(1, 128), (3, 384), (129, 1152), (40, 4096), (1025, 256)])
+def test_checkpoint(api, dtype, T, K):
+    rng = np.random.default_rng(T + K)
+    with np.errstate(over="ignore"):
+        x32 = special_rows(T, K, rng)
+        if dtype == "f32":
+            X, xv = dev(x32), x32
+        else:
+            bits = torch.from_numpy(x32).to(TD[dtype])
+            X, xv = bits.to("cuda:0"), bits.float().numpy()
+    codes, steps = api.act_pack8(X)
+    back = api.act_unpack8(codes, steps, X.dtype)
+    torch.cuda.synchronize()
+    rc, rs = R.pack8(xv)
+    assert np.array_equal(codes.cpu().numpy(), rc)
+    gs = steps.cpu().numpy()
+    assert np.array_equal(np.isnan(gs), np.isnan(rs))
+    assert np.array_equal(gs[~np.isnan(rs)], rs[~np.isnan(rs)])
+    want = torch.from_numpy(R.unpack8(rc, rs)).to(X.dtype)
+    got = back.cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    ok = ~torch.isnan(want)
+    assert torch.equal(got[ok], want[ok])
