@@ -763,13 +763,16 @@ extern "C" awq_status awq_w4a16_lora_matmul(
   p.w = {qweight, qzeros, scales, N, K, group_size};
   p.s = {static_cast<const uint16_t*>(A), static_cast<const uint16_t*>(B), scaling, ids, L, r};
   p.Y = static_cast<uint16_t*>(Y);
-  p.H = H ? H : at<float>(ws, l.h);
+  p.H = H;
+  p.codes = x8_codes;
+  p.steps = x8_steps;
   p.f16 = dtype == AWQ_F16;
+  p.Q = at<uint16_t>(ws, l.q);
+  p.E = at<float>(ws, l.e);
+  p.Wd = at<uint16_t>(ws, l.wd);
+  p.P = at<float>(ws, l.h);
+  p.RW = lora_q_width(r);
   AWQ_HIP(timed(AWQ_K_LORA, st, [&] { return launch_lora_forward(p, st); }), "lora_matmul");
-  if (x8_codes)
-    AWQ_HIP(timed(AWQ_K_ACT8, st,
-                  [&] { return launch_act_pack8(X, dt(dtype), T, K, x8_codes, x8_steps, st); }),
-            "lora_matmul checkpoint");
   return AWQ_OK;
 }
 

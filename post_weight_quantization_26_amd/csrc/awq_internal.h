@@ -206,8 +206,14 @@ awq_status check_w4a16(const void* X, awq_dtype d, int64_t T, int64_t N, int64_t
 // Low-rank adapters: byte offsets of the regions of a call's workspace.
 constexpr int kLoraMaxRank = 128;
 constexpr int kLoraMaxAdapters = 4096;
+// Columns of a token's wide-product operand: c·P as two 16-bit halves, padded
+// with zeros to whole 32-wide MFMA steps.
+inline int lora_q_width(int32_t r) { return int((2 * r + 31) / 32 * 32); }
 struct LoraLayout {
-  size_t h;       // [T, r] f32: H (forward) or G (backward)
+  size_t h;       // [T, r] f32 G (backward)
+  size_t q;       // [T, lora_q_width(r)] 16-bit
+  size_t e;       // [T] f32
+  size_t wd;      // [N, K] 16-bit dequantised layer
   size_t total;
 };
 LoraLayout lora_layout(int64_t T, int64_t N, int64_t K, int32_t L, int32_t r);

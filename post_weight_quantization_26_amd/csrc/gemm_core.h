@@ -24,22 +24,10 @@
 #pragma once
 
 #include "device_common.h"
+#include "gemm_types.h"
 
 namespace awq {
 namespace {
-
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
-
-// MFMA operand vector of 8 elements: bf16 or fp16 (F16 = true).
-template <bool F16>
-struct Operand {
-  typedef bf16x8_t type;
-};
-template <>
-struct Operand<true> {
-  typedef f16x8_t type;
-};
 
 #define AWQ_LDS(p) ((__attribute__((address_space(3))) void*)(p))
 
@@ -196,7 +184,6 @@ __device__ __forceinline__ void dma64(const GemmCtx64& c, int kt) {
 // MFMA of each accumulator takes the constant 0 as its addend (no zeroing
 // moves), and the loop ends with an explicit wait tied to every
 // accumulator before anything reads them.
-typedef float floatx4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ void mfma16(floatx4& c, const bf16x8_t& a, const bf16x8_t& b) {
   asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
 }
@@ -263,7 +250,8 @@ __device__ __forceinline__ void dma64_a(const GemmCtx64& c, int kt) {
 // k-step 0's MFMAs (f0) carry k-step 1's reads, one per four MFMAs.
 // NEXT: the copies fetch k-tile 0 of another tile (context cn) instead of
 // k-tile kt + 1 of this one.
-template <int S, bool PREV, bool NEXT = false, class V>
+// INIT: without PREV, the accumulators hold a starting value.
+template <int S, bool PREV, bool NEXT = false, bool INIT = false, class V>
 __device__ __forceinline__ void region16(const GemmCtx64& c, const int (&rdA)[2], const int (&rdB)[2],
                                          int kt, floatx4 (&acc)[8][8], V (&f0a)[8], V (&f0b)[8],
                                          V (&f1a)[8], V (&f1b)[8], const GemmCtx64* cn = nullptr) {
@@ -290,11 +278,11 @@ __device__ __forceinline__ void region16(const GemmCtx64& c, const int (&rdA)[2]
 #pragma unroll
   for (int q = 0; q < 16; ++q) {
     const int i = q >> 1, j0 = (q & 1) * 4;
-    mfma16_acc<!PREV>(acc[i][j0], f0a[i], f0b[j0]);
+    mfma16_acc<!PREV && !INIT>(acc[i][j0], f0a[i], f0b[j0]);
     frag16<S>(rdA[1], rdB[1], q, f1a, f1b);
-    mfma16_acc<!PREV>(acc[i][j0 + 1], f0a[i], f0b[j0 + 1]);
-    mfma16_acc<!PREV>(acc[i][j0 + 2], f0a[i], f0b[j0 + 2]);
-    mfma16_acc<!PREV>(acc[i][j0 + 3], f0a[i], f0b[j0 + 3]);
+    mfma16_acc<!PREV && !INIT>(acc[i][j0 + 1], f0a[i], f0b[j0 + 1]);
+    mfma16_acc<!PREV && !INIT>(acc[i][j0 + 2], f0a[i], f0b[j0 + 2]);
+    mfma16_acc<!PREV && !INIT>(acc[i][j0 + 3], f0a[i], f0b[j0 + 3]);
   }
   __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
   __builtin_amdgcn_s_waitcnt(wait_vm(0));
@@ -308,17 +296,19 @@ __device__ __forceinline__ void mfma_8x8(floatx4 (&acc)[8][8], const V (&fa)[8],
     for (int j = 0; j < 8; ++j) mfma16(acc[i][j], fa[i], fb[j]);
 }
 // Writes every accumulator (no zeroing needed by the caller) and ends with
-// them safe to read (the last MFMAs have drained).
-template <bool F16>
+// them safe to read (the last MFMAs have drained). INIT: adds to what they
+// hold instead; k-tile 0's copies (dma64<0>(c, 0)) are the caller's then, so
+// that they can be in flight while it makes that starting value.
+template <bool F16, bool INIT = false>
 __device__ __forceinline__ void gemm_mainloop16(const GemmCtx64& c, floatx4 (&acc)[8][8]) {
   typedef typename Operand<F16>::type V;
   int rdA[2], rdB[2];
   frag_offsets16(c, rdA, rdB);
-  dma64<0>(c, 0);
+  if constexpr (!INIT) dma64<0>(c, 0);
   __builtin_amdgcn_s_waitcnt(wait_vm(0));
   region_barrier();
   V f0a[8], f0b[8], f1a[8], f1b[8];
-  region16<0, false>(c, rdA, rdB, 0, acc, f0a, f0b, f1a, f1b);
+  region16<0, false, false, INIT>(c, rdA, rdB, 0, acc, f0a, f0b, f1a, f1b);
   int kt = 1;
   for (; kt + 1 < c.KT; kt += 2) {
     region16<1, true>(c, rdA, rdB, kt, acc, f0a, f0b, f1a, f1b);

@@ -1,9 +1,11 @@
-// Arguments of the low-rank adapter kernels (lora.hip), shared with abi.cpp.
+// Arguments of the low-rank adapter kernels (lora*.hip), shared with abi.cpp.
 #pragma once
 
 #include "device_common.h"
 
 namespace awq {
+
+constexpr int kLoraRankMax = 128;
 
 // The packed 4-bit layer (quantize_pack's layout).
 struct LoraLayer {
@@ -23,14 +25,60 @@ struct LoraSet {
   int L, r;
 };
 
+// The narrow product P[t][j] = Σ_c V[t][c]·M_a[j][c] (lora_down.hip).
+struct LoraDown {
+  const uint16_t* V;      // [T, ldv]
+  const uint16_t* M;      // [L, r, ldm]
+  const float* scaling;
+  const int32_t* ids;
+  int64_t T, C, ldv, ldm; // C a multiple of 128
+  int L, r, f16;
+  float* H;               // [T, r] or NULL; rows without an adapter get zeros
+  float* Pt;              // [r, ldp] transposed, token t at column pos[t], or NULL
+  float* row_max;         // [ldp] max_j |P| at pos[t] (with Pt)
+  const int32_t* pos;
+  int64_t ldp;
+  uint16_t* Q;            // [T, RW]: c·P as halves hi [r], lo [r], zeros up to RW
+  int RW;                 // 2r rounded up to 32
+  float* E;               // [T] the power of two that Q is scaled down by
+  int8_t* codes;          // [T, C] 8-bit checkpoint of V, or NULL
+  float* steps;           // [T, C / 128]
+};
+hipError_t launch_lora_down(const LoraDown& p, hipStream_t st);
+
+// The wide product's operands for a fused epilogue (lora_gemm.hip).
+struct LoraUp {
+  const uint16_t* Q;      // [T, RW]
+  const float* E;         // [T]
+  const int32_t* ids;     // [T]
+  const uint16_t* U;      // [L, N, r]
+  int L, r, RW;
+};
+hipError_t launch_lora_gemm(const uint16_t* V, int64_t ldv, const uint16_t* Wd, int64_t ldw,
+                            int64_t M, int64_t N, int64_t C, const LoraUp& u, int f16,
+                            uint16_t* O, hipStream_t st);
+
+// The dequantisation pass of the W4A16 GEMM (w4a16.hip): Ŵ [N, K], rounded.
+hipError_t launch_w4a16_dequant(const int32_t* qweight, const int32_t* qzeros,
+                                const uint16_t* scales, int64_t N, int64_t K, int group, int f16,
+                                uint16_t* Wd, hipStream_t st);
+
 struct LoraForward {
   const uint16_t* X;      // [T, K]
   int64_t T;
   LoraLayer w;
   LoraSet s;
   uint16_t* Y;            // [T, N]
-  float* H;               // [T, r]
+  float* H;               // [T, r] or NULL
+  int8_t* codes;          // [T, K] or NULL
+  float* steps;           // [T, K / 128]
   int f16;
+  // workspace
+  uint16_t* Q;            // [T, RW]
+  float* E;               // [T]
+  uint16_t* Wd;           // [N, K]
+  float* P;               // [T, r] (T <= 16)
+  int RW;
 };
 
 struct LoraBackward {

@@ -158,15 +158,6 @@ __global__ __launch_bounds__(256) void lora_grad_b_kernel(const uint16_t* __rest
 }
 
 template <bool F16>
-hipError_t forward(const LoraForward& p, hipStream_t st) {
-  lora_down_kernel<F16, true, false>
-      <<<unsigned(p.T), 256, 0, st>>>(p.X, p.w.K, p.s, p.s.A, p.H);
-  const dim3 grid(unsigned((p.w.N + 63) / 64), unsigned((p.T + 63) / 64));
-  lora_product_kernel<F16, false><<<grid, 256, 0, st>>>(p.X, p.T, p.w, p.s, p.H, p.Y);
-  return hipGetLastError();
-}
-
-template <bool F16>
 hipError_t backward(const LoraBackward& p, hipStream_t st) {
   lora_down_kernel<F16, false, true>
       <<<unsigned(p.T), 256, 0, st>>>(p.dY, p.w.N, p.s, p.s.B, p.G);
@@ -188,8 +179,42 @@ hipError_t backward(const LoraBackward& p, hipStream_t st) {
 
 }  // namespace
 
+template <bool F16>
+hipError_t forward_few(const LoraForward& p, hipStream_t st) {
+  float* H = p.H ? p.H : p.P;
+  lora_down_kernel<F16, true, false>
+      <<<unsigned(p.T), 256, 0, st>>>(p.X, p.w.K, p.s, p.s.A, H);
+  const dim3 grid(unsigned((p.w.N + 63) / 64), unsigned((p.T + 63) / 64));
+  lora_product_kernel<F16, false><<<grid, 256, 0, st>>>(p.X, p.T, p.w, p.s, H, p.Y);
+  if (!p.codes) return hipGetLastError();
+  return launch_act_pack8(p.X, F16 ? 2 : 1, p.T, p.w.K, p.codes, p.steps, st);
+}
+
 hipError_t launch_lora_forward(const LoraForward& p, hipStream_t st) {
-  return p.f16 ? forward<true>(p, st) : forward<false>(p, st);
+  if (p.T <= 16) return p.f16 ? forward_few<true>(p, st) : forward_few<false>(p, st);
+  LoraDown d{};
+  d.V = p.X;
+  d.M = p.s.A;
+  d.scaling = p.s.scaling;
+  d.ids = p.s.ids;
+  d.T = p.T;
+  d.C = d.ldv = d.ldm = p.w.K;
+  d.L = p.s.L;
+  d.r = p.s.r;
+  d.f16 = p.f16;
+  d.H = p.H;
+  d.Q = p.Q;
+  d.RW = p.RW;
+  d.E = p.E;
+  d.codes = p.codes;
+  d.steps = p.steps;
+  hipError_t e = launch_lora_down(d, st);
+  if (e != hipSuccess) return e;
+  e = launch_w4a16_dequant(p.w.qweight, p.w.qzeros, p.w.scales, p.w.N, p.w.K, p.w.group, p.f16,
+                           p.Wd, st);
+  if (e != hipSuccess) return e;
+  const LoraUp u{p.Q, p.E, p.s.ids, p.s.B, p.s.L, p.s.r, p.RW};
+  return launch_lora_gemm(p.X, p.w.K, p.Wd, p.w.K, p.T, p.w.N, p.w.K, u, p.f16, p.Y, st);
 }
 
 hipError_t launch_lora_backward(const LoraBackward& p, hipStream_t st) {

@@ -1,0 +1,49 @@
+// Device helpers of the low-rank adapter kernels.
+#pragma once
+
+#include "device_common.h"
+
+namespace awq {
+namespace {
+
+template <bool F16>
+__device__ __forceinline__ uint16_t round16(float f) {
+  if constexpr (F16) return __builtin_bit_cast(uint16_t, static_cast<_Float16>(f));
+  else return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f));
+}
+
+template <bool F16>
+__device__ __forceinline__ float widen16(uint16_t h) {
+  if constexpr (F16) return f16_to_f32(h);
+  else return bf16_to_f32(h);
+}
+
+// The least id of this wave's lanes that is above `prev` and below L, or L
+// when there is none (ids < 0 never count: prev starts at -1). The same value
+// in every lane; `id2` is a second id of the lane (or -1).
+__device__ __forceinline__ int next_adapter(int id, int id2, int prev, int L) {
+  int m = id > prev && id < L ? id : L;
+  const int m2 = id2 > prev && id2 < L ? id2 : L;
+  m = m < m2 ? m : m2;
+#pragma unroll
+  for (int o = 32; o; o >>= 1) {
+    const int u = __shfl_xor(m, o);
+    m = m < u ? m : u;
+  }
+  return __builtin_amdgcn_readfirstlane(m);
+}
+
+// 2^e of a float32 magnitude's exponent, clamped to [-60, 60] (0 and values
+// that are not finite: 0).
+__device__ __forceinline__ int exponent_of(float m) {
+  if (!(m > 0.f) || !(m < __builtin_inff())) return 0;
+  const int e = int((__float_as_uint(m) >> 23) & 0xFFu) - 127;
+  return e < -60 ? -60 : e > 60 ? 60 : e;
+}
+
+__device__ __forceinline__ float exp2i(int e) {   // 2^e, -126 <= e <= 127
+  return __uint_as_float(uint32_t(e + 127) << 23);
+}
+
+}  // namespace
+}  // namespace awq

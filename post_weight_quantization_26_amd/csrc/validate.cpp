@@ -492,10 +492,19 @@ bool lora_sizes_ok(int64_t T, int64_t N, int64_t K, int32_t L, int32_t r, awq_dt
          L <= kLoraMaxAdapters && r >= 8 && r <= kLoraMaxRank && r % 8 == 0;
 }
 
-LoraLayout lora_layout(int64_t T, int64_t, int64_t, int32_t, int32_t r) {
+LoraLayout lora_layout(int64_t T, int64_t N, int64_t K, int32_t, int32_t r) {
   LoraLayout l{};
-  l.h = 0;
-  l.total = align_up(size_t(T) * size_t(r) * 4);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += align_up(bytes);
+    return at;
+  };
+  if (T <= kW4A16GemvMaxT) l.h = take(size_t(T) * size_t(r) * 4);
+  l.q = take(size_t(T) * size_t(lora_q_width(r)) * 2);
+  l.e = take(size_t(T) * 4);
+  l.wd = take(size_t(N) * size_t(K) * 2);
+  l.total = off;
   return l;
 }
 
