@@ -787,21 +787,89 @@ extern "C" awq_status awq_w4a16_lora_backward(
                                        ws, ws_bytes);
   if (st_ != AWQ_OK) return st_;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const LoraLayout l = lora_backward_layout(T, N, K, L, r);
-  LoraBackward p{};
-  p.dY = static_cast<const uint16_t*>(dY);
-  p.X = X;
-  p.steps = x8_steps;
-  p.H = H;
-  p.T = T;
-  p.w = {qweight, qzeros, scales, N, K, group_size};
-  p.s = {static_cast<const uint16_t*>(A), static_cast<const uint16_t*>(B), scaling, ids, L, r};
-  p.G = at<float>(ws, l.h);
-  p.dX = static_cast<uint16_t*>(dX);
-  p.dA = static_cast<uint16_t*>(dA);
-  p.dB = static_cast<uint16_t*>(dB);
-  p.f16 = dtype == AWQ_F16;
-  AWQ_HIP(timed(AWQ_K_LORA, st, [&] { return launch_lora_backward(p, st); }), "lora_backward");
+  const LoraBackwardLayout l = lora_backward_layout(T, N, K, L, r);
+  const int f16 = dtype == AWQ_F16;
+  const bool padded = l.Np != N;
+
+  LoraPrep pr{};
+  pr.w = {qweight, qzeros, scales, N, K, group_size};
+  pr.s = {static_cast<const uint16_t*>(A), static_cast<const uint16_t*>(B), scaling, ids, L, r};
+  pr.T = T;
+  pr.Np = l.Np;
+  pr.piece = int(l.piece);
+  pr.f16 = f16;
+  pr.dY = static_cast<const uint16_t*>(dY);
+  pr.Wt = dX ? at<uint16_t>(ws, l.wt) : nullptr;
+  pr.Bt = at<uint16_t>(ws, l.bt);
+  pr.At = at<uint16_t>(ws, l.at);
+  pr.dYp = padded ? at<uint16_t>(ws, l.dyp) : nullptr;
+  pr.token = at<int>(ws, l.token);
+  pr.pos = at<int>(ws, l.pos);
+  pr.pieces = at<LoraPiece>(ws, l.table);
+  pr.n_pieces = at<int>(ws, l.n_pieces);
+  pr.slots = at<int>(ws, l.n_slots);
+  pr.first_slot = at<int>(ws, l.first_slot);
+  pr.last_pos = at<int>(ws, l.last_pos);
+
+  LoraDown d{};
+  d.V = padded ? pr.dYp : pr.dY;
+  d.M = pr.Bt;
+  d.scaling = scaling;
+  d.ids = ids;
+  d.T = T;
+  d.C = d.ldv = d.ldm = l.Np;
+  d.L = L;
+  d.r = r;
+  d.f16 = f16;
+  d.Pt = at<float>(ws, l.gt);
+  d.row_max = at<float>(ws, l.gmax);
+  d.pos = pr.pos;
+  d.ldp = l.Tp;
+  d.Q = at<uint16_t>(ws, l.q);
+  d.RW = lora_q_width(r);
+  d.E = at<float>(ws, l.e);
+  d.Hin = H;
+  d.Ht = at<float>(ws, l.ht);
+  d.h_max = at<float>(ws, l.hmax);
+
+  const LoraUp u{d.Q, d.E, ids, pr.At, L, r, d.RW};
+
+  LoraGrad g{};
+  g.dY = pr.dY;
+  g.X = X;
+  g.steps = x8_steps;
+  g.Gt = d.Pt;
+  g.Ht = d.Ht;
+  g.g_max = d.row_max;
+  g.h_max = d.h_max;
+  g.scaling = scaling;
+  g.token = pr.token;
+  g.pieces = pr.pieces;
+  g.n_pieces = pr.n_pieces;
+  g.slots = pr.slots;
+  g.first_slot = pr.first_slot;
+  g.N = N;
+  g.K = K;
+  g.Tp = l.Tp;
+  g.L = L;
+  g.r = r;
+  g.f16 = f16;
+  g.partial = at<float>(ws, l.partial);
+  g.dA = static_cast<uint16_t*>(dA);
+  g.dB = static_cast<uint16_t*>(dB);
+
+  AWQ_HIP(timed(AWQ_K_LORA, st,
+                [&] {
+                  hipError_t e = launch_lora_prep(pr, st);
+                  if (e == hipSuccess) e = launch_lora_down(d, st);
+                  if (e == hipSuccess && dX)
+                    e = launch_lora_gemm(d.V, l.Np, pr.Wt, l.Np, T, K, l.Np, u, f16,
+                                         static_cast<uint16_t*>(dX), st);
+                  if (e == hipSuccess)
+                    e = launch_lora_grad(g, int(l.pieces), T > l.piece, st);
+                  return e;
+                }),
+          "lora_backward");
   return AWQ_OK;
 }
 

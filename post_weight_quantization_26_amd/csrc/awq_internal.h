@@ -210,14 +210,26 @@ constexpr int kLoraMaxAdapters = 4096;
 // with zeros to whole 32-wide MFMA steps.
 inline int lora_q_width(int32_t r) { return int((2 * r + 31) / 32 * 32); }
 struct LoraLayout {
-  size_t h;       // [T, r] f32 G (backward)
+  size_t h;       // [T, r] f32 (T <= 16)
   size_t q;       // [T, lora_q_width(r)] 16-bit
   size_t e;       // [T] f32
   size_t wd;      // [N, K] 16-bit dequantised layer
   size_t total;
 };
 LoraLayout lora_layout(int64_t T, int64_t N, int64_t K, int32_t L, int32_t r);
-LoraLayout lora_backward_layout(int64_t T, int64_t N, int64_t K, int32_t L, int32_t r);
+// The gradient: runs of tokens cut into pieces of `piece` (a multiple of 32),
+// at most `pieces` of them; runs of more than one leave partial sums.
+struct LoraBackwardLayout {
+  int64_t Np, Tp;             // N padded to 128; sorted positions
+  int64_t piece, pieces, slots;
+  size_t wt, bt, at, dyp;     // 16-bit: Ŵᵀ [K, Np], Bᵀ [L, r, Np], Aᵀ [L, K, r], dY [T, Np]
+  size_t q, e;                // as in LoraLayout
+  size_t gt, ht, gmax, hmax;  // f32: [r, Tp] twice, [Tp] twice
+  size_t token, pos, table, n_pieces, n_slots, first_slot, last_pos;
+  size_t partial;             // f32 [slots, (K + N)·r]
+  size_t total;
+};
+LoraBackwardLayout lora_backward_layout(int64_t T, int64_t N, int64_t K, int32_t L, int32_t r);
 bool lora_sizes_ok(int64_t T, int64_t N, int64_t K, int32_t L, int32_t r, awq_dtype d);
 awq_status check_lora(const void* X, awq_dtype d, int64_t T, int64_t N, int64_t K,
                       const int32_t* qweight, const int32_t* qzeros, const uint16_t* scales,

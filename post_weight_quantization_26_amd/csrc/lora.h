@@ -43,6 +43,9 @@ struct LoraDown {
   float* E;               // [T] the power of two that Q is scaled down by
   int8_t* codes;          // [T, C] 8-bit checkpoint of V, or NULL
   float* steps;           // [T, C / 128]
+  const float* Hin;       // [T, r] to lay out as Pt into Ht and h_max, or NULL
+  float* Ht;
+  float* h_max;
 };
 hipError_t launch_lora_down(const LoraDown& p, hipStream_t st);
 
@@ -81,23 +84,61 @@ struct LoraForward {
   int RW;
 };
 
-struct LoraBackward {
+// A piece of one adapter's run of sorted tokens: positions pos .. pos + n - 1;
+// slot of its partial sums, or -1 where it is the whole run.
+struct LoraPiece {
+  int a, pos, n, slot;
+};
+
+// The gradient's preparation (lora_prep.hip).
+struct LoraPrep {
+  LoraLayer w;
+  LoraSet s;
+  int64_t T, Np;          // Np: N rounded up to 128
+  int piece, f16;
+  const uint16_t* dY;
+  uint16_t* Wt;           // [K, Np], or NULL (no dX: then no At either)
+  uint16_t* Bt;           // [L, r, Np]
+  uint16_t* At;           // [L, K, r]
+  uint16_t* dYp;          // [T, Np], or NULL where N = Np
+  int* token;             // [Tp] token at each position
+  int* pos;               // [T] position of each token with an adapter
+  LoraPiece* pieces;      // adapters in order, one piece at least for each
+  int* n_pieces;
+  int* slots;             // [L] pieces of each adapter
+  int* first_slot;        // [L]
+  int* last_pos;          // [L]
+};
+struct LoraPrepGrid {
+  uint32_t tb, ta, dq, pad;
+  int waves;
+};
+hipError_t launch_lora_prep(const LoraPrep& p, hipStream_t st);
+
+// The adapters' gradients (lora_grad.hip).
+struct LoraGrad {
   const uint16_t* dY;     // [T, N]
   const void* X;          // [T, K] 16-bit, or int8 codes (then steps is set)
   const float* steps;     // [T, K / 128] or NULL
-  const float* H;         // [T, r]
-  int64_t T;
-  LoraLayer w;
-  LoraSet s;
-  float* G;               // [T, r]
-  uint16_t* dX;           // [T, K] or NULL
+  const float* Gt;        // [r, Tp] dY·B, transposed, in sorted order
+  const float* Ht;        // [r, Tp]
+  const float* g_max;     // [Tp] largest |value| of each token
+  const float* h_max;
+  const float* scaling;
+  const int* token;
+  const LoraPiece* pieces;
+  const int* n_pieces;
+  const int* slots;
+  const int* first_slot;
+  int64_t N, K, Tp;
+  int L, r, f16;
+  float* partial;         // [slots, (K + N)·r]
   uint16_t* dA;           // [L, r, K]
   uint16_t* dB;           // [L, N, r]
-  int f16;
 };
+hipError_t launch_lora_grad(const LoraGrad& p, int pieces, bool sums, hipStream_t st);
 
 hipError_t launch_lora_forward(const LoraForward& p, hipStream_t st);
-hipError_t launch_lora_backward(const LoraBackward& p, hipStream_t st);
 
 // Activation checkpoints: codes [T, K] int8, steps [T, K / 128] float32.
 hipError_t launch_act_pack8(const void* X, int dtype, int64_t T, int64_t K, int8_t* codes,

@@ -114,69 +114,6 @@ __global__ __launch_bounds__(256) void lora_product_kernel(const uint16_t* __res
   }
 }
 
-// dA_a[j][k] = Σ_t G[t][j]·X[t][k] over the tokens of a (grid: k blocks of
-// 256, blocks of 8 j, adapters). X is 16-bit, or 8-bit codes and steps.
-template <bool F16, bool X8>
-__global__ __launch_bounds__(256) void lora_grad_a_kernel(const void* __restrict__ X,
-                                                          const float* __restrict__ steps,
-                                                          int64_t T, int64_t K, LoraSet s,
-                                                          const float* __restrict__ G,
-                                                          uint16_t* __restrict__ dA) {
-  const int64_t k = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  const int j0 = int(blockIdx.y) * 8, a = int(blockIdx.z);
-  if (k >= K) return;
-  float acc[8] = {};
-  for (int64_t t = 0; t < T; ++t) {
-    if (s.ids[t] != a) continue;
-    float x;
-    if constexpr (X8)
-      x = float(static_cast<const int8_t*>(X)[t * K + k]) * steps[t * (K / 128) + k / 128];
-    else
-      x = from16<F16>(static_cast<const uint16_t*>(X)[t * K + k]);
-    for (int j = 0; j < 8; ++j) acc[j] = __builtin_fmaf(G[t * s.r + j0 + j], x, acc[j]);
-  }
-  for (int j = 0; j < 8; ++j) dA[(int64_t(a) * s.r + j0 + j) * K + k] = to16<F16>(acc[j]);
-}
-
-// dB_a[n][j] = c_a·Σ_t dY[t][n]·H[t][j] over the tokens of a.
-template <bool F16>
-__global__ __launch_bounds__(256) void lora_grad_b_kernel(const uint16_t* __restrict__ dY,
-                                                          int64_t T, int64_t N, LoraSet s,
-                                                          const float* __restrict__ H,
-                                                          uint16_t* __restrict__ dB) {
-  const int64_t n = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  const int j0 = int(blockIdx.y) * 8, a = int(blockIdx.z);
-  if (n >= N) return;
-  float acc[8] = {};
-  for (int64_t t = 0; t < T; ++t) {
-    if (s.ids[t] != a) continue;
-    const float dy = from16<F16>(dY[t * N + n]);
-    for (int j = 0; j < 8; ++j) acc[j] = __builtin_fmaf(H[t * s.r + j0 + j], dy, acc[j]);
-  }
-  for (int j = 0; j < 8; ++j)
-    dB[(int64_t(a) * N + n) * s.r + j0 + j] = to16<F16>(s.scaling[a] * acc[j]);
-}
-
-template <bool F16>
-hipError_t backward(const LoraBackward& p, hipStream_t st) {
-  lora_down_kernel<F16, false, true>
-      <<<unsigned(p.T), 256, 0, st>>>(p.dY, p.w.N, p.s, p.s.B, p.G);
-  if (p.dX) {
-    const dim3 grid(unsigned((p.w.K + 63) / 64), unsigned((p.T + 63) / 64));
-    lora_product_kernel<F16, true><<<grid, 256, 0, st>>>(p.dY, p.T, p.w, p.s, p.G, p.dX);
-  }
-  const dim3 ga(unsigned((p.w.K + 255) / 256), unsigned(p.s.r / 8), unsigned(p.s.L));
-  if (p.steps)
-    lora_grad_a_kernel<F16, true>
-        <<<ga, 256, 0, st>>>(p.X, p.steps, p.T, p.w.K, p.s, p.G, p.dA);
-  else
-    lora_grad_a_kernel<F16, false>
-        <<<ga, 256, 0, st>>>(p.X, p.steps, p.T, p.w.K, p.s, p.G, p.dA);
-  const dim3 gb(unsigned((p.w.N + 255) / 256), unsigned(p.s.r / 8), unsigned(p.s.L));
-  lora_grad_b_kernel<F16><<<gb, 256, 0, st>>>(p.dY, p.T, p.w.N, p.s, p.H, p.dB);
-  return hipGetLastError();
-}
-
 }  // namespace
 
 template <bool F16>
@@ -215,10 +152,6 @@ hipError_t launch_lora_forward(const LoraForward& p, hipStream_t st) {
   if (e != hipSuccess) return e;
   const LoraUp u{p.Q, p.E, p.s.ids, p.s.B, p.s.L, p.s.r, p.RW};
   return launch_lora_gemm(p.X, p.w.K, p.Wd, p.w.K, p.T, p.w.N, p.w.K, u, p.f16, p.Y, st);
-}
-
-hipError_t launch_lora_backward(const LoraBackward& p, hipStream_t st) {
-  return p.f16 ? backward<true>(p, st) : backward<false>(p, st);
 }
 
 }  // namespace awq

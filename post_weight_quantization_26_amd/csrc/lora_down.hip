@@ -34,6 +34,31 @@ namespace {
 constexpr int kDownWaves = 8;
 constexpr int kDownThreads = 64 * kDownWaves;
 
+// H as the gradients read it: transposed, in sorted order. 64 tokens a
+// workgroup, a wave per token at a time.
+__device__ __forceinline__ void transpose_h(const LoraDown& p, int64_t block) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int i = wave; i < 64; i += kDownWaves) {
+    const int64_t t = block * 64 + i;
+    if (t >= p.T) return;
+    const int id = p.ids[t];
+    if (id < 0 || id >= p.L) continue;
+    const int pos = p.pos[t];
+    float m = 0.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int j = lane + 64 * h;
+      if (j >= p.r) continue;
+      const float v = p.Hin[t * p.r + j];
+      p.Ht[int64_t(j) * p.ldp + pos] = v;
+      m = fmaxf(m, fabsf(v));
+    }
+#pragma unroll
+    for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    if (lane == 0) p.h_max[pos] = m;
+  }
+}
+
 // JB·16 >= min(r, 64): rank columns per pass (r above 64 takes two passes).
 template <bool F16, int MT, int JB, bool PACK8>
 __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(LoraDown p) {
@@ -46,6 +71,7 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(LoraDown p) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lg = lane >> 4;
   const int64_t t0 = int64_t(blockIdx.x) * R;
+  if (t0 >= p.T) return transpose_h(p, int64_t(blockIdx.x) - (p.T + R - 1) / R);
   if (tid < R) sid[tid] = t0 + tid < p.T ? p.ids[t0 + tid] : -1;
   __syncthreads();
   const int my_id = lane < R ? sid[lane] : -1;
@@ -199,7 +225,9 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(LoraDown p) {
 
 template <bool F16, int MT, int JB>
 hipError_t launch_jb(const LoraDown& p, hipStream_t st) {
-  const unsigned grid = unsigned((p.T + 16 * MT - 1) / (16 * MT));
+  // the tokens' tiles, then H's
+  const unsigned grid =
+      unsigned((p.T + 16 * MT - 1) / (16 * MT) + (p.Hin ? (p.T + 63) / 64 : 0));
   if (p.codes) lora_down_kernel<F16, MT, JB, true><<<grid, kDownThreads, 0, st>>>(p);
   else lora_down_kernel<F16, MT, JB, false><<<grid, kDownThreads, 0, st>>>(p);
   return hipGetLastError();

@@ -1,0 +1,272 @@
+// Gradients of the adapters,
+//
+//   dA_a[j][k] = c_a·Σ_t P[t][j]·X[t][k],   dB_a[n][j] = c_a·Σ_t dY[t][n]·H[t][j]
+//
+// over the tokens t of a, P = dY·B_a: products with a long contraction (tokens)
+// and one narrow side (r). Both are Z ᵀ·S with Z = X or dY, read once, and S
+// the narrow side, laid out as Sᵀ [r, positions] in the plan's sorted order.
+//
+// A workgroup takes 128 columns of Z, up to 64 ranks and one piece of a run;
+// its 4 waves take every fourth step of 32 tokens. A lane loads 8 channels of
+// 8 tokens (rows gathered through the plan, 256 contiguous bytes for 16
+// lanes); 32 byte permutes turn the 8x8 block into 8 MFMA operands of 8
+// tokens each, channel 8·(l % 16) + i for operand i: no pass through LDS.
+// S comes as float32 and is split in registers into two 16-bit halves, so
+// that its rounding is u² (bf16 2^-16). fp16 halves are scaled by one power
+// of two per piece that takes the piece's largest |S| to 2^14: a value 2^-17
+// times as large still keeps 2^-22 of itself.
+//
+// An 8-bit checkpoint of X enters as fp16 numbers (code, exact) and its steps
+// go into S: a strip of 128 channels has one step per token.
+//
+// The waves add up in LDS in a fixed order. A run of one piece is finished
+// here; pieces of a longer run leave float32 sums that lora_grad_sum_kernel adds
+// in order. Runs never share a piece and padding repeats a run's last token
+// with S = 0, so no adapter sees another's values.
+#include "gemm_types.h"
+#include "lora.h"
+#include "lora_common.h"
+
+namespace awq {
+namespace {
+
+constexpr int kGradWaves = 4;
+constexpr int kGradStrip = 128;
+
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  return uint32_t(round16<F16>(a)) | uint32_t(round16<F16>(b)) << 16;
+}
+
+// MF: fp16 matrix-core operands (fp16 Z, or 8-bit codes); else bf16.
+template <bool F16, bool X8, int JB>
+__device__ __forceinline__ void grad_piece(const LoraGrad& p, const LoraPiece& pc, bool is_a,
+                                           int64_t strip, int j0, float (*red)[16 * JB][kGradStrip + 4]) {
+  constexpr bool MF = F16 || X8;
+  typedef typename Operand<MF>::type V;
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+  const int64_t C = is_a ? p.K : p.N;
+  const float* St = is_a ? p.Gt : p.Ht;
+  const float* row_max = is_a ? p.g_max : p.h_max;
+  const int64_t c0 = strip * kGradStrip;
+  const int64_t cl = c0 + 8 * lr < C ? c0 + 8 * lr : C - 8;   // lanes past the last column reread it
+  const int64_t KB = p.K / 128;
+
+  float scale = 1.f;
+  if constexpr (MF) {
+    float m = 0.f;
+    for (int i = lane; i < pc.n; i += 64) {
+      float v = row_max[pc.pos + i];
+      if constexpr (X8) v *= p.steps[int64_t(p.token[pc.pos + i]) * KB + strip];
+      m = fmaxf(m, v);
+    }
+#pragma unroll
+    for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    if (m > 0.f && m < __builtin_inff()) scale = exp2i(14 - exponent_of(m));
+  }
+  floatx4 acc[JB][8];
+#pragma unroll
+  for (int q = 0; q < JB; ++q)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[q][i] = floatx4{0.f, 0.f, 0.f, 0.f};
+
+  for (int s = 32 * wave; s < pc.n; s += 32 * kGradWaves) {
+    const int at = pc.pos + s + 8 * lg;
+    const int4 ta = *reinterpret_cast<const int4*>(p.token + at);
+    const int4 tb = *reinterpret_cast<const int4*>(p.token + at + 4);
+    const int tok[8] = {ta.x, ta.y, ta.z, ta.w, tb.x, tb.y, tb.z, tb.w};
+    uint32_t z[8][X8 ? 2 : 4];
+    float step[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (X8) {
+        const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const int8_t*>(p.X) +
+                                                        int64_t(tok[e]) * C + cl);
+        z[e][0] = x.x ^ 0x80808080u;
+        z[e][1] = x.y ^ 0x80808080u;
+        step[e] = p.steps[int64_t(tok[e]) * KB + strip];
+      } else {
+        const uint16_t* Z = is_a ? static_cast<const uint16_t*>(p.X) : p.dY;
+        const uint4 x = *reinterpret_cast<const uint4*>(Z + int64_t(tok[e]) * C + cl);
+        z[e][0] = x.x;
+        z[e][1] = x.y;
+        z[e][2] = x.z;
+        z[e][3] = x.w;
+      }
+    }
+    V sh[JB], sl[JB];
+#pragma unroll
+    for (int q = 0; q < JB; ++q) {
+      const int j = j0 + 16 * q + lr;
+      const float* row = St + int64_t(j < p.r ? j : p.r - 1) * p.Tp + at;
+      const float4 a = *reinterpret_cast<const float4*>(row);
+      const float4 b = *reinterpret_cast<const float4*>(row + 4);
+      float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if constexpr (X8) v[e] *= step[e];
+        if constexpr (MF) v[e] *= scale;
+        if (s + 8 * lg + e >= pc.n) v[e] = 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        hi[e] = pack2<MF>(v[2 * e], v[2 * e + 1]);
+        lo[e] = pack2<MF>(v[2 * e] - widen16<MF>(uint16_t(hi[e])),
+                          v[2 * e + 1] - widen16<MF>(uint16_t(hi[e] >> 16)));
+      }
+      sh[q] = __builtin_bit_cast(V, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+      sl[q] = __builtin_bit_cast(V, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (X8) {
+          constexpr uint32_t kZero = 0x0C000C00u;
+          const uint32_t b = i & 3;
+          const uint32_t x = __builtin_amdgcn_perm(z[2 * e + 1][i >> 2], z[2 * e][i >> 2],
+                                                   kZero | ((4u + b) << 16) | b);
+          // fp16 1024 + (code + 128), less 1152: the code
+          const f16x2_t v = __builtin_bit_cast(f16x2_t, x | 0x64006400u) -
+                            f16x2_t{_Float16(1152.f), _Float16(1152.f)};
+          w[e] = __builtin_bit_cast(uint32_t, v);
+        } else {
+          w[e] = __builtin_amdgcn_perm(z[2 * e + 1][i >> 1], z[2 * e][i >> 1],
+                                       i & 1 ? 0x07060302u : 0x05040100u);
+        }
+      }
+      const V zv = __builtin_bit_cast(V, make_uint4(w[0], w[1], w[2], w[3]));
+#pragma unroll
+      for (int q = 0; q < JB; ++q) {
+        acc[q][i] = mfma_16x16x32(sh[q], zv, acc[q][i]);
+        acc[q][i] = mfma_16x16x32(sl[q], zv, acc[q][i]);
+      }
+    }
+  }
+  // lane l holds channel 8·(l % 16) + i and ranks 16·q + 4·(l / 16) + v
+  const float post = pc.n ? p.scaling[pc.a] / scale : 0.f;   // no tokens: zeros
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    if (wave >> 1 == half) {
+      float(*R)[kGradStrip + 4] = red[wave & 1];
+#pragma unroll
+      for (int q = 0; q < JB; ++q)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          float* row = &R[16 * q + 4 * lg + v][8 * lr];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float4 x = make_float4(acc[q][4 * h][v], acc[q][4 * h + 1][v], acc[q][4 * h + 2][v],
+                                   acc[q][4 * h + 3][v]);
+            if (half) {
+              const float4 y = *reinterpret_cast<const float4*>(row + 4 * h);
+              x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+            }
+            *reinterpret_cast<float4*>(row + 4 * h) = x;
+          }
+        }
+    }
+    __syncthreads();
+  }
+  // 8 consecutive values of the output's rows per thread: channels of dA
+  // [r, K], ranks of dB [N, r]
+  const int ranks = p.r - j0 < 16 * JB ? p.r - j0 : 16 * JB;
+  const int items = ranks / 8 * kGradStrip;
+  for (int e = threadIdx.x; e < items; e += 64 * kGradWaves) {
+    int j, c;
+    float v[8];
+    if (is_a) {
+      j = e / (kGradStrip / 8);
+      c = e % (kGradStrip / 8) * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = (red[0][j][c + i] + red[1][j][c + i]) * post;
+    } else {
+      c = e % kGradStrip;
+      j = e / kGradStrip * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = (red[0][j + i][c] + red[1][j + i][c]) * post;
+    }
+    if (c0 + c >= C) continue;
+    const int64_t at = is_a ? int64_t(j0 + j) * C + c0 + c : (c0 + c) * p.r + j0 + j;
+    if (pc.slot < 0) {
+      uint16_t* out = (is_a ? p.dA : p.dB) + int64_t(pc.a) * p.r * C + at;
+      *reinterpret_cast<uint4*>(out) = make_uint4(pack2<F16>(v[0], v[1]), pack2<F16>(v[2], v[3]),
+                                                  pack2<F16>(v[4], v[5]), pack2<F16>(v[6], v[7]));
+    } else {
+      float* out = p.partial + (int64_t(pc.slot) * (p.K + p.N) + (is_a ? 0 : p.K)) * p.r + at;
+      *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(out + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  }
+}
+
+// Grid: strips of X then of dY; pieces; blocks of 16·JB ranks.
+template <bool F16, bool X8, int JB>
+__global__ __launch_bounds__(64 * kGradWaves, 2) void lora_grad_kernel(LoraGrad p) {
+  __shared__ float red[2][16 * JB][kGradStrip + 4];
+  if (int(blockIdx.y) >= *p.n_pieces) return;
+  const LoraPiece pc = p.pieces[blockIdx.y];
+  const int64_t sa = p.K / kGradStrip, strip = blockIdx.x;
+  const int j0 = int(blockIdx.z) * 16 * JB;
+  if (strip < sa) grad_piece<F16, X8, JB>(p, pc, true, strip, j0, red);
+  else grad_piece<F16, false, JB>(p, pc, false, strip - sa, j0, red);
+}
+
+// The sum of a longer run's pieces, in order; 8 values per thread.
+template <bool F16>
+__global__ __launch_bounds__(256) void lora_grad_sum_kernel(LoraGrad p) {
+  const int a = int(blockIdx.y), n = p.slots[a];
+  if (n < 2) return;
+  const int64_t ra = p.K * p.r, all = (p.K + p.N) * p.r;
+  const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 8;
+  if (i >= all) return;
+  const float* src = p.partial + int64_t(p.first_slot[a]) * all + i;
+  float v[8] = {};
+  for (int q = 0; q < n; ++q) {
+    const float4 x = *reinterpret_cast<const float4*>(src + q * all);
+    const float4 y = *reinterpret_cast<const float4*>(src + q * all + 4);
+    v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+    v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+  }
+  uint16_t* out = i < ra ? p.dA + a * ra + i : p.dB + a * (all - ra) + (i - ra);
+  *reinterpret_cast<uint4*>(out) = make_uint4(pack2<F16>(v[0], v[1]), pack2<F16>(v[2], v[3]),
+                                              pack2<F16>(v[4], v[5]), pack2<F16>(v[6], v[7]));
+}
+
+template <bool F16, bool X8>
+void launch_x8(const LoraGrad& p, int pieces, hipStream_t st) {
+  const unsigned strips = unsigned(p.K / kGradStrip + (p.N + kGradStrip - 1) / kGradStrip);
+  if (p.r <= 16)
+    lora_grad_kernel<F16, X8, 1><<<dim3(strips, pieces, 1), 64 * kGradWaves, 0, st>>>(p);
+  else if (p.r <= 32)
+    lora_grad_kernel<F16, X8, 2><<<dim3(strips, pieces, 1), 64 * kGradWaves, 0, st>>>(p);
+  else
+    lora_grad_kernel<F16, X8, 4><<<dim3(strips, pieces, (p.r + 63) / 64), 64 * kGradWaves, 0,
+                                   st>>>(p);
+}
+
+template <bool F16>
+hipError_t launch_f(const LoraGrad& p, int pieces, bool sums, hipStream_t st) {
+  if (p.steps) launch_x8<F16, true>(p, pieces, st);
+  else launch_x8<F16, false>(p, pieces, st);
+  if (sums) {
+    const unsigned blocks = unsigned(((p.K + p.N) * p.r / 8 + 255) / 256);
+    lora_grad_sum_kernel<F16><<<dim3(blocks, p.L), 256, 0, st>>>(p);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// pieces: at least the plan's; sums: whether a run may have more than one.
+hipError_t launch_lora_grad(const LoraGrad& p, int pieces, bool sums, hipStream_t st) {
+  if (p.K % kGradStrip || p.N % 8 || p.r % 8 || pieces > 65535) return hipErrorInvalidValue;
+  return p.f16 ? launch_f<true>(p, pieces, sums, st) : launch_f<false>(p, pieces, sums, st);
+}
+
+}  // namespace awq

@@ -508,10 +508,44 @@ LoraLayout lora_layout(int64_t T, int64_t N, int64_t K, int32_t, int32_t r) {
   return l;
 }
 
-LoraLayout lora_backward_layout(int64_t T, int64_t, int64_t, int32_t, int32_t r) {
-  LoraLayout l{};
-  l.h = 0;
-  l.total = align_up(size_t(T) * size_t(r) * 4);
+LoraBackwardLayout lora_backward_layout(int64_t T, int64_t N, int64_t K, int32_t L, int32_t r) {
+  LoraBackwardLayout l{};
+  l.Np = ceil_div(N, 128) * 128;
+  const int64_t runs = std::min<int64_t>(L, T);
+  l.Tp = ceil_div(T, 32) * 32 + 32 * runs;
+  // Pieces as long as still gives 1024 workgroups of 128 columns (4 per CU):
+  // each piece of a longer run costs its float32 sums once out and in.
+  const int64_t strips = ceil_div(K, 128) + ceil_div(N, 128);
+  l.piece = std::min<int64_t>(2048, ceil_div(ceil_div(T * strips, 1024), 32) * 32);
+  l.piece = std::max<int64_t>({l.piece, 128, ceil_div(ceil_div(T, 32768), 32) * 32});
+  l.pieces = T / l.piece + L;
+  l.slots = T > l.piece ? 2 * (T / l.piece) + 1 : 0;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += align_up(bytes);
+    return at;
+  };
+  const size_t t = size_t(T), n = size_t(l.Np), k = size_t(K), tp = size_t(l.Tp), a = size_t(L);
+  l.wt = take(k * n * 2);
+  l.bt = take(a * r * n * 2);
+  l.at = take(a * r * k * 2);
+  l.dyp = take(l.Np == N ? 0 : t * n * 2);
+  l.q = take(t * size_t(lora_q_width(r)) * 2);
+  l.e = take(t * 4);
+  l.gt = take(tp * r * 4);
+  l.ht = take(tp * r * 4);
+  l.gmax = take(tp * 4);
+  l.hmax = take(tp * 4);
+  l.token = take(tp * 4);
+  l.pos = take(t * 4);
+  l.table = take(size_t(l.pieces) * 16);
+  l.n_pieces = take(4);
+  l.n_slots = take(a * 4);
+  l.first_slot = take(a * 4);
+  l.last_pos = take(a * 4);
+  l.partial = take(size_t(l.slots) * (k + size_t(N)) * r * 4);
+  l.total = off;
   return l;
 }
 
@@ -594,11 +628,20 @@ awq_status check_lora_backward(const void* dY, const void* X, const float* x8_st
   if (!tile_rows_fit(N))
     return set_error(AWQ_E_UNSUPPORTED, "%s: N=%lld exceeds the 32-bit offsets (512 * N must "
                      "stay below 2^31)", name, (long long)N);
+  const LoraBackwardLayout l = lora_backward_layout(T, N, K, L, r);
+  const int64_t prep = 1 + L * (l.Np + K) / 64 + ceil_div(K / 8 * (l.Np / 8), 1024) +
+                       ceil_div(T * (l.Np / 8), 1024);
+  const int64_t grad = (K / 128 + ceil_div(N, 128)) * l.pieces * 2;
+  const int64_t sums = ceil_div((K + N) * r / 8, 256) * L;
+  if (l.pieces > 65535 || l.Tp > kMaxDim || !grid_fits(prep, 1024) || !grid_fits(grad, 256) ||
+      !grid_fits(sums, 256))
+    return set_error(AWQ_E_UNSUPPORTED, "%s: T=%lld tokens of L=%d adapters exceed the grids",
+                     name, (long long)T, int(L));
   if (!aligned16(X) || !aligned16(H) || !aligned4(x8_steps) || !aligned16(dX) ||
       !aligned16(dA) || !aligned16(dB))
     return set_error(AWQ_E_INVALID,
                      "%s: X, H and the gradients must be 16-byte aligned, steps 4", name);
-  const size_t need = lora_backward_layout(T, N, K, L, r).total;
+  const size_t need = l.total;
   if (!ws || !aligned16(ws) || ws_bytes < need)
     return set_error(AWQ_E_WORKSPACE, "%s: workspace needs %zu bytes (16-byte aligned)", name,
                      need);
