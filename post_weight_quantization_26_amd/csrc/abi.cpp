@@ -757,22 +757,66 @@ extern "C" awq_status awq_w4a16_lora_matmul(
   if (st_ != AWQ_OK) return st_;
   hipStream_t st = static_cast<hipStream_t>(stream);
   const LoraLayout l = lora_layout(T, N, K, L, r);
-  LoraForward p{};
-  p.X = static_cast<const uint16_t*>(X);
-  p.T = T;
-  p.w = {qweight, qzeros, scales, N, K, group_size};
-  p.s = {static_cast<const uint16_t*>(A), static_cast<const uint16_t*>(B), scaling, ids, L, r};
-  p.Y = static_cast<uint16_t*>(Y);
-  p.H = H;
-  p.codes = x8_codes;
-  p.steps = x8_steps;
-  p.f16 = dtype == AWQ_F16;
-  p.Q = at<uint16_t>(ws, l.q);
-  p.E = at<float>(ws, l.e);
-  p.Wd = at<uint16_t>(ws, l.wd);
-  p.P = at<float>(ws, l.h);
-  p.RW = lora_q_width(r);
-  AWQ_HIP(timed(AWQ_K_LORA, st, [&] { return launch_lora_forward(p, st); }), "lora_matmul");
+  const LoraLayer layer = {qweight, qzeros, scales, N, K, group_size};
+  const LoraSet set = {static_cast<const uint16_t*>(A), static_cast<const uint16_t*>(B), scaling,
+                       ids, L, r};
+  const uint16_t* x = static_cast<const uint16_t*>(X);
+  uint16_t* y = static_cast<uint16_t*>(Y);
+  const int f16 = dtype == AWQ_F16;
+  if (T <= kLoraFewMaxT) {
+    LoraFew p{};
+    p.X = x;
+    p.T = T;
+    p.w = layer;
+    p.s = set;
+    p.Y = y;
+    p.H = H;
+    p.partial = at<float>(ws, l.partial);
+    p.hpart = at<float>(ws, l.hpart);
+    p.S = int(l.S);
+    p.S2 = int(l.S2);
+    p.kpw = int(l.kpw);
+    p.tiles = int(l.tiles);
+    p.col_blocks = int(l.col_blocks);
+    p.gshift = group_size == 32 ? 5 : group_size == 64 ? 6 : 7;
+    p.gemv = N % 16 != 0;
+    p.f16 = f16;
+    AWQ_HIP(timed(AWQ_K_LORA, st, [&] { return launch_lora_few(p, st); }), "lora_matmul");
+    if (x8_codes)
+      AWQ_HIP(timed(AWQ_K_ACT8, st,
+                    [&] { return launch_act_pack8(X, dt(dtype), T, K, x8_codes, x8_steps, st); }),
+              "lora_matmul checkpoint");
+    return AWQ_OK;
+  }
+  LoraDown d{};
+  d.V = x;
+  d.M = set.A;
+  d.scaling = scaling;
+  d.ids = ids;
+  d.T = T;
+  d.C = d.ldv = d.ldm = K;
+  d.L = L;
+  d.r = r;
+  d.f16 = f16;
+  d.H = H;
+  d.Q = at<uint16_t>(ws, l.q);
+  d.RW = lora_q_width(r);
+  d.E = at<float>(ws, l.e);
+  d.codes = x8_codes;
+  d.steps = x8_steps;
+  uint16_t* Wd = at<uint16_t>(ws, l.wd);
+  const LoraUp u{d.Q, d.E, ids, set.B, L, r, d.RW};
+  AWQ_HIP(timed(AWQ_K_LORA, st,
+                [&] {
+                  hipError_t e = launch_lora_down(d, st);
+                  if (e == hipSuccess)
+                    e = launch_w4a16_dequant(qweight, qzeros, scales, N, K, group_size, f16, Wd,
+                                             st);
+                  if (e == hipSuccess)
+                    e = launch_lora_gemm(x, K, Wd, K, T, N, K, u, f16, y, st);
+                  return e;
+                }),
+          "lora_matmul");
   return AWQ_OK;
 }
 

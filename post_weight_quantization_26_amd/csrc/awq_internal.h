@@ -209,8 +209,12 @@ constexpr int kLoraMaxAdapters = 4096;
 // Columns of a token's wide-product operand: c·P as two 16-bit halves, padded
 // with zeros to whole 32-wide MFMA steps.
 inline int lora_q_width(int32_t r) { return int((2 * r + 31) / 32 * 32); }
+// Token rows up to which the forward call runs without a dequantised layer.
+constexpr int64_t kLoraFewMaxT = 256;
 struct LoraLayout {
-  size_t h;       // [T, r] f32 (T <= 16)
+  size_t partial; // few tokens: [S, T, N] f32 sums of the shared product, ..
+  size_t hpart;   // .. and [S2, T, r] f32 of the narrow one
+  int64_t S, S2, kpw, tiles, col_blocks;
   size_t q;       // [T, lora_q_width(r)] 16-bit
   size_t e;       // [T] f32
   size_t wd;      // [N, K] 16-bit dequantised layer

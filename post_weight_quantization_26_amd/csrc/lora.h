@@ -66,23 +66,27 @@ hipError_t launch_w4a16_dequant(const int32_t* qweight, const int32_t* qzeros,
                                 const uint16_t* scales, int64_t N, int64_t K, int group, int f16,
                                 uint16_t* Wd, hipStream_t st);
 
-struct LoraForward {
+// The float32 decode for N not a multiple of 16 (w4a16.hip).
+hipError_t launch_w4a16_gemv(const uint16_t* X, int64_t T, int64_t N, int64_t K,
+                             const int32_t* qweight, const int32_t* qzeros,
+                             const uint16_t* scales, int group, int f16, int64_t kpw,
+                             float* partial, hipStream_t st);
+
+// Few tokens, forward (lora_few.hip).
+struct LoraFew {
   const uint16_t* X;      // [T, K]
   int64_t T;
   LoraLayer w;
   LoraSet s;
   uint16_t* Y;            // [T, N]
   float* H;               // [T, r] or NULL
-  int8_t* codes;          // [T, K] or NULL
-  float* steps;           // [T, K / 128]
-  int f16;
-  // workspace
-  uint16_t* Q;            // [T, RW]
-  float* E;               // [T]
-  uint16_t* Wd;           // [N, K]
-  float* P;               // [T, r] (T <= 16)
-  int RW;
+  float* partial;         // [S, T, N]
+  float* hpart;           // [S2, T, r]
+  int S, S2, kpw;         // runs of k of the two products; k rows per wave of the shared one
+  int tiles, col_blocks;  // T > 16: token tiles and column blocks
+  int gshift, gemv, f16;  // log2 of the group; T <= 16: the float32 decode
 };
+hipError_t launch_lora_few(const LoraFew& p, hipStream_t st);
 
 // A piece of one adapter's run of sorted tokens: positions pos .. pos + n - 1;
 // slot of its partial sums, or -1 where it is the whole run.
@@ -137,8 +141,6 @@ struct LoraGrad {
   uint16_t* dB;           // [L, N, r]
 };
 hipError_t launch_lora_grad(const LoraGrad& p, int pieces, bool sums, hipStream_t st);
-
-hipError_t launch_lora_forward(const LoraForward& p, hipStream_t st);
 
 // Activation checkpoints: codes [T, K] int8, steps [T, K / 128] float32.
 hipError_t launch_act_pack8(const void* X, int dtype, int64_t T, int64_t K, int8_t* codes,

@@ -1,0 +1,451 @@
+// Low-rank adapters for few tokens (decoding requests, short prompts), in two
+// launches:
+//
+//  1. the shared product as float32 partial sums over runs of k, and beside
+//     it, in workgroups of their own, the narrow products A_a·x;
+//  2. the sum of the partials, the wide product B_a·h of each token's adapter,
+//     one rounding, and H if it is wanted.
+//
+// Both are bound by the bytes of the packed layer and of the adapters in use:
+// nothing but partial sums goes to memory in between, and the adapters' reads
+// overlap the layer's.
+//
+// The shared product, T <= 16: the matrix-core decode of w4a16.hip (exact Ŵ).
+// Above: a wave takes 16·MT tokens x 128 outputs and a run of k. Lane l holds
+// k rows 8·(l / 16) .. + 7 of word column l % 16, so nibble r of its 8 words
+// is the MFMA operand of outputs 8·(l % 16) + r; the words become the rounded
+// Ŵ in registers, as the dequantisation pass rounds it:
+//   the codes of two k rows, put in the halves of a word by one byte permute,
+//   turn into fp16 numbers B + q by one and-or (B = 1024 for the low nibble
+//   of a byte, 64 for the high one);
+//   fp16: (B + q) - (B + z) exactly, times scale, rounded once;
+//   bf16: float32 fma((B + q), scale, -(B + z)·scale), which is (q - z)·scale
+//   exactly, rounded once.
+// Each word serves 16·MT tokens. The 4 waves' runs meet in LDS, in order.
+#include "gemm_types.h"
+#include "lora.h"
+#include "lora_common.h"
+#include "w4a16_mgemv.h"
+
+namespace awq {
+namespace {
+
+constexpr int kFewWaves = 4;
+constexpr int kFewCols = 128;     // outputs per workgroup (T > 16)
+
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+
+// ---------------------------------------------------------------------------
+// launch 1: the narrow product
+// ---------------------------------------------------------------------------
+
+// Workgroup (tile of 16 tokens, row, block of 16 ranks, run of k): if `row` is
+// the first of the tile with its adapter, the adapter's 16 x 16 block of P for
+// all rows of the tile that have it, as a float32 partial sum.
+__device__ __forceinline__ void few_down_index(const LoraFew& p, int id, int& tile, int& row,
+                                               int& jb, int& ks) {
+  const int jbs = (p.s.r + 15) / 16, rows = p.T < 16 ? int(p.T) : 16;
+  ks = id % p.S2;
+  id /= p.S2;
+  jb = id % jbs;
+  id /= jbs;
+  row = id % rows;
+  tile = id / rows;
+}
+
+template <bool F16>
+__device__ __forceinline__ void few_down(const LoraFew& p, int id, float (*red)[16][17]) {
+  typedef typename Operand<F16>::type V;
+  int tile, row, jb, ks;
+  few_down_index(p, id, tile, row, jb, ks);
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+  const int64_t t0 = int64_t(tile) * 16, t = t0 + lr, K = p.w.K;
+  const int my = t < p.T ? p.s.ids[t] : -1;
+  const int a = __builtin_amdgcn_readlane(my, row);
+  const uint32_t mine = uint32_t(__ballot(my == a)) & 0xFFFFu;
+  if (a < 0 || a >= p.s.L || int(__builtin_ctz(mine)) != row) return;
+  const int nb = int(K / 128), b0 = int(int64_t(nb) * ks / p.S2),
+            b1 = int(int64_t(nb) * (ks + 1) / p.S2);
+  const int j = 16 * jb + lr;
+  const uint16_t* xr = p.X + (t < p.T ? t : p.T - 1) * K + 8 * lg;
+  const uint16_t* ar = p.s.A + (int64_t(a) * p.s.r + (j < p.s.r ? j : p.s.r - 1)) * K + 8 * lg;
+  floatx4 acc = {0.f, 0.f, 0.f, 0.f};
+  for (int b = b0 + wave; b < b1; b += kFewWaves) {
+    uint4 x[4], w[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      x[s] = *reinterpret_cast<const uint4*>(xr + int64_t(b) * 128 + 32 * s);
+      w[s] = *reinterpret_cast<const uint4*>(ar + int64_t(b) * 128 + 32 * s);
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      acc = mfma_16x16x32(__builtin_bit_cast(V, x[s]), __builtin_bit_cast(V, w[s]), acc);
+  }
+#pragma unroll
+  for (int v = 0; v < 4; ++v) red[wave][4 * lg + v][lr] = acc[v];
+  __syncthreads();
+  const int i = threadIdx.x >> 4, jj = threadIdx.x & 15;
+  if (((mine >> i) & 1u) && 16 * jb + jj < p.s.r)
+    p.hpart[(int64_t(ks) * p.T + t0 + i) * p.s.r + 16 * jb + jj] =
+        ((red[0][i][jj] + red[1][i][jj]) + red[2][i][jj]) + red[3][i][jj];
+}
+
+// ---------------------------------------------------------------------------
+// launch 1: the shared product, T > 16
+// ---------------------------------------------------------------------------
+
+template <int MT>
+struct FewSlot {
+  uint32_t w[8], z;
+  uint4 s, x[MT];
+};
+
+// The MFMA operand of nibble R: its 8 codes, one per word, as rounded Ŵ.
+template <bool F16, int R>
+__device__ __forceinline__ uint4 few_operand(const uint32_t (&w)[8], uint32_t z,
+                                             const uint32_t (&sw)[4]) {
+  constexpr uint32_t kSel = 0x0C000C00u | uint32_t(4 + R / 2) << 16 | uint32_t(R / 2);
+  constexpr uint32_t kMask = R & 1 ? 0x00F000F0u : 0x000F000Fu;
+  constexpr uint32_t kBase = R & 1 ? 0x54005400u : 0x64006400u;   // fp16 64 and 1024
+  const f16x2_t zb =
+      __builtin_bit_cast(f16x2_t, (__builtin_amdgcn_perm(z, z, kSel) & kMask) | kBase);
+  const _Float16 sc =
+      __builtin_bit_cast(_Float16, uint16_t(sw[R / 2] >> (16 * (R & 1))));
+  uint32_t out[4];
+  if constexpr (F16) {
+    const f16x2_t s2 = {sc, sc};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const f16x2_t q = __builtin_bit_cast(
+          f16x2_t, (__builtin_amdgcn_perm(w[2 * e + 1], w[2 * e], kSel) & kMask) | kBase);
+      const f16x2_t d = q - zb;
+      out[e] = __builtin_bit_cast(uint32_t, d * s2);
+    }
+  } else {
+    const float s = float(sc), nzs = -(float(zb[0]) * s);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const f16x2_t q = __builtin_bit_cast(
+          f16x2_t, (__builtin_amdgcn_perm(w[2 * e + 1], w[2 * e], kSel) & kMask) | kBase);
+      const float lo = __builtin_fmaf(float(q[0]), float(sc), nzs);
+      const float hi = __builtin_fmaf(float(q[1]), float(sc), nzs);
+      out[e] = uint32_t(round16<false>(lo)) | uint32_t(round16<false>(hi)) << 16;
+    }
+  }
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+template <bool F16, int MT>
+__device__ __forceinline__ void few_block(const FewSlot<MT>& sl, floatx4 (&acc)[8][MT]) {
+  typedef typename Operand<F16>::type V;
+  const uint32_t sw[4] = {sl.s.x, sl.s.y, sl.s.z, sl.s.w};
+#define AWQ_FEW_NIBBLE(R)                                                              \
+  {                                                                                    \
+    const V b = __builtin_bit_cast(V, few_operand<F16, R>(sl.w, sl.z, sw));            \
+    for (int m = 0; m < MT; ++m)                                                       \
+      acc[R][m] = mfma_16x16x32(__builtin_bit_cast(V, sl.x[m]), b, acc[R][m]);         \
+  }
+  // (two operands at a time: all eight at once would spill)
+  AWQ_FEW_NIBBLE(0) AWQ_FEW_NIBBLE(1)
+  __builtin_amdgcn_sched_barrier(0);
+  AWQ_FEW_NIBBLE(2) AWQ_FEW_NIBBLE(3)
+  __builtin_amdgcn_sched_barrier(0);
+  AWQ_FEW_NIBBLE(4) AWQ_FEW_NIBBLE(5)
+  __builtin_amdgcn_sched_barrier(0);
+  AWQ_FEW_NIBBLE(6) AWQ_FEW_NIBBLE(7)
+  __builtin_amdgcn_sched_barrier(0);
+#undef AWQ_FEW_NIBBLE
+}
+
+template <bool F16, int MT>
+__device__ __forceinline__ void few_product(const LoraFew& p, int id, int blocks,
+                                            float (*red)[16 * MT][kFewCols + 4]) {
+  constexpr int R = 16 * MT;
+  const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+  const int64_t N = p.w.N, K = p.w.K, N8 = N / 8;
+  // XCD i takes a contiguous run of (run of k, column block, token tile)
+  // indices, token tiles fastest: the tiles that read the same packed words
+  // and neighbouring column blocks, whose row segments share cache lines, meet
+  // in one L2
+  int tt, cb, s;
+  {
+    const int q = blocks / 8, rem = blocks % 8, xi = id % 8;
+    int l = xi * q + (xi < rem ? xi : rem) + id / 8;
+    tt = l % p.tiles;
+    l /= p.tiles;
+    cb = l % p.col_blocks;
+    s = l / p.col_blocks;
+  }
+  const int64_t t0 = int64_t(tt) * R, n0 = int64_t(cb) * kFewCols;
+  const int kw0 = (s * kFewWaves + wave) * p.kpw;
+  const int kw1 = kw0 + p.kpw < int(K) ? kw0 + p.kpw : int(K);
+  // lanes past N read column 0, token rows past T the last one: neither is
+  // ever stored, and no MFMA row or column depends on another
+  const int64_t col = n0 / 8 + lr < N8 ? n0 / 8 + lr : 0;
+  const int32_t* qw = p.w.qweight + int64_t(8 * lg) * N8 + col;
+  const uint16_t* xr[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int64_t t = t0 + 16 * m + lr;
+    xr[m] = p.X + (t < p.T ? t : p.T - 1) * K + 8 * lg;
+  }
+  floatx4 acc[8][MT];
+#pragma unroll
+  for (int r = 0; r < 8; ++r)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[r][m] = floatx4{0.f, 0.f, 0.f, 0.f};
+  if (kw0 < kw1) {
+    // blocks past the wave's last one read it again
+    auto load = [&](FewSlot<MT>& sl, int kb) {
+      const int k = kb < kw1 ? kb : kw1 - 32;
+      const int g = (k + 8 * lg) >> p.gshift;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sl.w[e] = uint32_t(qw[int64_t(k + e) * N8]);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) sl.x[m] = *reinterpret_cast<const uint4*>(xr[m] + k);
+      sl.z = uint32_t(p.w.qzeros[int64_t(g) * N8 + col]);
+      sl.s = *reinterpret_cast<const uint4*>(p.w.scales + int64_t(g) * N + 8 * col);
+    };
+    FewSlot<MT> a, b;
+    load(a, kw0);
+    for (int kb = kw0; kb < kw1; kb += 64) {
+      load(b, kb + 32);
+      few_block<F16, MT>(a, acc);
+      if (kb + 32 >= kw1) break;
+      load(a, kb + 64);
+      few_block<F16, MT>(b, acc);
+    }
+  }
+  // lane l holds outputs 8·(l % 16) + r, tokens 16·m + 4·(l / 16) + v
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    if (wave >> 1 == half) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          float* row = &red[wave & 1][16 * m + 4 * lg + v][8 * lr];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float4 x = make_float4(acc[4 * h][m][v], acc[4 * h + 1][m][v], acc[4 * h + 2][m][v],
+                                   acc[4 * h + 3][m][v]);
+            if (half) {
+              const float4 y = *reinterpret_cast<const float4*>(row + 4 * h);
+              x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+            }
+            *reinterpret_cast<float4*>(row + 4 * h) = x;
+          }
+        }
+    }
+    __syncthreads();
+  }
+  for (int e = threadIdx.x; e < R * kFewCols / 4; e += 64 * kFewWaves) {
+    const int i = e / (kFewCols / 4), c = e % (kFewCols / 4) * 4;
+    if (t0 + i >= p.T || n0 + c >= N) continue;
+    const float4 x = *reinterpret_cast<const float4*>(&red[0][i][c]);
+    const float4 y = *reinterpret_cast<const float4*>(&red[1][i][c]);
+    *reinterpret_cast<float4*>(p.partial + (int64_t(s) * p.T + t0 + i) * N + n0 + c) =
+        make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+  }
+}
+
+template <bool F16, int MT>
+__global__ __launch_bounds__(64 * kFewWaves, 2) void lora_few_kernel(LoraFew p, int downs) {
+  __shared__ union {
+    float down[kFewWaves][16][17];
+    float prod[2][16 * MT][kFewCols + 4];
+  } red;
+  const int id = int(blockIdx.x);
+  if (id < downs) few_down<F16>(p, id, red.down);
+  else few_product<F16, MT>(p, id - downs, int(gridDim.x) - downs, red.prod);
+}
+
+// T <= 16, N a multiple of 16.
+template <bool F16, int G, int TV>
+__global__ __launch_bounds__(64 * kFewWaves, 2) void lora_decode_kernel(LoraFew p, int downs,
+                                                                       int gx, int gy) {
+  __shared__ union {
+    float down[kFewWaves][16][17];
+    MgRed mg[kMgWaves];
+  } red;
+  const int id = int(blockIdx.x);
+  if (id < downs) few_down<F16>(p, id, red.down);
+  else
+    mgemv_workgroup<F16, 4, G, TV>(p.X, p.T, p.w.N, p.w.K, p.w.qweight, p.w.qzeros, p.w.scales,
+                                   p.kpw, p.partial, id - downs, gx, gy, red.mg);
+}
+
+template <bool F16>
+__global__ __launch_bounds__(64 * kFewWaves) void lora_few_down_kernel(LoraFew p) {
+  __shared__ float red[kFewWaves][16][17];
+  few_down<F16>(p, int(blockIdx.x), red);
+}
+
+// ---------------------------------------------------------------------------
+// launch 2
+// ---------------------------------------------------------------------------
+
+// Workgroup: 64 outputs x 16 tokens, a wave 16 outputs. NC·32 >= r. The rows'
+// h (summed over the runs of k) become two 16-bit halves in LDS, as in
+// lora_down.hip, and each adapter among the rows takes one pass of MFMAs whose
+// rows are kept where they belong to it. The next adapter's B is loaded while
+// the current one is used.
+template <bool F16, int NC>
+__global__ __launch_bounds__(64 * kFewWaves) void lora_few_finish_kernel(LoraFew p) {
+  typedef typename Operand<F16>::type V;
+  constexpr int RP = 32 * NC;
+  __shared__ float hs[16][RP + 1];
+  __shared__ __align__(16) uint16_t q[2][16][RP + 8];
+  __shared__ float se[16];
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t t0 = int64_t(blockIdx.y) * 16, N = p.w.N;
+  const int64_t n = int64_t(blockIdx.x) * 64 + 16 * wave + lr, nc = n < N ? n : N - 1;
+  const int r = p.s.r;
+  const int my = t0 + lr < p.T ? p.s.ids[t0 + lr] : -1;
+  uint32_t left = uint32_t(__ballot(my >= 0 && my < p.s.L)) & 0xFFFFu;
+  const uint32_t valid = left;
+
+  auto next = [&](int& a, uint32_t& mask) {
+    const int first = __builtin_ctz(left);
+    a = __builtin_amdgcn_readlane(my, first);
+    mask = uint32_t(__ballot(my == a)) & 0xFFFFu;
+    left &= ~mask;
+  };
+  auto load = [&](int a, uint4 (&u)[NC]) {
+    const uint16_t* row = p.s.B + (int64_t(a) * N + nc) * r;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int j = 32 * c + 8 * lg;
+      u[c] = *reinterpret_cast<const uint4*>(row + (j < r ? j : r - 8));
+    }
+  };
+  int a = -1;
+  uint32_t mask = 0;
+  uint4 u[NC];
+  if (left) {
+    next(a, mask);
+    load(a, u);
+  }
+  // the shared product
+  float y[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < p.S; ++s)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int64_t t = t0 + 4 * lg + v;
+      if (t < p.T) y[v] += p.partial[(int64_t(s) * p.T + t) * N + nc];
+    }
+  // h of the rows, and their 16-bit halves
+  for (int e = tid; e < 16 * RP; e += 64 * kFewWaves) {
+    const int i = e / RP, j = e % RP;
+    const int64_t t = t0 + i;
+    float h = 0.f;
+    if (((valid >> i) & 1u) && j < r)
+      for (int ks = 0; ks < p.S2; ++ks) h += p.hpart[(int64_t(ks) * p.T + t) * r + j];
+    hs[i][j] = h;
+    if (p.H && blockIdx.x == 0 && t < p.T && j < r) p.H[t * r + j] = h;
+  }
+  __syncthreads();
+  for (int i = wave; i < 16; i += kFewWaves) {
+    const int id = __builtin_amdgcn_readlane(my, i);
+    const float c = (valid >> i) & 1u ? p.s.scaling[id] : 0.f;
+    float m = 0.f;
+    for (int j = lane; j < RP; j += 64) m = fmaxf(m, fabsf(hs[i][j]));
+#pragma unroll
+    for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    const float cm = fabsf(c) * m;
+    int e = 0;
+    if (F16 && !(cm >= 0x1p-3f && cm < 0x1p14f)) e = exponent_of(cm);
+    const float down = exp2i(-e);
+    if (lane == 0) se[i] = exp2i(e);
+    for (int j = lane; j < RP; j += 64) {
+      const float s = c * hs[i][j] * down;
+      const uint16_t hi = round16<F16>(s);
+      q[0][i][j] = hi;
+      q[1][i][j] = round16<F16>(s - widen16<F16>(hi));
+    }
+  }
+  __syncthreads();
+  V qh[NC], ql[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    qh[c] = __builtin_bit_cast(V, *reinterpret_cast<const uint4*>(&q[0][lr][32 * c + 8 * lg]));
+    ql[c] = __builtin_bit_cast(V, *reinterpret_cast<const uint4*>(&q[1][lr][32 * c + 8 * lg]));
+  }
+  while (mask) {
+    uint4 un[NC];
+    int an = -1;
+    uint32_t mn = 0;
+    if (left) {
+      next(an, mn);
+      load(an, un);
+    }
+    floatx4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      d = mfma_16x16x32(qh[c], __builtin_bit_cast(V, u[c]), d);
+      d = mfma_16x16x32(ql[c], __builtin_bit_cast(V, u[c]), d);
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int i = 4 * lg + v;
+      const float add = F16 ? se[i] * d[v] : d[v];
+      y[v] = (mask >> i) & 1u ? y[v] + add : y[v];
+    }
+    a = an;
+    mask = mn;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) u[c] = un[c];
+  }
+  if (n < N)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int64_t t = t0 + 4 * lg + v;
+      if (t < p.T) p.Y[t * N + n] = round16<F16>(y[v]);
+    }
+}
+
+template <bool F16, int G>
+void launch_decode(const LoraFew& p, int downs, int gx, int gy, hipStream_t st) {
+  const unsigned grid = unsigned(downs + gx * gy);
+  if (p.T == 1) lora_decode_kernel<F16, G, 1><<<grid, 256, 0, st>>>(p, downs, gx, gy);
+  else if (p.T == 2) lora_decode_kernel<F16, G, 2><<<grid, 256, 0, st>>>(p, downs, gx, gy);
+  else lora_decode_kernel<F16, G, 4><<<grid, 256, 0, st>>>(p, downs, gx, gy);
+}
+
+template <bool F16>
+hipError_t launch_few(LoraFew p, hipStream_t st) {
+  const int jbs = (p.s.r + 15) / 16, rows = p.T < 16 ? int(p.T) : 16;
+  const int downs = int((p.T + 15) / 16) * rows * jbs * p.S2;
+  if (p.T <= 16 && p.gemv) {
+    const hipError_t e =
+        launch_w4a16_gemv(p.X, p.T, p.w.N, p.w.K, p.w.qweight, p.w.qzeros, p.w.scales,
+                          p.w.group, F16, p.kpw, p.partial, st);
+    if (e != hipSuccess) return e;
+    lora_few_down_kernel<F16><<<unsigned(downs), 256, 0, st>>>(p);
+  } else if (p.T <= 16) {
+    const int gx = int((p.w.N + kMgCols * 8 - 1) / (kMgCols * 8));
+    if (p.w.group == 32) launch_decode<F16, 32>(p, downs, gx, p.S, st);
+    else if (p.w.group == 64) launch_decode<F16, 64>(p, downs, gx, p.S, st);
+    else launch_decode<F16, 128>(p, downs, gx, p.S, st);
+  } else {
+    const unsigned grid = unsigned(downs + p.tiles * p.col_blocks * p.S);
+    if (p.T <= 32) lora_few_kernel<F16, 2><<<grid, 256, 0, st>>>(p, downs);
+    else lora_few_kernel<F16, 4><<<grid, 256, 0, st>>>(p, downs);
+  }
+  const dim3 grid(unsigned((p.w.N + 63) / 64), unsigned((p.T + 15) / 16));
+  if (p.s.r <= 32) lora_few_finish_kernel<F16, 1><<<grid, 256, 0, st>>>(p);
+  else if (p.s.r <= 64) lora_few_finish_kernel<F16, 2><<<grid, 256, 0, st>>>(p);
+  else lora_few_finish_kernel<F16, 4><<<grid, 256, 0, st>>>(p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_lora_few(const LoraFew& p, hipStream_t st) {
+  return p.f16 ? launch_few<true>(p, st) : launch_few<false>(p, st);
+}
+
+}  // namespace awq

@@ -500,10 +500,31 @@ LoraLayout lora_layout(int64_t T, int64_t N, int64_t K, int32_t, int32_t r) {
     off += align_up(bytes);
     return at;
   };
-  if (T <= kW4A16GemvMaxT) l.h = take(size_t(T) * size_t(r) * 4);
-  l.q = take(size_t(T) * size_t(lora_q_width(r)) * 2);
-  l.e = take(size_t(T) * 4);
-  l.wd = take(size_t(N) * size_t(K) * 2);
+  if (T <= kLoraFewMaxT) {
+    if (T <= kW4A16GemvMaxT && N % 16) {
+      l.kpw = w4a16_gemv_kpw(N, K);
+      l.S = w4a16_gemv_chunks(N, K);
+    } else if (T <= kW4A16GemvMaxT) {
+      l.kpw = w4a16_mgemv_kpw(N, K);
+      l.S = w4a16_mgemv_chunks(N, K);
+    } else {
+      // runs of k for two workgroups per CU, each wave with 128 rows or more
+      l.tiles = ceil_div(T, T <= 32 ? 32 : 64);
+      l.col_blocks = ceil_div(N, 128);
+      const int64_t runs = std::min(ceil_div(512, l.tiles * l.col_blocks), ceil_div(K, 512));
+      l.kpw = ceil_div(K, 4 * runs * 32) * 32;
+      l.S = ceil_div(K, 4 * l.kpw);
+    }
+    // runs of the narrow product: its workgroups read 128 rows or more per
+    // wave, and fewer runs with more tokens, whose second launch sums them
+    l.S2 = std::max<int64_t>(1, std::min<int64_t>({8, K / 1024, 256 / T}));
+    l.partial = take(size_t(l.S) * size_t(T) * size_t(N) * 4);
+    l.hpart = take(size_t(l.S2) * size_t(T) * size_t(r) * 4);
+  } else {
+    l.q = take(size_t(T) * size_t(lora_q_width(r)) * 2);
+    l.e = take(size_t(T) * 4);
+    l.wd = take(size_t(N) * size_t(K) * 2);
+  }
   l.total = off;
   return l;
 }
