@@ -386,25 +386,36 @@ def w4a16_matmul(X: torch.Tensor, qweight: torch.Tensor, qzeros: torch.Tensor,
 
 def _on_device_of(t: torch.Tensor):
     """Makes t's GPU the current one, so that the stream and the kernels are its."""
-    if t.device.index == torch.cuda.current_device():
+    if t.get_device() == torch.cuda.current_device():
         return contextlib.nullcontext()
     return torch.cuda.device(t.device)
 
 
-def _same_device(t: torch.Tensor, **others) -> None:
-    for name, o in others.items():
-        if o is not None and o.device != t.device:
-            raise ValueError(f"{name} is on {o.device}, not on {t.device}")
+def _check_on(device: int, **tensors) -> None:
+    """Each tensor (or None) is a contiguous one on GPU number ``device``."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.get_device() != device:
+            raise ValueError(f"{name} is on {t.device}, not on GPU {device}")
 
 
 def _out(t: Optional[torch.Tensor], shape, dtype, like: torch.Tensor, name: str) -> torch.Tensor:
     """The caller's output buffer, checked, or a new one."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=like.device)
-    _dev(t, name)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    _check_on(like.get_device(), **{name: t})
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name} must be {tuple(shape)} {dtype}")
     return t
+
+
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def w4a16_lora_workspace_bytes(T: int, N: int, K: int, L_: int, r: int,
@@ -422,11 +433,13 @@ def w4a16_lora_backward_workspace_bytes(T: int, N: int, K: int, L_: int, r: int,
 def _lora_args(V: torch.Tensor, V_cols: str, qweight, qzeros, scales, A, B, scaling, ids,
                group: int):
     """Checks what the forward and the backward call share; (T, N, K, L, r)."""
-    for t, name in ((V, V_cols), (qweight, "qweight"), (qzeros, "qzeros"), (scales, "scales"),
-                    (A, "A"), (B, "B"), (scaling, "scaling"), (ids, "ids")):
-        _dev(t, name)
-    _same_device(V, qweight=qweight, qzeros=qzeros, scales=scales, A=A, B=B, scaling=scaling,
-                 ids=ids)
+    _dev(V, V_cols)
+    _check_on(V.get_device(), qweight=qweight, qzeros=qzeros, scales=scales, A=A, B=B,
+              scaling=scaling, ids=ids)
+    for name, t in (("qweight", qweight), ("qzeros", qzeros), ("scales", scales), ("A", A),
+                    ("B", B), ("scaling", scaling), ("ids", ids)):
+        if t is None:
+            raise ValueError(f"{name} must be a GPU tensor")
     if V.dim() != 2 or qweight.dim() != 2 or scales.dim() != 2 or A.dim() != 3:
         raise ValueError(f"{V_cols}, qweight and scales must have 2 dimensions, A 3")
     T, K, N = V.shape[0], qweight.shape[0], scales.shape[1]
@@ -466,14 +479,15 @@ def w4a16_lora_matmul(X: torch.Tensor, qweight: torch.Tensor, qzeros: torch.Tens
     if x8 is not None:
         codes = _out(x8[0], (T, K), torch.int8, X, "x8 codes")
         steps = _out(x8[1], (T, K // 128), torch.float32, X, "x8 steps")
-    _same_device(X, out=Y, h=h, codes=codes, steps=steps, ws=ws)
+    if ws is None:
+        ws = _workspace(ws, w4a16_lora_workspace_bytes(T, N, K, n, r, X.dtype), X.device)
+    _check_on(X.get_device(), ws=ws)
     with _on_device_of(X):
-        if ws is None:
-            ws = _workspace(ws, w4a16_lora_workspace_bytes(T, N, K, n, r, X.dtype), X.device)
         L.check(L.lib().awq_w4a16_lora_matmul(
-            _ptr(X), _dtype(X), T, N, K, _ptr(qweight), _ptr(qzeros), _ptr(scales), int(group),
-            _ptr(A), _ptr(B), _ptr(scaling), _ptr(ids), n, r, _ptr(Y), _ptr(h), _ptr(codes),
-            _ptr(steps), _ptr(ws), ws.numel() * ws.element_size(), _stream()))
+            X.data_ptr(), _dtype(X), T, N, K, qweight.data_ptr(), qzeros.data_ptr(),
+            scales.data_ptr(), int(group), A.data_ptr(), B.data_ptr(), scaling.data_ptr(),
+            ids.data_ptr(), n, r, Y.data_ptr(), _at(h), _at(codes), _at(steps), ws.data_ptr(),
+            ws.numel() * ws.element_size(), torch.cuda.current_stream().cuda_stream))
     return Y
 
 
@@ -491,29 +505,34 @@ def w4a16_lora_backward(dY: torch.Tensor, X, h: torch.Tensor, qweight: torch.Ten
     if isinstance(X, (tuple, list)):
         X, steps = X
         _dev(steps, "steps")
+        _dev(X, "X")
         if X.dtype != torch.int8 or steps.dtype != torch.float32 or steps.shape != (T, K // 128):
             raise ValueError("a checkpoint is (codes [T, K] int8, steps [T, K / 128] float32)")
-    elif X.dtype != dY.dtype:
-        raise ValueError("X must share dY's dtype or be a checkpoint")
-    _dev(X, "X")
+    else:
+        _dev(X, "X")
+        if X.dtype != dY.dtype:
+            raise ValueError("X must share dY's dtype or be a checkpoint")
     if X.shape != (T, K):
         raise ValueError("X must be [T, K]")
     _dev(h, "h")
-    _out(h, (T, r), torch.float32, dY, "h")
+    _check_on(dY.get_device(), X=X, steps=steps, h=h)
+    if h.shape != (T, r) or h.dtype != torch.float32:
+        raise ValueError("h must be [T, r] float32")
     dX, dA, dB = out if out is not None else (None, None, None)
     dX = _out(dX, (T, K), dY.dtype, dY, "dX") if want_dx else None
     dA = _out(dA, (n, r, K), dY.dtype, dY, "dA")
     dB = _out(dB, (n, N, r), dY.dtype, dY, "dB")
-    _same_device(dY, X=X, steps=steps, h=h, dX=dX, dA=dA, dB=dB, ws=ws)
+    if ws is None:
+        ws = _workspace(ws, w4a16_lora_backward_workspace_bytes(T, N, K, n, r, dY.dtype),
+                        dY.device)
+    _check_on(dY.get_device(), ws=ws)
     with _on_device_of(dY):
-        if ws is None:
-            ws = _workspace(ws, w4a16_lora_backward_workspace_bytes(T, N, K, n, r, dY.dtype),
-                            dY.device)
         L.check(L.lib().awq_w4a16_lora_backward(
-            _ptr(dY), _ptr(X), _ptr(steps), _ptr(h), _dtype(dY), T, N, K, _ptr(qweight),
-            _ptr(qzeros), _ptr(scales), int(group), _ptr(A), _ptr(B), _ptr(scaling), _ptr(ids),
-            n, r, _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel() * ws.element_size(),
-            _stream()))
+            dY.data_ptr(), X.data_ptr(), _at(steps), h.data_ptr(), _dtype(dY), T, N, K,
+            qweight.data_ptr(), qzeros.data_ptr(), scales.data_ptr(), int(group), A.data_ptr(),
+            B.data_ptr(), scaling.data_ptr(), ids.data_ptr(), n, r, _at(dX), dA.data_ptr(),
+            dB.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+            torch.cuda.current_stream().cuda_stream))
     return dX, dA, dB
 
 
@@ -526,10 +545,10 @@ def act_pack8(X: torch.Tensor, out=None):
     codes, steps = out if out is not None else (None, None)
     codes = _out(codes, (T, K), torch.int8, X, "codes")
     steps = _out(steps, (T, K // 128), torch.float32, X, "steps")
-    _same_device(X, codes=codes, steps=steps)
     with _on_device_of(X):
-        L.check(L.lib().awq_act_pack8(_ptr(X), _dtype(X), T, K, _ptr(codes), _ptr(steps),
-                                      _stream()))
+        L.check(L.lib().awq_act_pack8(X.data_ptr(), _dtype(X), T, K, codes.data_ptr(),
+                                      steps.data_ptr(),
+                                      torch.cuda.current_stream().cuda_stream))
     return codes, steps
 
 
@@ -542,10 +561,10 @@ def act_unpack8(codes: torch.Tensor, steps: torch.Tensor, dtype: torch.dtype,
     if codes.dtype != torch.int8 or steps.dtype != torch.float32 or steps.shape != (T, K // 128):
         raise ValueError("a checkpoint is (codes [T, K] int8, steps [T, K / 128] float32)")
     X = _out(out, (T, K), dtype, codes, "out")
-    _same_device(codes, steps=steps, out=X)
+    _check_on(codes.get_device(), steps=steps)
     with _on_device_of(codes):
-        L.check(L.lib().awq_act_unpack8(_ptr(codes), _ptr(steps), _dtype(X), T, K, _ptr(X),
-                                        _stream()))
+        L.check(L.lib().awq_act_unpack8(codes.data_ptr(), steps.data_ptr(), _dtype(X), T, K,
+                                        X.data_ptr(), torch.cuda.current_stream().cuda_stream))
     return X
 
 

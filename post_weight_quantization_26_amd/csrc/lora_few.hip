@@ -148,13 +148,13 @@ __device__ __forceinline__ void few_block(const FewSlot<MT>& sl, floatx4 (&acc)[
   }
   // (two operands at a time: all eight at once would spill)
   AWQ_FEW_NIBBLE(0) AWQ_FEW_NIBBLE(1)
-  __builtin_amdgcn_sched_barrier(0);
+
   AWQ_FEW_NIBBLE(2) AWQ_FEW_NIBBLE(3)
-  __builtin_amdgcn_sched_barrier(0);
+
   AWQ_FEW_NIBBLE(4) AWQ_FEW_NIBBLE(5)
-  __builtin_amdgcn_sched_barrier(0);
+
   AWQ_FEW_NIBBLE(6) AWQ_FEW_NIBBLE(7)
-  __builtin_amdgcn_sched_barrier(0);
+
 #undef AWQ_FEW_NIBBLE
 }
 
@@ -184,12 +184,15 @@ __device__ __forceinline__ void few_product(const LoraFew& p, int id, int blocks
   // lanes past N read column 0, token rows past T the last one: neither is
   // ever stored, and no MFMA row or column depends on another
   const int64_t col = n0 / 8 + lr < N8 ? n0 / 8 + lr : 0;
-  const int32_t* qw = p.w.qweight + int64_t(8 * lg) * N8 + col;
-  const uint16_t* xr[MT];
+  // 32-bit lane offsets (bytes) from bases common to the wave: 8·lg + col / ..
+  // rows of the packed words (K < 2^22, N·K <= 2^34), at most 256 tokens of X
+  const uint32_t qoff = uint32_t((int64_t(8 * lg) * N8 + col) * 4);
+  const uint32_t zoff = uint32_t(col * 4), soff = uint32_t(col * 16);
+  uint32_t xoff[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int64_t t = t0 + 16 * m + lr;
-    xr[m] = p.X + (t < p.T ? t : p.T - 1) * K + 8 * lg;
+    xoff[m] = uint32_t(((t < p.T ? t : p.T - 1) * K + 8 * lg) * 2);
   }
   floatx4 acc[8][MT];
 #pragma unroll
@@ -197,23 +200,27 @@ __device__ __forceinline__ void few_product(const LoraFew& p, int id, int blocks
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[r][m] = floatx4{0.f, 0.f, 0.f, 0.f};
   if (kw0 < kw1) {
-    // blocks past the wave's last one read it again
+    // (kpw and K are multiples of 64) blocks past the wave's last one read it again
     auto load = [&](FewSlot<MT>& sl, int kb) {
       const int k = kb < kw1 ? kb : kw1 - 32;
-      const int g = (k + 8 * lg) >> p.gshift;
+      const int g = k >> p.gshift;
+      const char* q = reinterpret_cast<const char*>(p.w.qweight) + int64_t(k) * N8 * 4;
+      const char* x = reinterpret_cast<const char*>(p.X) + int64_t(k) * 2;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sl.w[e] = uint32_t(qw[int64_t(k + e) * N8]);
+      for (int e = 0; e < 8; ++e)
+        sl.w[e] = *reinterpret_cast<const uint32_t*>(q + int64_t(e) * N8 * 4 + qoff);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) sl.x[m] = *reinterpret_cast<const uint4*>(xr[m] + k);
-      sl.z = uint32_t(p.w.qzeros[int64_t(g) * N8 + col]);
-      sl.s = *reinterpret_cast<const uint4*>(p.w.scales + int64_t(g) * N + 8 * col);
+      for (int m = 0; m < MT; ++m) sl.x[m] = *reinterpret_cast<const uint4*>(x + xoff[m]);
+      sl.z = *reinterpret_cast<const uint32_t*>(
+          reinterpret_cast<const char*>(p.w.qzeros) + int64_t(g) * N8 * 4 + zoff);
+      sl.s = *reinterpret_cast<const uint4*>(
+          reinterpret_cast<const char*>(p.w.scales) + int64_t(g) * N * 2 + soff);
     };
     FewSlot<MT> a, b;
     load(a, kw0);
     for (int kb = kw0; kb < kw1; kb += 64) {
       load(b, kb + 32);
       few_block<F16, MT>(a, acc);
-      if (kb + 32 >= kw1) break;
       load(a, kb + 64);
       few_block<F16, MT>(b, acc);
     }
@@ -287,72 +294,110 @@ __global__ __launch_bounds__(64 * kFewWaves) void lora_few_down_kernel(LoraFew p
 // launch 2
 // ---------------------------------------------------------------------------
 
-// Workgroup: 64 outputs x 16 tokens, a wave 16 outputs. NC·32 >= r. The rows'
-// h (summed over the runs of k) become two 16-bit halves in LDS, as in
-// lora_down.hip, and each adapter among the rows takes one pass of MFMAs whose
-// rows are kept where they belong to it. The next adapter's B is loaded while
-// the current one is used.
+// Workgroup: 32 outputs x 16 tokens. NC·32 >= r. Its 4 waves share the work
+// by reads, not by outputs: each takes every fourth run of partial sums and
+// every fourth adapter among the rows, with all their loads in flight, and
+// they add up in LDS in order. The rows' h (summed over the runs of k) become
+// two 16-bit halves in LDS, as in lora_down.hip; an adapter takes one pass of
+// MFMAs whose rows are kept where they belong to it.
+constexpr int kFinishCols = 32;
+
 template <bool F16, int NC>
 __global__ __launch_bounds__(64 * kFewWaves) void lora_few_finish_kernel(LoraFew p) {
   typedef typename Operand<F16>::type V;
-  constexpr int RP = 32 * NC;
-  __shared__ float hs[16][RP + 1];
+  constexpr int RP = 32 * NC, NB = NC == 4 ? 2 : 4;   // adapters in flight per wave
+  __shared__ union {
+    float h[16][RP + 1];
+    float y[kFewWaves][16][kFinishCols + 1];
+  } sm;
   __shared__ __align__(16) uint16_t q[2][16][RP + 8];
   __shared__ float se[16];
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t t0 = int64_t(blockIdx.y) * 16, N = p.w.N;
-  const int64_t n = int64_t(blockIdx.x) * 64 + 16 * wave + lr, nc = n < N ? n : N - 1;
+  const int64_t t0 = int64_t(blockIdx.y) * 16, N = p.w.N, n0 = int64_t(blockIdx.x) * kFinishCols;
   const int r = p.s.r;
   const int my = t0 + lr < p.T ? p.s.ids[t0 + lr] : -1;
-  uint32_t left = uint32_t(__ballot(my >= 0 && my < p.s.L)) & 0xFFFFu;
-  const uint32_t valid = left;
-
-  auto next = [&](int& a, uint32_t& mask) {
-    const int first = __builtin_ctz(left);
-    a = __builtin_amdgcn_readlane(my, first);
-    mask = uint32_t(__ballot(my == a)) & 0xFFFFu;
-    left &= ~mask;
-  };
-  auto load = [&](int a, uint4 (&u)[NC]) {
-    const uint16_t* row = p.s.B + (int64_t(a) * N + nc) * r;
+  const uint32_t valid = uint32_t(__ballot(my >= 0 && my < p.s.L)) & 0xFFFFu;
+  int64_t col[2];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int j = 32 * c + 8 * lg;
-      u[c] = *reinterpret_cast<const uint4*>(row + (j < r ? j : r - 8));
-    }
-  };
-  int a = -1;
-  uint32_t mask = 0;
-  uint4 u[NC];
-  if (left) {
-    next(a, mask);
-    load(a, u);
+  for (int c = 0; c < 2; ++c) {
+    const int64_t n = n0 + 16 * c + lr;
+    col[c] = n < N ? n : N - 1;
   }
-  // the shared product
-  float y[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < p.S; ++s)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int64_t t = t0 + 4 * lg + v;
-      if (t < p.T) y[v] += p.partial[(int64_t(s) * p.T + t) * N + nc];
+
+  // this wave's next adapters (every fourth distinct one) and their rows; mask
+  // 0 when there are none left
+  uint32_t left = valid;
+  int turn = 0;
+  auto next = [&](int& a, uint32_t& mask) {
+    a = 0;
+    mask = 0;
+    while (left) {
+      const int id = __builtin_amdgcn_readlane(my, __builtin_ctz(left));
+      const uint32_t m = uint32_t(__ballot(my == id)) & 0xFFFFu;
+      left &= ~m;
+      if ((turn++ & (kFewWaves - 1)) == wave) {
+        a = id;
+        mask = m;
+        return;
+      }
     }
-  // h of the rows, and their 16-bit halves
+  };
+  int a[NB];
+  uint32_t mask[NB];
+  uint4 u[NB][2][NC];
+  auto load = [&] {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      next(a[b], mask[b]);
+      if (!mask[b]) continue;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const uint16_t* row = p.s.B + (int64_t(a[b]) * N + col[c]) * r;
+#pragma unroll
+        for (int k = 0; k < NC; ++k) {
+          const int j = 32 * k + 8 * lg;
+          u[b][c][k] = *reinterpret_cast<const uint4*>(row + (j < r ? j : r - 8));
+        }
+      }
+    }
+  };
+  load();
+  // h of the rows
   for (int e = tid; e < 16 * RP; e += 64 * kFewWaves) {
     const int i = e / RP, j = e % RP;
     const int64_t t = t0 + i;
     float h = 0.f;
-    if (((valid >> i) & 1u) && j < r)
-      for (int ks = 0; ks < p.S2; ++ks) h += p.hpart[(int64_t(ks) * p.T + t) * r + j];
-    hs[i][j] = h;
+    if (((valid >> i) & 1u) && j < r) {
+      const float* src = p.hpart + t * r + j;
+#pragma unroll 4
+      for (int ks = 0; ks < p.S2; ++ks) h += src[int64_t(ks) * p.T * r];
+    }
+    sm.h[i][j] = h;
     if (p.H && blockIdx.x == 0 && t < p.T && j < r) p.H[t * r + j] = h;
+  }
+  // this wave's runs of the shared product (rows past T read the last one)
+  float y[2][4] = {};
+  {
+    const float* src[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int64_t t = t0 + 4 * lg + v;
+      src[v] = p.partial + (t < p.T ? t : p.T - 1) * N;
+    }
+#pragma unroll 4
+    for (int s = wave; s < p.S; s += kFewWaves)
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) y[c][v] += src[v][int64_t(s) * p.T * N + col[c]];
   }
   __syncthreads();
   for (int i = wave; i < 16; i += kFewWaves) {
     const int id = __builtin_amdgcn_readlane(my, i);
     const float c = (valid >> i) & 1u ? p.s.scaling[id] : 0.f;
     float m = 0.f;
-    for (int j = lane; j < RP; j += 64) m = fmaxf(m, fabsf(hs[i][j]));
+    for (int j = lane; j < RP; j += 64) m = fmaxf(m, fabsf(sm.h[i][j]));
 #pragma unroll
     for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
     const float cm = fabsf(c) * m;
@@ -361,7 +406,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void lora_few_finish_kernel(LoraFew
     const float down = exp2i(-e);
     if (lane == 0) se[i] = exp2i(e);
     for (int j = lane; j < RP; j += 64) {
-      const float s = c * hs[i][j] * down;
+      const float s = c * sm.h[i][j] * down;
       const uint16_t hi = round16<F16>(s);
       q[0][i][j] = hi;
       q[1][i][j] = round16<F16>(s - widen16<F16>(hi));
@@ -370,41 +415,44 @@ __global__ __launch_bounds__(64 * kFewWaves) void lora_few_finish_kernel(LoraFew
   __syncthreads();
   V qh[NC], ql[NC];
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    qh[c] = __builtin_bit_cast(V, *reinterpret_cast<const uint4*>(&q[0][lr][32 * c + 8 * lg]));
-    ql[c] = __builtin_bit_cast(V, *reinterpret_cast<const uint4*>(&q[1][lr][32 * c + 8 * lg]));
+  for (int k = 0; k < NC; ++k) {
+    qh[k] = __builtin_bit_cast(V, *reinterpret_cast<const uint4*>(&q[0][lr][32 * k + 8 * lg]));
+    ql[k] = __builtin_bit_cast(V, *reinterpret_cast<const uint4*>(&q[1][lr][32 * k + 8 * lg]));
   }
-  while (mask) {
-    uint4 un[NC];
-    int an = -1;
-    uint32_t mn = 0;
-    if (left) {
-      next(an, mn);
-      load(an, un);
-    }
-    floatx4 d = {0.f, 0.f, 0.f, 0.f};
+  while (true) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      d = mfma_16x16x32(qh[c], __builtin_bit_cast(V, u[c]), d);
-      d = mfma_16x16x32(ql[c], __builtin_bit_cast(V, u[c]), d);
-    }
+    for (int b = 0; b < NB; ++b) {
+      if (!mask[b]) continue;
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int i = 4 * lg + v;
-      const float add = F16 ? se[i] * d[v] : d[v];
-      y[v] = (mask >> i) & 1u ? y[v] + add : y[v];
-    }
-    a = an;
-    mask = mn;
+      for (int c = 0; c < 2; ++c) {
+        floatx4 d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int c = 0; c < NC; ++c) u[c] = un[c];
+        for (int k = 0; k < NC; ++k) {
+          d = mfma_16x16x32(qh[k], __builtin_bit_cast(V, u[b][c][k]), d);
+          d = mfma_16x16x32(ql[k], __builtin_bit_cast(V, u[b][c][k]), d);
+        }
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int i = 4 * lg + v;
+          const float add = F16 ? se[i] * d[v] : d[v];
+          y[c][v] = (mask[b] >> i) & 1u ? y[c][v] + add : y[c][v];
+        }
+      }
+    }
+    if (!left) break;
+    load();
   }
-  if (n < N)
+  // (every wave has read sm.h: the barrier above)
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int64_t t = t0 + 4 * lg + v;
-      if (t < p.T) p.Y[t * N + n] = round16<F16>(y[v]);
-    }
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) sm.y[wave][4 * lg + v][16 * c + lr] = y[c][v];
+  __syncthreads();
+  for (int e = tid; e < 16 * kFinishCols; e += 64 * kFewWaves) {
+    const int i = e / kFinishCols, c = e % kFinishCols;
+    const float s = ((sm.y[0][i][c] + sm.y[1][i][c]) + sm.y[2][i][c]) + sm.y[3][i][c];
+    if (t0 + i < p.T && n0 + c < N) p.Y[(t0 + i) * N + n0 + c] = round16<F16>(s);
+  }
 }
 
 template <bool F16, int G>
@@ -435,7 +483,7 @@ hipError_t launch_few(LoraFew p, hipStream_t st) {
     if (p.T <= 32) lora_few_kernel<F16, 2><<<grid, 256, 0, st>>>(p, downs);
     else lora_few_kernel<F16, 4><<<grid, 256, 0, st>>>(p, downs);
   }
-  const dim3 grid(unsigned((p.w.N + 63) / 64), unsigned((p.T + 15) / 16));
+  const dim3 grid(unsigned((p.w.N + kFinishCols - 1) / kFinishCols), unsigned((p.T + 15) / 16));
   if (p.s.r <= 32) lora_few_finish_kernel<F16, 1><<<grid, 256, 0, st>>>(p);
   else if (p.s.r <= 64) lora_few_finish_kernel<F16, 2><<<grid, 256, 0, st>>>(p);
   else lora_few_finish_kernel<F16, 4><<<grid, 256, 0, st>>>(p);

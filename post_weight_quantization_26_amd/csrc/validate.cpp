@@ -512,7 +512,7 @@ LoraLayout lora_layout(int64_t T, int64_t N, int64_t K, int32_t, int32_t r) {
       l.tiles = ceil_div(T, T <= 32 ? 32 : 64);
       l.col_blocks = ceil_div(N, 128);
       const int64_t runs = std::min(ceil_div(512, l.tiles * l.col_blocks), ceil_div(K, 512));
-      l.kpw = ceil_div(K, 4 * runs * 32) * 32;
+      l.kpw = ceil_div(K, 4 * runs * 64) * 64;
       l.S = ceil_div(K, 4 * l.kpw);
     }
     // runs of the narrow product: its workgroups read 128 rows or more per
