@@ -18,6 +18,20 @@ __device__ __forceinline__ float widen16(uint16_t h) {
   else return bf16_to_f32(h);
 }
 
+// Two float32 values rounded to nearest even into a packed 16-bit pair, low
+// half first, by a vector conversion, which is one instruction (two casts
+// are four). Not inline asm: the compiler would put no wait states between
+// that and an MFMA that reads the result.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 b16x2 __attribute__((ext_vector_type(2)));
+  typedef _Float16 h16x2 __attribute__((ext_vector_type(2)));
+  const f32x2 v = {a, b};
+  if constexpr (F16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, h16x2));
+  else return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, b16x2));
+}
+
 // The least id of this wave's lanes that is above `prev` and below L, or L
 // when there is none (ids < 0 never count: prev starts at -1). The same value
 // in every lane; `id2` is a second id of the lane (or -1).

@@ -104,10 +104,11 @@ struct FewSlot {
 // The MFMA operand of nibble R: its 8 codes, one per word, as rounded Ŵ.
 template <bool F16, int R>
 __device__ __forceinline__ uint4 few_operand(const uint32_t (&w)[8], uint32_t z,
-                                             const uint32_t (&sw)[4]) {
+                                             const uint32_t (&sw)[4],
+                                             const uint32_t (&base)[2]) {
   constexpr uint32_t kSel = 0x0C000C00u | uint32_t(4 + R / 2) << 16 | uint32_t(R / 2);
   constexpr uint32_t kMask = R & 1 ? 0x00F000F0u : 0x000F000Fu;
-  constexpr uint32_t kBase = R & 1 ? 0x54005400u : 0x64006400u;   // fp16 64 and 1024
+  const uint32_t kBase = base[R & 1];
   const f16x2_t zb =
       __builtin_bit_cast(f16x2_t, (__builtin_amdgcn_perm(z, z, kSel) & kMask) | kBase);
   const _Float16 sc =
@@ -130,23 +131,23 @@ __device__ __forceinline__ uint4 few_operand(const uint32_t (&w)[8], uint32_t z,
           f16x2_t, (__builtin_amdgcn_perm(w[2 * e + 1], w[2 * e], kSel) & kMask) | kBase);
       const float lo = __builtin_fmaf(float(q[0]), float(sc), nzs);
       const float hi = __builtin_fmaf(float(q[1]), float(sc), nzs);
-      out[e] = uint32_t(round16<false>(lo)) | uint32_t(round16<false>(hi)) << 16;
+      out[e] = pack2<false>(lo, hi);
     }
   }
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
 template <bool F16, int MT>
-__device__ __forceinline__ void few_block(const FewSlot<MT>& sl, floatx4 (&acc)[8][MT]) {
+__device__ __forceinline__ void few_block(const FewSlot<MT>& sl, const uint32_t (&base)[2],
+                                          floatx4 (&acc)[8][MT]) {
   typedef typename Operand<F16>::type V;
   const uint32_t sw[4] = {sl.s.x, sl.s.y, sl.s.z, sl.s.w};
 #define AWQ_FEW_NIBBLE(R)                                                              \
   {                                                                                    \
-    const V b = __builtin_bit_cast(V, few_operand<F16, R>(sl.w, sl.z, sw));            \
+    const V b = __builtin_bit_cast(V, few_operand<F16, R>(sl.w, sl.z, sw, base));            \
     for (int m = 0; m < MT; ++m)                                                       \
       acc[R][m] = mfma_16x16x32(__builtin_bit_cast(V, sl.x[m]), b, acc[R][m]);         \
   }
-  // (two operands at a time: all eight at once would spill)
   AWQ_FEW_NIBBLE(0) AWQ_FEW_NIBBLE(1)
 
   AWQ_FEW_NIBBLE(2) AWQ_FEW_NIBBLE(3)
@@ -216,13 +217,17 @@ __device__ __forceinline__ void few_product(const LoraFew& p, int id, int blocks
       sl.s = *reinterpret_cast<const uint4*>(
           reinterpret_cast<const char*>(p.w.scales) + int64_t(g) * N * 2 + soff);
     };
+    // fp16 1024 and 64, opaque so that they stay in registers (with the mask in
+    // a scalar one, and-or is one instruction)
+    uint32_t base[2] = {0x64006400u, 0x54005400u};
+    asm volatile("" : "+v"(base[0]), "+v"(base[1]));
     FewSlot<MT> a, b;
     load(a, kw0);
     for (int kb = kw0; kb < kw1; kb += 64) {
       load(b, kb + 32);
-      few_block<F16, MT>(a, acc);
+      few_block<F16, MT>(a, base, acc);
       load(a, kb + 64);
-      few_block<F16, MT>(b, acc);
+      few_block<F16, MT>(b, base, acc);
     }
   }
   // lane l holds outputs 8·(l % 16) + r, tokens 16·m + 4·(l / 16) + v

@@ -35,11 +35,6 @@ constexpr int kGradStrip = 128;
 
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 
-template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  return uint32_t(round16<F16>(a)) | uint32_t(round16<F16>(b)) << 16;
-}
-
 // MF: fp16 matrix-core operands (fp16 Z, or 8-bit codes); else bf16.
 template <bool F16, bool X8, int JB>
 __device__ __forceinline__ void grad_piece(const LoraGrad& p, const LoraPiece& pc, bool is_a,

@@ -161,7 +161,7 @@ __device__ __forceinline__ void dequant_t(const LoraPrep& p, int64_t i) {
     for (int r = 0; r < 4; ++r) {
       const float a = (float((w[e] >> (8 * r)) & 15u) - zf[2 * r]) * sc[2 * r];
       const float b = (float((w[e] >> (8 * r + 4)) & 15u) - zf[2 * r + 1]) * sc[2 * r + 1];
-      h[r] = uint32_t(round16<F16>(a)) | uint32_t(round16<F16>(b)) << 16;
+      h[r] = pack2<F16>(a, b);
     }
     *reinterpret_cast<uint4*>(out + e * p.Np) = make_uint4(h[0], h[1], h[2], h[3]);
   }

@@ -511,7 +511,8 @@ LoraLayout lora_layout(int64_t T, int64_t N, int64_t K, int32_t, int32_t r) {
       // runs of k for two workgroups per CU, each wave with 128 rows or more
       l.tiles = ceil_div(T, T <= 32 ? 32 : 64);
       l.col_blocks = ceil_div(N, 128);
-      const int64_t runs = std::min(ceil_div(512, l.tiles * l.col_blocks), ceil_div(K, 512));
+      const int64_t runs = std::max<int64_t>(
+          1, std::min(512 / (l.tiles * l.col_blocks), ceil_div(K, 512)));
       l.kpw = ceil_div(K, 4 * runs * 64) * 64;
       l.S = ceil_div(K, 4 * l.kpw);
     }
