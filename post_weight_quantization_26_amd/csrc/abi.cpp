@@ -798,6 +798,8 @@ extern "C" awq_status awq_w4a16_lora_matmul(
   d.L = L;
   d.r = r;
   d.f16 = f16;
+  d.S = int(l.runs);
+  d.part = at<float>(ws, l.part);
   d.H = H;
   d.Q = at<uint16_t>(ws, l.q);
   d.RW = lora_q_width(r);
@@ -865,6 +867,8 @@ extern "C" awq_status awq_w4a16_lora_backward(
   d.L = L;
   d.r = r;
   d.f16 = f16;
+  d.S = int(l.runs);
+  d.part = at<float>(ws, l.part);
   d.Pt = at<float>(ws, l.gt);
   d.row_max = at<float>(ws, l.gmax);
   d.pos = pr.pos;

@@ -48,6 +48,17 @@ __device__ __forceinline__ uint2 act8_codes(const float (&x)[8], const Act8Scale
   return make_uint2(w[0], w[1]);
 }
 
+// max of m over the 16 lanes of a DPP row, in every lane
+__device__ __forceinline__ uint32_t row16_max(uint32_t m) {
+  uint32_t u;
+#define AWQ_ROR_MAX(N)                                                              \
+  u = uint32_t(__builtin_amdgcn_update_dpp(0, int(m), 0x120 + N, 0xF, 0xF, false)); \
+  m = m > u ? m : u;
+  AWQ_ROR_MAX(8) AWQ_ROR_MAX(4) AWQ_ROR_MAX(2) AWQ_ROR_MAX(1)
+#undef AWQ_ROR_MAX
+  return m;
+}
+
 // 8 channels of a block whose largest |x| `reduce` finds over its lanes.
 template <class Reduce>
 __device__ __forceinline__ Act8 act8_block(const float (&x)[8], const Reduce& reduce) {

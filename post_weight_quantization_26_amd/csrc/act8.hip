@@ -19,17 +19,6 @@ namespace {
 // kActUnroll such pieces a workgroup apart, all loaded before any is used.
 constexpr int kActUnroll = 4;
 
-// max of m over the 16 lanes of a DPP row, in every lane
-__device__ __forceinline__ uint32_t row16_max(uint32_t m) {
-  uint32_t u;
-#define AWQ_ROR_MAX(N)                                                              \
-  u = uint32_t(__builtin_amdgcn_update_dpp(0, int(m), 0x120 + N, 0xF, 0xF, false)); \
-  m = m > u ? m : u;
-  AWQ_ROR_MAX(8) AWQ_ROR_MAX(4) AWQ_ROR_MAX(2) AWQ_ROR_MAX(1)
-#undef AWQ_ROR_MAX
-  return m;
-}
-
 template <int DT>
 __device__ __forceinline__ void store8(void* X, int64_t i, const float (&v)[8]) {
   if constexpr (DT == 0) {

@@ -215,6 +215,8 @@ struct LoraLayout {
   size_t partial; // few tokens: [S, T, N] f32 sums of the shared product, ..
   size_t hpart;   // .. and [S2, T, r] f32 of the narrow one
   int64_t S, S2, kpw, tiles, col_blocks;
+  size_t part;    // otherwise: [runs, T, r] f32 sums of the narrow product,
+  int64_t runs;
   size_t q;       // [T, lora_q_width(r)] 16-bit
   size_t e;       // [T] f32
   size_t wd;      // [N, K] 16-bit dequantised layer
@@ -227,7 +229,8 @@ struct LoraBackwardLayout {
   int64_t Np, Tp;             // N padded to 128; sorted positions
   int64_t piece, pieces, slots;
   size_t wt, bt, at, dyp;     // 16-bit: Ŵᵀ [K, Np], Bᵀ [L, r, Np], Aᵀ [L, K, r], dY [T, Np]
-  size_t q, e;                // as in LoraLayout
+  int64_t runs;
+  size_t part, q, e;          // as in LoraLayout
   size_t gt, ht, gmax, hmax;  // f32: [r, Tp] twice, [Tp] twice
   size_t token, pos, table, n_pieces, n_slots, first_slot, last_pos;
   size_t partial;             // f32 [slots, (K + N)·r]

@@ -32,10 +32,14 @@ struct LoraDown {
   const float* scaling;
   const int32_t* ids;
   int64_t T, C, ldv, ldm; // C a multiple of 128
-  int L, r, f16;
+  int L, r, f16, S;       // S: runs of the contraction
+  float* part;            // [S, T, r] their sums
   float* H;               // [T, r] or NULL; rows without an adapter get zeros
+  const float* Hin;       // [T, r], with Pt
   float* Pt;              // [r, ldp] transposed, token t at column pos[t], or NULL
-  float* row_max;         // [ldp] max_j |P| at pos[t] (with Pt)
+  float* Ht;              // Hin likewise
+  float* row_max;         // [ldp] max_j |P| at pos[t]
+  float* h_max;           // [ldp] max_j |Hin|
   const int32_t* pos;
   int64_t ldp;
   uint16_t* Q;            // [T, RW]: c·P as halves hi [r], lo [r], zeros up to RW
@@ -43,9 +47,6 @@ struct LoraDown {
   float* E;               // [T] the power of two that Q is scaled down by
   int8_t* codes;          // [T, C] 8-bit checkpoint of V, or NULL
   float* steps;           // [T, C / 128]
-  const float* Hin;       // [T, r] to lay out as Pt into Ht and h_max, or NULL
-  float* Ht;
-  float* h_max;
 };
 hipError_t launch_lora_down(const LoraDown& p, hipStream_t st);
 

@@ -25,6 +25,7 @@
 #include "gemm_types.h"
 #include "lora.h"
 #include "lora_common.h"
+#include "lora_stage.h"
 #include "w4a16_mgemv.h"
 
 namespace awq {
@@ -32,6 +33,16 @@ namespace {
 
 constexpr int kFewWaves = 4;
 constexpr int kFewCols = 128;     // outputs per workgroup (T > 16)
+
+// Keeps memory operations and instructions on their side of it.
+__device__ __forceinline__ void fence() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ void wait_lds() {   // lgkmcnt(0)
+  __builtin_amdgcn_s_waitcnt(0xF | (3 << 14) | (0x7 << 4));
+}
 
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 
@@ -53,35 +64,57 @@ __device__ __forceinline__ void few_down_index(const LoraFew& p, int id, int& ti
   tile = id / rows;
 }
 
+// Per wave and stage: a 16-row tile of X and one of A (lora_stage.h).
+typedef uint4 FewStage[kFewWaves][2][kTile16];
+
 template <bool F16>
-__device__ __forceinline__ void few_down(const LoraFew& p, int id, float (*red)[16][17]) {
+__device__ __forceinline__ void few_down(const LoraFew& p, int id, FewStage& s0, FewStage& s1) {
   typedef typename Operand<F16>::type V;
   int tile, row, jb, ks;
   few_down_index(p, id, tile, row, jb, ks);
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
-  const int64_t t0 = int64_t(tile) * 16, t = t0 + lr, K = p.w.K;
-  const int my = t < p.T ? p.s.ids[t] : -1;
+  const int64_t t0 = int64_t(tile) * 16, K = p.w.K;
+  const int my = t0 + lr < p.T ? p.s.ids[t0 + lr] : -1;
   const int a = __builtin_amdgcn_readlane(my, row);
   const uint32_t mine = uint32_t(__ballot(my == a)) & 0xFFFFu;
   if (a < 0 || a >= p.s.L || int(__builtin_ctz(mine)) != row) return;
   const int nb = int(K / 128), b0 = int(int64_t(nb) * ks / p.S2),
             b1 = int(int64_t(nb) * (ks + 1) / p.S2);
-  const int j = 16 * jb + lr;
-  const uint16_t* xr = p.X + (t < p.T ? t : p.T - 1) * K + 8 * lg;
-  const uint16_t* ar = p.s.A + (int64_t(a) * p.s.r + (j < p.s.r ? j : p.s.r - 1)) * K + 8 * lg;
-  floatx4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int b = b0 + wave; b < b1; b += kFewWaves) {
-    uint4 x[4], w[4];
+  const int64_t rows = p.T - t0 < 16 ? p.T - t0 : 16;
+  const int ranks = p.s.r - 16 * jb < 16 ? p.s.r - 16 * jb : 16;
+  const auto rsX = rows_rsrc(p.X + t0 * K, rows, K);
+  const auto rsA = rows_rsrc(p.s.A + (int64_t(a) * p.s.r + 16 * jb) * K, ranks, K);
+  uint32_t off[4];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      x[s] = *reinterpret_cast<const uint4*>(xr + int64_t(b) * 128 + 32 * s);
-      w[s] = *reinterpret_cast<const uint4*>(ar + int64_t(b) * 128 + 32 * s);
+  for (int i = 0; i < 4; ++i) off[i] = tile_offset(0, i, K);
+  auto copy = [&](FewStage& st, int b) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      tile_copy(rsX, off[i], 128 * b, st[wave][0], i);
+      tile_copy(rsA, off[i], 128 * b, st[wave][1], i);
     }
+  };
+  floatx4 acc = {0.f, 0.f, 0.f, 0.f};
+  auto use = [&](const FewStage& st) {
 #pragma unroll
     for (int s = 0; s < 4; ++s)
-      acc = mfma_16x16x32(__builtin_bit_cast(V, x[s]), __builtin_bit_cast(V, w[s]), acc);
+      acc = mfma_16x16x32(__builtin_bit_cast(V, tile_read(st[wave][0], s)),
+                          __builtin_bit_cast(V, tile_read(st[wave][1], s)), acc);
+  };
+  // a wave reads only what it copied itself: waits, no barriers
+  for (int b = b0 + wave; b < b1; b += 2 * kFewWaves) {
+    copy(s0, b);
+    if (b + kFewWaves < b1) copy(s1, b + kFewWaves);
+    wait_vmem<0>();
+    fence();
+    use(s0);
+    if (b + kFewWaves < b1) use(s1);
+    wait_lds();
+    fence();
   }
+  float(*red)[16][17] = reinterpret_cast<float(*)[16][17]>(&s0);
+  __syncthreads();
 #pragma unroll
   for (int v = 0; v < 4; ++v) red[wave][4 * lg + v][lr] = acc[v];
   __syncthreads();
@@ -95,11 +128,21 @@ __device__ __forceinline__ void few_down(const LoraFew& p, int id, float (*red)[
 // launch 1: the shared product, T > 16
 // ---------------------------------------------------------------------------
 
-template <int MT>
-struct FewSlot {
-  uint32_t w[8], z;
-  uint4 s, x[MT];
+// A block of 32 k rows of the packed words; the zero points and scales of the
+// group that one (group size 32) or two (64, 128) blocks lie in.
+struct FewWords {
+  uint32_t w[8];
 };
+struct FewGroup {
+  uint32_t z;
+  uint4 s;
+};
+constexpr int kFewSlots = 4;
+
+// Per wave and stage: 16·MT tokens x 64 channels of X, rows of 8 chunks of 16
+// bytes, chunk c of row i at c ^ (i / 2) % 8.
+template <int MT>
+using FewX = uint4[kFewWaves][16 * MT * 8];
 
 // The MFMA operand of nibble R: its 8 codes, one per word, as rounded Ŵ.
 template <bool F16, int R>
@@ -137,31 +180,49 @@ __device__ __forceinline__ uint4 few_operand(const uint32_t (&w)[8], uint32_t z,
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-template <bool F16, int MT>
-__device__ __forceinline__ void few_block(const FewSlot<MT>& sl, const uint32_t (&base)[2],
-                                          floatx4 (&acc)[8][MT]) {
-  typedef typename Operand<F16>::type V;
-  const uint32_t sw[4] = {sl.s.x, sl.s.y, sl.s.z, sl.s.w};
-#define AWQ_FEW_NIBBLE(R)                                                              \
-  {                                                                                    \
-    const V b = __builtin_bit_cast(V, few_operand<F16, R>(sl.w, sl.z, sw, base));            \
-    for (int m = 0; m < MT; ++m)                                                       \
-      acc[R][m] = mfma_16x16x32(__builtin_bit_cast(V, sl.x[m]), b, acc[R][m]);         \
-  }
-  AWQ_FEW_NIBBLE(0) AWQ_FEW_NIBBLE(1)
-
-  AWQ_FEW_NIBBLE(2) AWQ_FEW_NIBBLE(3)
-
-  AWQ_FEW_NIBBLE(4) AWQ_FEW_NIBBLE(5)
-
-  AWQ_FEW_NIBBLE(6) AWQ_FEW_NIBBLE(7)
-
-#undef AWQ_FEW_NIBBLE
+// The accumulators stay in AGPRs through inline asm: 128 of them among the
+// vector registers make the allocator spill at two waves per SIMD. The
+// compiler puts no wait states around asm: s_nop 1 covers an operand that the
+// instruction before wrote, and few_settle the reads at the end.
+__device__ __forceinline__ void mfma_few(floatx4& c, const bf16x8_t& a, const bf16x8_t& b) {
+  asm("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
+__device__ __forceinline__ void mfma_few(floatx4& c, const f16x8_t& a, const f16x8_t& b) {
+  asm("s_nop 1\n\tv_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
+template <int MT>
+__device__ __forceinline__ void few_settle(floatx4 (&acc)[8][MT]) {
+  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+  for (int r = 0; r < 8; ++r)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) asm volatile("" : "+a"(acc[r][m]));
 }
 
 template <bool F16, int MT>
-__device__ __forceinline__ void few_product(const LoraFew& p, int id, int blocks,
-                                            float (*red)[16 * MT][kFewCols + 4]) {
+__device__ __forceinline__ void few_block(const FewWords& sl, const FewGroup& gr,
+                                          const FewX<MT>& x, uint32_t xat,
+                                          const uint32_t (&base)[2], floatx4 (&acc)[8][MT]) {
+  typedef typename Operand<F16>::type V;
+  V xv[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+    xv[m] = __builtin_bit_cast(V, (&x[0][0])[xat + 128 * m]);
+  const uint32_t sw[4] = {gr.s.x, gr.s.y, gr.s.z, gr.s.w};
+#define AWQ_FEW_NIBBLE(R)                                                              \
+  {                                                                                    \
+    const V b = __builtin_bit_cast(V, few_operand<F16, R>(sl.w, gr.z, sw, base));      \
+    for (int m = 0; m < MT; ++m) mfma_few(acc[R][m], xv[m], b);                        \
+  }
+  AWQ_FEW_NIBBLE(0) AWQ_FEW_NIBBLE(1) AWQ_FEW_NIBBLE(2) AWQ_FEW_NIBBLE(3)
+  AWQ_FEW_NIBBLE(4) AWQ_FEW_NIBBLE(5) AWQ_FEW_NIBBLE(6) AWQ_FEW_NIBBLE(7)
+#undef AWQ_FEW_NIBBLE
+}
+
+// s0, s1: the wave's X stages and, at the end, the meeting of the waves.
+template <bool F16, int MT, bool G32>
+__device__ __forceinline__ void few_product(const LoraFew& p, int id, int blocks, FewX<MT>& s0,
+                                            FewX<MT>& s1) {
   constexpr int R = 16 * MT;
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
@@ -182,54 +243,108 @@ __device__ __forceinline__ void few_product(const LoraFew& p, int id, int blocks
   const int64_t t0 = int64_t(tt) * R, n0 = int64_t(cb) * kFewCols;
   const int kw0 = (s * kFewWaves + wave) * p.kpw;
   const int kw1 = kw0 + p.kpw < int(K) ? kw0 + p.kpw : int(K);
-  // lanes past N read column 0, token rows past T the last one: neither is
-  // ever stored, and no MFMA row or column depends on another
+  // Lanes past N read column 0 and are never stored; token rows past T read as
+  // zero.
   const int64_t col = n0 / 8 + lr < N8 ? n0 / 8 + lr : 0;
-  // 32-bit lane offsets (bytes) from bases common to the wave: 8·lg + col / ..
-  // rows of the packed words (K < 2^22, N·K <= 2^34), at most 256 tokens of X
   const uint32_t qoff = uint32_t((int64_t(8 * lg) * N8 + col) * 4);
   const uint32_t zoff = uint32_t(col * 4), soff = uint32_t(col * 16);
-  uint32_t xoff[MT];
+  const auto rsX = rows_rsrc(p.X + t0 * K, p.T - t0 < R ? p.T - t0 : R, K);
+  uint32_t xoff[2];      // rows 8i + l / 8 of X: the swizzle repeats every 16 rows
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int64_t t = t0 + 16 * m + lr;
-    xoff[m] = uint32_t(((t < p.T ? t : p.T - 1) * K + 8 * lg) * 2);
+  for (int i = 0; i < 2; ++i) {
+    const int row = 8 * i + (lane >> 3);
+    xoff[i] = uint32_t((row * K + ((lane & 7) ^ (row >> 1)) * 8) * 2);
   }
+  const int xstep = int(16 * K * 2);
+  auto copy_x = [&](FewX<MT>& st, int k) {
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsX, AWQ_LORA_LDS(st[wave] + 64 * i), 16,
+                                               xoff[i & 1], (i >> 1) * xstep + 2 * k, 0, 0);
+  };
+  // The wave's rows of packed words (at most a quarter of N·K / 2 <= 2^33
+  // bytes), and the layer's zero points and scales, as buffer resources: one
+  // lane offset each, everything else in scalar registers.
+  const int kw = kw0 < kw1 ? kw0 : 0, rowb = int(N8 * 4);
+  const auto rsQ = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<int32_t*>(p.w.qweight) + int64_t(kw) * N8, 0,
+      int(uint32_t((kw1 - kw0 > 0 ? kw1 - kw0 : 0) * N8 * 4)), 0x00020000);
+  const auto rsZ = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<int32_t*>(p.w.qzeros), 0, int((K >> p.gshift) * N8 * 4), 0x00020000);
+  const auto rsS = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint16_t*>(p.w.scales), 0, int((K >> p.gshift) * N * 2), 0x00020000);
+  // blocks past the wave's last one read it again (and are not used)
+  auto load_words = [&](FewWords& sl, int kb) {
+    const int k = kb < kw1 ? kb : kw1 - 32;
+    const uint32_t at = uint32_t(k - kw0) * uint32_t(rowb);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      sl.w[e] = __builtin_amdgcn_raw_buffer_load_b32(rsQ, qoff, int(at + uint32_t(e * rowb)), 0);
+  };
+  auto load_group = [&](FewGroup& gr, int kb) {
+    const int g = (kb < kw1 ? kb : kw1 - 32) >> p.gshift;
+    gr.z = __builtin_amdgcn_raw_buffer_load_b32(rsZ, zoff, g * rowb, 0);
+    const auto v = __builtin_amdgcn_raw_buffer_load_b128(
+        rsS, soff, int(uint32_t(g) * uint32_t(rowb) * 4u), 0);
+    gr.s = make_uint4(v[0], v[1], v[2], v[3]);
+  };
   floatx4 acc[8][MT];
 #pragma unroll
   for (int r = 0; r < 8; ++r)
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[r][m] = floatx4{0.f, 0.f, 0.f, 0.f};
   if (kw0 < kw1) {
-    // (kpw and K are multiples of 64) blocks past the wave's last one read it again
-    auto load = [&](FewSlot<MT>& sl, int kb) {
-      const int k = kb < kw1 ? kb : kw1 - 32;
-      const int g = k >> p.gshift;
-      const char* q = reinterpret_cast<const char*>(p.w.qweight) + int64_t(k) * N8 * 4;
-      const char* x = reinterpret_cast<const char*>(p.X) + int64_t(k) * 2;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        sl.w[e] = *reinterpret_cast<const uint32_t*>(q + int64_t(e) * N8 * 4 + qoff);
-#pragma unroll
-      for (int m = 0; m < MT; ++m) sl.x[m] = *reinterpret_cast<const uint4*>(x + xoff[m]);
-      sl.z = *reinterpret_cast<const uint32_t*>(
-          reinterpret_cast<const char*>(p.w.qzeros) + int64_t(g) * N8 * 4 + zoff);
-      sl.s = *reinterpret_cast<const uint4*>(
-          reinterpret_cast<const char*>(p.w.scales) + int64_t(g) * N * 2 + soff);
-    };
     // fp16 1024 and 64, opaque so that they stay in registers (with the mask in
     // a scalar one, and-or is one instruction)
     uint32_t base[2] = {0x64006400u, 0x54005400u};
     asm volatile("" : "+v"(base[0]), "+v"(base[1]));
-    FewSlot<MT> a, b;
-    load(a, kw0);
-    for (int kb = kw0; kb < kw1; kb += 64) {
-      load(b, kb + 32);
-      few_block<F16, MT>(a, base, acc);
-      load(a, kb + 64);
-      few_block<F16, MT>(b, base, acc);
+    // where the lane's operand of 32-channel step h lies in a stage (as opaque:
+    // two registers, not one for every stage and token block)
+    uint32_t xat[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      xat[h] = uint32_t(wave * (R * 8) + lr * 8 + ((4 * h + lg) ^ (lr >> 1)));
+    asm volatile("" : "+v"(xat[0]), "+v"(xat[1]));
+    FewWords sl[kFewSlots];
+    FewGroup gr[G32 ? 4 : 2];
+    copy_x(s0, kw0);
+    fence();
+#pragma unroll
+    for (int i = 0; i < kFewSlots; ++i) {
+      load_words(sl[i], kw0 + 32 * i);
+      if (G32 || i % 2) load_group(gr[G32 ? i : i / 2], kw0 + 32 * i);
     }
+    // kpw and K are multiples of 128: two stages of X, four slots of words.
+    // A stage's copies are followed by the loads of two slots and their groups
+    // (the first stage's by twice that), which may be outstanding when it is
+    // read. A wave reads only what it copied itself, so no barrier is needed.
+    constexpr int kBehind = 16 + (G32 ? 4 : 2);
+    for (int kb = kw0; kb < kw1; kb += 128) {
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        fence();
+        wait_lds();
+        wait_vmem<kBehind>();
+        fence();
+        if (st == 0) copy_x(s1, kb + 64);
+        else copy_x(s0, kb + 128);
+        fence();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int i = 2 * st + h, next = kb + 32 * (kFewSlots + i);
+          few_block<F16, MT>(sl[i], gr[G32 ? i : st], st == 0 ? s0 : s1, xat[h], base, acc);
+          __builtin_amdgcn_sched_barrier(0);
+          load_words(sl[i], next);
+          if (G32 || h) load_group(gr[G32 ? i : st], next);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    }
+    wait_vmem<0>();
   }
+  few_settle<MT>(acc);
+  __syncthreads();
+  float* const red[2] = {reinterpret_cast<float*>(&s0), reinterpret_cast<float*>(&s1)};
   // lane l holds outputs 8·(l % 16) + r, tokens 16·m + 4·(l / 16) + v
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
@@ -238,7 +353,7 @@ __device__ __forceinline__ void few_product(const LoraFew& p, int id, int blocks
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-          float* row = &red[wave & 1][16 * m + 4 * lg + v][8 * lr];
+          float* row = red[wave & 1] + (16 * m + 4 * lg + v) * kFewCols + 8 * lr;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float4 x = make_float4(acc[4 * h][m][v], acc[4 * h + 1][m][v], acc[4 * h + 2][m][v],
@@ -256,22 +371,26 @@ __device__ __forceinline__ void few_product(const LoraFew& p, int id, int blocks
   for (int e = threadIdx.x; e < R * kFewCols / 4; e += 64 * kFewWaves) {
     const int i = e / (kFewCols / 4), c = e % (kFewCols / 4) * 4;
     if (t0 + i >= p.T || n0 + c >= N) continue;
-    const float4 x = *reinterpret_cast<const float4*>(&red[0][i][c]);
-    const float4 y = *reinterpret_cast<const float4*>(&red[1][i][c]);
+    const float4 x = *reinterpret_cast<const float4*>(red[0] + i * kFewCols + c);
+    const float4 y = *reinterpret_cast<const float4*>(red[1] + i * kFewCols + c);
     *reinterpret_cast<float4*>(p.partial + (int64_t(s) * p.T + t0 + i) * N + n0 + c) =
         make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
   }
 }
 
-template <bool F16, int MT>
+template <bool F16, int MT, bool G32>
 __global__ __launch_bounds__(64 * kFewWaves, 2) void lora_few_kernel(LoraFew p, int downs) {
-  __shared__ union {
-    float down[kFewWaves][16][17];
-    float prod[2][16 * MT][kFewCols + 4];
-  } red;
+  // two stages each; separate arrays, so that the compiler can tell the one
+  // being read from the one being filled
+  constexpr int kStage = sizeof(FewX<MT>) > sizeof(FewStage) ? sizeof(FewX<MT>) : sizeof(FewStage);
+  __shared__ uint4 s0[kStage / 16], s1[kStage / 16];
   const int id = int(blockIdx.x);
-  if (id < downs) few_down<F16>(p, id, red.down);
-  else few_product<F16, MT>(p, id - downs, int(gridDim.x) - downs, red.prod);
+  if (id < downs)
+    few_down<F16>(p, id, reinterpret_cast<FewStage&>(s0), reinterpret_cast<FewStage&>(s1));
+  else
+    few_product<F16, MT, G32>(p, id - downs, int(gridDim.x) - downs,
+                              reinterpret_cast<FewX<MT>&>(s0),
+                              reinterpret_cast<FewX<MT>&>(s1));
 }
 
 // T <= 16, N a multiple of 16.
@@ -279,20 +398,20 @@ template <bool F16, int G, int TV>
 __global__ __launch_bounds__(64 * kFewWaves, 2) void lora_decode_kernel(LoraFew p, int downs,
                                                                        int gx, int gy) {
   __shared__ union {
-    float down[kFewWaves][16][17];
+    FewStage down[2];
     MgRed mg[kMgWaves];
-  } red;
+  } sm;
   const int id = int(blockIdx.x);
-  if (id < downs) few_down<F16>(p, id, red.down);
+  if (id < downs) few_down<F16>(p, id, sm.down[0], sm.down[1]);
   else
     mgemv_workgroup<F16, 4, G, TV>(p.X, p.T, p.w.N, p.w.K, p.w.qweight, p.w.qzeros, p.w.scales,
-                                   p.kpw, p.partial, id - downs, gx, gy, red.mg);
+                                   p.kpw, p.partial, id - downs, gx, gy, sm.mg);
 }
 
 template <bool F16>
 __global__ __launch_bounds__(64 * kFewWaves) void lora_few_down_kernel(LoraFew p) {
-  __shared__ float red[kFewWaves][16][17];
-  few_down<F16>(p, int(blockIdx.x), red);
+  __shared__ FewStage s0, s1;
+  few_down<F16>(p, int(blockIdx.x), s0, s1);
 }
 
 // ---------------------------------------------------------------------------
@@ -485,8 +604,13 @@ hipError_t launch_few(LoraFew p, hipStream_t st) {
     else launch_decode<F16, 128>(p, downs, gx, p.S, st);
   } else {
     const unsigned grid = unsigned(downs + p.tiles * p.col_blocks * p.S);
-    if (p.T <= 32) lora_few_kernel<F16, 2><<<grid, 256, 0, st>>>(p, downs);
-    else lora_few_kernel<F16, 4><<<grid, 256, 0, st>>>(p, downs);
+    if (p.T <= 32) {
+      if (p.w.group == 32) lora_few_kernel<F16, 2, true><<<grid, 256, 0, st>>>(p, downs);
+      else lora_few_kernel<F16, 2, false><<<grid, 256, 0, st>>>(p, downs);
+    } else {
+      if (p.w.group == 32) lora_few_kernel<F16, 4, true><<<grid, 256, 0, st>>>(p, downs);
+      else lora_few_kernel<F16, 4, false><<<grid, 256, 0, st>>>(p, downs);
+    }
   }
   const dim3 grid(unsigned((p.w.N + kFinishCols - 1) / kFinishCols), unsigned((p.T + 15) / 16));
   if (p.s.r <= 32) lora_few_finish_kernel<F16, 1><<<grid, 256, 0, st>>>(p);

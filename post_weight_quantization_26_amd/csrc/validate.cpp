@@ -492,6 +492,13 @@ bool lora_sizes_ok(int64_t T, int64_t N, int64_t K, int32_t L, int32_t r, awq_dt
          L <= kLoraMaxAdapters && r >= 8 && r <= kLoraMaxRank && r % 8 == 0;
 }
 
+// Runs of the narrow product over C channels: three workgroups of 64 tokens per
+// CU, each with 4 or more 128-wide blocks.
+static int64_t lora_down_runs(int64_t T, int64_t C) {
+  const int64_t tiles = ceil_div(T, 64);
+  return std::max<int64_t>(1, std::min({int64_t(16), 768 / tiles, C / 512}));
+}
+
 LoraLayout lora_layout(int64_t T, int64_t N, int64_t K, int32_t, int32_t r) {
   LoraLayout l{};
   size_t off = 0;
@@ -513,15 +520,17 @@ LoraLayout lora_layout(int64_t T, int64_t N, int64_t K, int32_t, int32_t r) {
       l.col_blocks = ceil_div(N, 128);
       const int64_t runs = std::max<int64_t>(
           1, std::min(512 / (l.tiles * l.col_blocks), ceil_div(K, 512)));
-      l.kpw = ceil_div(K, 4 * runs * 64) * 64;
+      l.kpw = ceil_div(K, 4 * runs * 128) * 128;
       l.S = ceil_div(K, 4 * l.kpw);
     }
-    // runs of the narrow product: its workgroups read 128 rows or more per
-    // wave, and fewer runs with more tokens, whose second launch sums them
-    l.S2 = std::max<int64_t>(1, std::min<int64_t>({8, K / 1024, 256 / T}));
+    // runs of the narrow product: 2 blocks of 128 rows or more per wave, and
+    // at most 16 KiB of partial sums for the second launch's workgroups to add
+    l.S2 = std::max<int64_t>(1, std::min<int64_t>({8, K / 1024, 256 / r}));
     l.partial = take(size_t(l.S) * size_t(T) * size_t(N) * 4);
     l.hpart = take(size_t(l.S2) * size_t(T) * size_t(r) * 4);
   } else {
+    l.runs = lora_down_runs(T, K);
+    l.part = take(size_t(l.runs) * size_t(T) * size_t(r) * 4);
     l.q = take(size_t(T) * size_t(lora_q_width(r)) * 2);
     l.e = take(size_t(T) * 4);
     l.wd = take(size_t(N) * size_t(K) * 2);
@@ -553,6 +562,8 @@ LoraBackwardLayout lora_backward_layout(int64_t T, int64_t N, int64_t K, int32_t
   l.bt = take(a * r * n * 2);
   l.at = take(a * r * k * 2);
   l.dyp = take(l.Np == N ? 0 : t * n * 2);
+  l.runs = lora_down_runs(T, l.Np);
+  l.part = take(size_t(l.runs) * t * r * 4);
   l.q = take(t * size_t(lora_q_width(r)) * 2);
   l.e = take(t * 4);
   l.gt = take(tp * r * 4);
