@@ -808,6 +808,7 @@ extern "C" awq_status awq_w4a16_lora_matmul(
   d.steps = x8_steps;
   uint16_t* Wd = at<uint16_t>(ws, l.wd);
   const LoraUp u{d.Q, d.E, ids, set.B, L, r, d.RW};
+  const LoraSplit cut{int(l.cut.full), int(l.cut.runs), at<float>(ws, l.tiles_part)};
   AWQ_HIP(timed(AWQ_K_LORA, st,
                 [&] {
                   hipError_t e = launch_lora_down(d, st);
@@ -815,7 +816,7 @@ extern "C" awq_status awq_w4a16_lora_matmul(
                     e = launch_w4a16_dequant(qweight, qzeros, scales, N, K, group_size, f16, Wd,
                                              st);
                   if (e == hipSuccess)
-                    e = launch_lora_gemm(x, K, Wd, K, T, N, K, u, f16, y, st);
+                    e = launch_lora_gemm(x, K, Wd, K, T, N, K, u, cut, f16, y, st);
                   return e;
                 }),
           "lora_matmul");
@@ -881,6 +882,7 @@ extern "C" awq_status awq_w4a16_lora_backward(
   d.h_max = at<float>(ws, l.hmax);
 
   const LoraUp u{d.Q, d.E, ids, pr.At, L, r, d.RW};
+  const LoraSplit cut{int(l.cut.full), int(l.cut.runs), at<float>(ws, l.tiles_part)};
 
   LoraGrad g{};
   g.dY = pr.dY;
@@ -911,7 +913,7 @@ extern "C" awq_status awq_w4a16_lora_backward(
                   hipError_t e = launch_lora_prep(pr, st);
                   if (e == hipSuccess) e = launch_lora_down(d, st);
                   if (e == hipSuccess && dX)
-                    e = launch_lora_gemm(d.V, l.Np, pr.Wt, l.Np, T, K, l.Np, u, f16,
+                    e = launch_lora_gemm(d.V, l.Np, pr.Wt, l.Np, T, K, l.Np, u, cut, f16,
                                          static_cast<uint16_t*>(dX), st);
                   if (e == hipSuccess)
                     e = launch_lora_grad(g, int(l.pieces), T > l.piece, st);

@@ -207,8 +207,14 @@ awq_status check_w4a16(const void* X, awq_dtype d, int64_t T, int64_t N, int64_t
 constexpr int kLoraMaxRank = 128;
 constexpr int kLoraMaxAdapters = 4096;
 // Columns of a token's wide-product operand: c·P as two 16-bit halves, padded
-// with zeros to whole 32-wide MFMA steps.
-inline int lora_q_width(int32_t r) { return int((2 * r + 31) / 32 * 32); }
+// with zeros to whole 64-wide k-tiles.
+inline int lora_q_width(int32_t r) { return int((2 * r + 63) / 64 * 64); }
+// The 256x256 GEMM's last tiles, cut into runs of the contraction.
+struct LoraCut {
+  int64_t full, runs;
+  size_t bytes;   // their partial tiles
+};
+LoraCut lora_cut(int64_t M, int64_t N, int64_t C);
 // Token rows up to which the forward call runs without a dequantised layer.
 constexpr int64_t kLoraFewMaxT = 256;
 struct LoraLayout {
@@ -220,6 +226,8 @@ struct LoraLayout {
   size_t q;       // [T, lora_q_width(r)] 16-bit
   size_t e;       // [T] f32
   size_t wd;      // [N, K] 16-bit dequantised layer
+  LoraCut cut;
+  size_t tiles_part;
   size_t total;
 };
 LoraLayout lora_layout(int64_t T, int64_t N, int64_t K, int32_t L, int32_t r);
@@ -234,6 +242,8 @@ struct LoraBackwardLayout {
   size_t gt, ht, gmax, hmax;  // f32: [r, Tp] twice, [Tp] twice
   size_t token, pos, table, n_pieces, n_slots, first_slot, last_pos;
   size_t partial;             // f32 [slots, (K + N)·r]
+  LoraCut cut;
+  size_t tiles_part;
   size_t total;
 };
 LoraBackwardLayout lora_backward_layout(int64_t T, int64_t N, int64_t K, int32_t L, int32_t r);

@@ -43,7 +43,7 @@ struct LoraDown {
   const int32_t* pos;
   int64_t ldp;
   uint16_t* Q;            // [T, RW]: c·P as halves hi [r], lo [r], zeros up to RW
-  int RW;                 // 2r rounded up to 32
+  int RW;                 // 2r rounded up to 64
   float* E;               // [T] the power of two that Q is scaled down by
   int8_t* codes;          // [T, C] 8-bit checkpoint of V, or NULL
   float* steps;           // [T, C / 128]
@@ -58,9 +58,15 @@ struct LoraUp {
   const uint16_t* U;      // [L, N, r]
   int L, r, RW;
 };
+// Tiles past the first `full` are cut into `runs` of the contraction (0 or 1:
+// none is); part holds a 256x256 float32 tile for each of them.
+struct LoraSplit {
+  int full, runs;
+  float* part;
+};
 hipError_t launch_lora_gemm(const uint16_t* V, int64_t ldv, const uint16_t* Wd, int64_t ldw,
-                            int64_t M, int64_t N, int64_t C, const LoraUp& u, int f16,
-                            uint16_t* O, hipStream_t st);
+                            int64_t M, int64_t N, int64_t C, const LoraUp& u,
+                            const LoraSplit& sp, int f16, uint16_t* O, hipStream_t st);
 
 // The dequantisation pass of the W4A16 GEMM (w4a16.hip): Ŵ [N, K], rounded.
 hipError_t launch_w4a16_dequant(const int32_t* qweight, const int32_t* qzeros,

@@ -161,7 +161,7 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(LoraDown p) {
   }
 }
 
-// A wave per token at a time, 16 tokens per workgroup: the sum of its partial
+// A wave per token: the sum of its partial
 // sums, in order, as H, as the gradients' transposed sorted rows, and as the
 // wide product's operand c_a·P in two 16-bit halves hi = rnd(v), lo =
 // rnd(v - hi), which lose at most u² (bf16: 2^-16) of v. fp16 halves are
@@ -171,60 +171,58 @@ template <bool F16>
 __global__ __launch_bounds__(256) void lora_combine_kernel(LoraDown p) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
-  for (int i = 0; i < 4; ++i) {
-    const int64_t t = int64_t(blockIdx.x) * 16 + 4 * wave + i;
-    if (t >= p.T) return;
-    const int a = p.ids[t];
-    const bool has = a >= 0 && a < p.L;
-    if (!has && !p.H) continue;
-    float v[2] = {0.f, 0.f}, h[2] = {0.f, 0.f};
-    if (has)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int j = lane + 64 * k;
-        if (j >= p.r) continue;
-        const float* src = p.part + t * p.r + j;
-#pragma unroll 4
-        for (int s = 0; s < p.S; ++s) v[k] += src[int64_t(s) * p.T * p.r];
-        if (p.Hin) h[k] = p.Hin[t * p.r + j];
-      }
-    if (p.H)
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (lane + 64 * k < p.r) p.H[t * p.r + lane + 64 * k] = v[k];
-    if (!has) continue;
-    float m = fmaxf(fabsf(v[0]), fabsf(v[1])), mh = fmaxf(fabsf(h[0]), fabsf(h[1]));
-#pragma unroll
-    for (int o = 32; o; o >>= 1) {
-      m = fmaxf(m, __shfl_xor(m, o));
-      mh = fmaxf(mh, __shfl_xor(mh, o));
-    }
-    const float c = p.scaling[a], cm = fabsf(c) * m;
-    int e = 0;
-    if (F16 && !(cm >= 0x1p-3f && cm < 0x1p14f)) e = exponent_of(cm);
-    const float down = exp2i(-e);
-    uint16_t* q = p.Q + t * p.RW;
-    const int pos = p.Pt ? p.pos[t] : 0;
+  const int64_t t = int64_t(blockIdx.x) * 4 + wave;
+  if (t >= p.T) return;
+  const int a = p.ids[t];
+  const bool has = a >= 0 && a < p.L;
+  if (!has && !p.H) return;
+  float v[2] = {0.f, 0.f}, h[2] = {0.f, 0.f};
+  if (has)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int j = lane + 64 * k;
       if (j >= p.r) continue;
-      if (p.Pt) {
-        p.Pt[int64_t(j) * p.ldp + pos] = v[k];
-        p.Ht[int64_t(j) * p.ldp + pos] = h[k];
-      }
-      const float s = c * v[k] * down;
-      const uint16_t hi = round16<F16>(s);
-      q[j] = hi;
-      q[p.r + j] = round16<F16>(s - widen16<F16>(hi));
+      const float* src = p.part + t * p.r + j;
+#pragma unroll 4
+      for (int s = 0; s < p.S; ++s) v[k] += src[int64_t(s) * p.T * p.r];
+      if (p.Hin) h[k] = p.Hin[t * p.r + j];
     }
-    for (int j = 2 * p.r + lane; j < p.RW; j += 64) q[j] = 0;
-    if (lane == 0) {
-      p.E[t] = exp2i(e);
-      if (p.Pt) {
-        p.row_max[pos] = m;
-        p.h_max[pos] = mh;
-      }
+  if (p.H)
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (lane + 64 * k < p.r) p.H[t * p.r + lane + 64 * k] = v[k];
+  if (!has) return;
+  float m = fmaxf(fabsf(v[0]), fabsf(v[1])), mh = fmaxf(fabsf(h[0]), fabsf(h[1]));
+#pragma unroll
+  for (int o = 32; o; o >>= 1) {
+    m = fmaxf(m, __shfl_xor(m, o));
+    mh = fmaxf(mh, __shfl_xor(mh, o));
+  }
+  const float c = p.scaling[a], cm = fabsf(c) * m;
+  int e = 0;
+  if (F16 && !(cm >= 0x1p-3f && cm < 0x1p14f)) e = exponent_of(cm);
+  const float down = exp2i(-e);
+  uint16_t* q = p.Q + t * p.RW;
+  const int pos = p.Pt ? p.pos[t] : 0;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int j = lane + 64 * k;
+    if (j >= p.r) continue;
+    if (p.Pt) {
+      p.Pt[int64_t(j) * p.ldp + pos] = v[k];
+      p.Ht[int64_t(j) * p.ldp + pos] = h[k];
+    }
+    const float s = c * v[k] * down;
+    const uint16_t hi = round16<F16>(s);
+    q[j] = hi;
+    q[p.r + j] = round16<F16>(s - widen16<F16>(hi));
+  }
+  for (int j = 2 * p.r + lane; j < p.RW; j += 64) q[j] = 0;
+  if (lane == 0) {
+    p.E[t] = exp2i(e);
+    if (p.Pt) {
+      p.row_max[pos] = m;
+      p.h_max[pos] = mh;
     }
   }
 }
@@ -242,7 +240,7 @@ hipError_t launch_f(const LoraDown& p, hipStream_t st) {
   else if (p.r <= 32) launch_jb<F16, 2>(p, grid, st);
   else if (p.r <= 64) launch_jb<F16, 4>(p, grid, st);
   else launch_jb<F16, 8>(p, grid, st);
-  lora_combine_kernel<F16><<<unsigned((p.T + 15) / 16), 256, 0, st>>>(p);
+  lora_combine_kernel<F16><<<unsigned((p.T + 3) / 4), 256, 0, st>>>(p);
   return hipGetLastError();
 }
 

@@ -499,6 +499,29 @@ static int64_t lora_down_runs(int64_t T, int64_t C) {
   return std::max<int64_t>(1, std::min({int64_t(16), 768 / tiles, C / 512}));
 }
 
+// Tiles past a multiple of 256 take as long as 256 of them. Cut into runs they
+// take 1 / runs of that, and their partial tiles (256 KiB out and in) about
+// 0.09 us each, with 4 us for the kernel that adds them; 64 channels of a tile
+// take 1.6 us. Runs of 8 or more 64-wide steps, as many as fill 256 CUs.
+LoraCut lora_cut(int64_t M, int64_t N, int64_t C) {
+  LoraCut c{};
+  const int64_t tiles = ceil_div(M, 256) * ceil_div(N, 256), rest = tiles % 256;
+  const double whole = 1.6 * double(C / 64);
+  double best = whole;
+  for (int64_t runs = 2; rest && runs <= std::min(256 / rest, C / 512); ++runs) {
+    const double t = whole / double(runs) + 0.09 * double(rest * runs) + 4.0;
+    if (t < best) {
+      best = t;
+      c.runs = runs;
+    }
+  }
+  if (c.runs) {
+    c.full = tiles - rest;
+    c.bytes = size_t(rest) * size_t(c.runs) * 256 * 256 * 4;
+  }
+  return c;
+}
+
 LoraLayout lora_layout(int64_t T, int64_t N, int64_t K, int32_t, int32_t r) {
   LoraLayout l{};
   size_t off = 0;
@@ -534,6 +557,8 @@ LoraLayout lora_layout(int64_t T, int64_t N, int64_t K, int32_t, int32_t r) {
     l.q = take(size_t(T) * size_t(lora_q_width(r)) * 2);
     l.e = take(size_t(T) * 4);
     l.wd = take(size_t(N) * size_t(K) * 2);
+    l.cut = lora_cut(T, N, K);
+    l.tiles_part = take(l.cut.bytes);
   }
   l.total = off;
   return l;
@@ -578,6 +603,8 @@ LoraBackwardLayout lora_backward_layout(int64_t T, int64_t N, int64_t K, int32_t
   l.first_slot = take(a * 4);
   l.last_pos = take(a * 4);
   l.partial = take(size_t(l.slots) * (k + size_t(N)) * r * 4);
+  l.cut = lora_cut(T, K, l.Np);
+  l.tiles_part = take(l.cut.bytes);
   l.total = off;
   return l;
 }
@@ -613,6 +640,9 @@ static awq_status check_lora_common(const char* name, const void* V, awq_dtype d
     return set_error(AWQ_E_UNSUPPORTED,
                      "%s: K=%lld, N=%lld exceed the 32-bit offsets (512 * K must stay below "
                      "2^31, N*K at most 2^34)", name, (long long)K, (long long)N);
+  if (std::max(N, K) * r >= (int64_t(1) << 31))
+    return set_error(AWQ_E_UNSUPPORTED, "%s: N=%lld x rank %d exceeds an adapter's 32-bit offsets "
+                     "(N * r and K * r must stay below 2^31)", name, (long long)N, int(r));
   if (!grid_fits(search_gemm_blocks(T, std::max(N, K), AWQ_BF16), 256) || !grid_fits(T, 256))
     return set_error(AWQ_E_UNSUPPORTED, "%s: T=%lld x N=%lld exceed the GEMM's grid", name,
                      (long long)T, (long long)N);
