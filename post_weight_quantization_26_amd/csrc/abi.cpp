@@ -837,6 +837,7 @@ extern "C" awq_status awq_w4a16_lora_backward(
   const LoraBackwardLayout l = lora_backward_layout(T, N, K, L, r);
   const int f16 = dtype == AWQ_F16;
   const bool padded = l.Np != N;
+  static_assert(kLoraPieceMax == kLoraMaxPiece, "a piece's tokens fit the gradients' LDS");
 
   LoraPrep pr{};
   pr.w = {qweight, qzeros, scales, N, K, group_size};
@@ -870,15 +871,14 @@ extern "C" awq_status awq_w4a16_lora_backward(
   d.f16 = f16;
   d.S = int(l.runs);
   d.part = at<float>(ws, l.part);
-  d.Pt = at<float>(ws, l.gt);
+  d.Ps = at<float>(ws, l.gs);
   d.row_max = at<float>(ws, l.gmax);
   d.pos = pr.pos;
-  d.ldp = l.Tp;
   d.Q = at<uint16_t>(ws, l.q);
   d.RW = lora_q_width(r);
   d.E = at<float>(ws, l.e);
   d.Hin = H;
-  d.Ht = at<float>(ws, l.ht);
+  d.Hs = at<float>(ws, l.hs);
   d.h_max = at<float>(ws, l.hmax);
 
   const LoraUp u{d.Q, d.E, ids, pr.At, L, r, d.RW};
@@ -888,8 +888,8 @@ extern "C" awq_status awq_w4a16_lora_backward(
   g.dY = pr.dY;
   g.X = X;
   g.steps = x8_steps;
-  g.Gt = d.Pt;
-  g.Ht = d.Ht;
+  g.Gs = d.Ps;
+  g.Hs = d.Hs;
   g.g_max = d.row_max;
   g.h_max = d.h_max;
   g.scaling = scaling;
@@ -900,7 +900,6 @@ extern "C" awq_status awq_w4a16_lora_backward(
   g.first_slot = pr.first_slot;
   g.N = N;
   g.K = K;
-  g.Tp = l.Tp;
   g.L = L;
   g.r = r;
   g.f16 = f16;

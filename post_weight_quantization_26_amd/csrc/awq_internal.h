@@ -206,6 +206,7 @@ awq_status check_w4a16(const void* X, awq_dtype d, int64_t T, int64_t N, int64_t
 // Low-rank adapters: byte offsets of the regions of a call's workspace.
 constexpr int kLoraMaxRank = 128;
 constexpr int kLoraMaxAdapters = 4096;
+constexpr int kLoraPieceMax = 2048;   // tokens in a piece of the gradients' work
 // Columns of a token's wide-product operand: c·P as two 16-bit halves, padded
 // with zeros to whole 64-wide k-tiles.
 inline int lora_q_width(int32_t r) { return int((2 * r + 63) / 64 * 64); }
@@ -239,7 +240,7 @@ struct LoraBackwardLayout {
   size_t wt, bt, at, dyp;     // 16-bit: Ŵᵀ [K, Np], Bᵀ [L, r, Np], Aᵀ [L, K, r], dY [T, Np]
   int64_t runs;
   size_t part, q, e;          // as in LoraLayout
-  size_t gt, ht, gmax, hmax;  // f32: [r, Tp] twice, [Tp] twice
+  size_t gs, hs, gmax, hmax;  // f32: [Tp, ranks padded to 16] twice, [Tp] twice
   size_t token, pos, table, n_pieces, n_slots, first_slot, last_pos;
   size_t partial;             // f32 [slots, (K + N)·r]
   LoraCut cut;

@@ -35,13 +35,12 @@ struct LoraDown {
   int L, r, f16, S;       // S: runs of the contraction
   float* part;            // [S, T, r] their sums
   float* H;               // [T, r] or NULL; rows without an adapter get zeros
-  const float* Hin;       // [T, r], with Pt
-  float* Pt;              // [r, ldp] transposed, token t at column pos[t], or NULL
-  float* Ht;              // Hin likewise
-  float* row_max;         // [ldp] max_j |P| at pos[t]
-  float* h_max;           // [ldp] max_j |Hin|
+  const float* Hin;       // [T, r], with Ps
+  float* Ps;              // P in the gradients' operand order, sorted by pos, or NULL
+  float* Hs;              // Hin likewise
+  float* row_max;         // [Tp] max_j |P| at pos[t]
+  float* h_max;           // [Tp] max_j |Hin|
   const int32_t* pos;
-  int64_t ldp;
   uint16_t* Q;            // [T, RW]: c·P as halves hi [r], lo [r], zeros up to RW
   int RW;                 // 2r rounded up to 64
   float* E;               // [T] the power of two that Q is scaled down by
@@ -100,6 +99,7 @@ hipError_t launch_lora_few(const LoraFew& p, hipStream_t st);
 struct LoraPiece {
   int a, pos, n, slot;
 };
+constexpr int kLoraMaxPiece = 2048;
 
 // The gradient's preparation (lora_prep.hip).
 struct LoraPrep {
@@ -131,8 +131,8 @@ struct LoraGrad {
   const uint16_t* dY;     // [T, N]
   const void* X;          // [T, K] 16-bit, or int8 codes (then steps is set)
   const float* steps;     // [T, K / 128] or NULL
-  const float* Gt;        // [r, Tp] dY·B, transposed, in sorted order
-  const float* Ht;        // [r, Tp]
+  const float* Gs;        // dY·B and H in operand order: [Tp / 32][16 ranks][lane][8]
+  const float* Hs;
   const float* g_max;     // [Tp] largest |value| of each token
   const float* h_max;
   const float* scaling;
@@ -141,7 +141,7 @@ struct LoraGrad {
   const int* n_pieces;
   const int* slots;
   const int* first_slot;
-  int64_t N, K, Tp;
+  int64_t N, K;
   int L, r, f16;
   float* partial;         // [slots, (K + N)·r]
   uint16_t* dA;           // [L, r, K]

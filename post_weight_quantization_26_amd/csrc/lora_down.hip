@@ -161,9 +161,8 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(LoraDown p) {
   }
 }
 
-// A wave per token: the sum of its partial
-// sums, in order, as H, as the gradients' transposed sorted rows, and as the
-// wide product's operand c_a·P in two 16-bit halves hi = rnd(v), lo =
+// A wave per token: the sum of its partial sums, in order, as H, in the
+// gradients' operand order (with Hin in the same), and as the wide product's operand c_a·P in two 16-bit halves hi = rnd(v), lo =
 // rnd(v - hi), which lose at most u² (bf16: 2^-16) of v. fp16 halves are
 // scaled by a power of two where a row's largest value lies outside [2^-3,
 // 2^14), so that neither half overflows and lo keeps 2^-22 of the largest.
@@ -203,14 +202,17 @@ __global__ __launch_bounds__(256) void lora_combine_kernel(LoraDown p) {
   if (F16 && !(cm >= 0x1p-3f && cm < 0x1p14f)) e = exponent_of(cm);
   const float down = exp2i(-e);
   uint16_t* q = p.Q + t * p.RW;
-  const int pos = p.Pt ? p.pos[t] : 0;
+  const int pos = p.Ps ? p.pos[t] : 0;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int j = lane + 64 * k;
     if (j >= p.r) continue;
-    if (p.Pt) {
-      p.Pt[int64_t(j) * p.ldp + pos] = v[k];
-      p.Ht[int64_t(j) * p.ldp + pos] = h[k];
+    if (p.Ps) {
+      // [step of 32 positions][16 ranks][lane][8 positions] (lora_grad.hip)
+      const int64_t at = ((int64_t(pos >> 5) * ((p.r + 15) / 16) + (j >> 4)) * 64 +
+                          ((pos >> 3) & 3) * 16 + (j & 15)) * 8 + (pos & 7);
+      p.Ps[at] = v[k];
+      p.Hs[at] = h[k];
     }
     const float s = c * v[k] * down;
     const uint16_t hi = round16<F16>(s);
@@ -220,7 +222,7 @@ __global__ __launch_bounds__(256) void lora_combine_kernel(LoraDown p) {
   for (int j = 2 * p.r + lane; j < p.RW; j += 64) q[j] = 0;
   if (lane == 0) {
     p.E[t] = exp2i(e);
-    if (p.Pt) {
+    if (p.Ps) {
       p.row_max[pos] = m;
       p.h_max[pos] = mh;
     }

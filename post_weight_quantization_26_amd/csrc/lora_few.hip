@@ -34,16 +34,6 @@ namespace {
 constexpr int kFewWaves = 4;
 constexpr int kFewCols = 128;     // outputs per workgroup (T > 16)
 
-// Keeps memory operations and instructions on their side of it.
-__device__ __forceinline__ void fence() {
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-}
-__device__ __forceinline__ void wait_lds() {   // lgkmcnt(0)
-  __builtin_amdgcn_s_waitcnt(0xF | (3 << 14) | (0x7 << 4));
-}
-
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 
 // ---------------------------------------------------------------------------

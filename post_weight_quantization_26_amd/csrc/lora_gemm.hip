@@ -30,11 +30,11 @@
 namespace awq {
 namespace {
 
-__shared__ int sid[BM];          // adapter of each row (-1: none, or past the end)
+__shared__ __align__(16) int sid[BM];   // adapter of each row (-1: none, or past the end)
 __shared__ int slist[BM];        // the first rows of the distinct adapters
 __shared__ int sfirst[BM];       // first row with the same adapter
 __shared__ uint32_t smark[BM][8];  // columns of U that are not finite, at that row
-__shared__ float sE[BM];         // the power of two a row's q is scaled down by
+__shared__ __align__(16) float sE[BM];  // the power of two a row's q is scaled down by
 __shared__ int scount[5];        // distinct adapters by wave; whether any column is marked
 
 struct LowCtx {
@@ -54,15 +54,18 @@ __device__ __forceinline__ int list_adapters() {
   const int i = threadIdx.x, lane = i & 63, wave = i >> 6;
   const int id = sid[i];
   int first = i;
-  if (id >= 0) {
-    const bool same = __ballot(id == sid[0]) == ~0ull;
-    if (same) first = 0;
-    else
-      for (int k = 0; k < i; ++k)
-        if (sid[k] == id) {
-          first = k;
-          break;
-        }
+  if (__syncthreads_and(id == sid[0])) {
+    first = 0;
+  } else {
+    // from the last row down, so that the first match is the one that stays
+#pragma unroll 8
+    for (int k = BM / 4 - 1; k >= 0; --k) {
+      const int4 x = reinterpret_cast<const int4*>(sid)[k];
+      first = x.w == id ? 4 * k + 3 : first;
+      first = x.z == id ? 4 * k + 2 : first;
+      first = x.y == id ? 4 * k + 1 : first;
+      first = x.x == id ? 4 * k : first;
+    }
   }
   sfirst[i] = first;
   const uint64_t lead = __ballot(id >= 0 && first == i);

@@ -3,14 +3,16 @@
 //   dA_a[j][k] = c_a·Σ_t P[t][j]·X[t][k],   dB_a[n][j] = c_a·Σ_t dY[t][n]·H[t][j]
 //
 // over the tokens t of a, P = dY·B_a: products with a long contraction (tokens)
-// and one narrow side (r). Both are Z ᵀ·S with Z = X or dY, read once, and S
-// the narrow side, laid out as Sᵀ [r, positions] in the plan's sorted order.
+// and one narrow side (r). Both are Zᵀ·S with Z = X or dY, read once, and S
+// the narrow side in the plan's sorted order. Bound by the reads of Z.
 //
 // A workgroup takes 128 columns of Z, up to 64 ranks and one piece of a run;
-// its 4 waves take every fourth step of 32 tokens. A lane loads 8 channels of
-// 8 tokens (rows gathered through the plan, 256 contiguous bytes for 16
-// lanes); 32 byte permutes turn the 8x8 block into 8 MFMA operands of 8
-// tokens each, channel 8·(l % 16) + i for operand i: no pass through LDS.
+// its 4 waves take every fourth step of 32 tokens. Z's rows, gathered through
+// the plan, go to LDS by DMA a step ahead (a wave's own part: no barriers), 16
+// lanes to a row's 256 bytes. A lane reads back 8 channels of 8 tokens; 32 byte
+// permutes turn that 8x8 block into 8 MFMA operands of 8 tokens each, channel
+// 8·(l % 16) + i for operand i. S lies in operand order ([step][16 ranks][lane]
+// [8 tokens], lora_down.hip), so its loads are contiguous.
 // S comes as float32 and is split in registers into two 16-bit halves, so
 // that its rounding is u² (bf16 2^-16). fp16 halves are scaled by one power
 // of two per piece that takes the piece's largest |S| to 2^14: a value 2^-17
@@ -26,6 +28,7 @@
 #include "gemm_types.h"
 #include "lora.h"
 #include "lora_common.h"
+#include "lora_stage.h"
 
 namespace awq {
 namespace {
@@ -35,57 +38,75 @@ constexpr int kGradStrip = 128;
 
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 
+// Per wave: 32 tokens x 128 channels of Z.
+typedef uint4 GradStage[kGradWaves][512];
+static_assert(sizeof(GradStage) == 64 * kGradStrip * 4, "half of the waves' meeting place");
+
 // MF: fp16 matrix-core operands (fp16 Z, or 8-bit codes); else bf16.
 template <bool F16, bool X8, int JB>
 __device__ __forceinline__ void grad_piece(const LoraGrad& p, const LoraPiece& pc, bool is_a,
-                                           int64_t strip, int j0, float (*red)[16 * JB][kGradStrip + 4]) {
+                                           int64_t strip, int j0, GradStage& z0, GradStage& z1,
+                                           int* tokens) {
   constexpr bool MF = F16 || X8;
+  constexpr int kCopies = X8 ? 4 : 8;          // 1 KiB each
   typedef typename Operand<MF>::type V;
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
   const int64_t C = is_a ? p.K : p.N;
-  const float* St = is_a ? p.Gt : p.Ht;
+  const int jbs = (p.r + 15) / 16;
+  const float* S = (is_a ? p.Gs : p.Hs) + int64_t(pc.pos / 32) * jbs * 512 + j0 / 16 * 512;
   const float* row_max = is_a ? p.g_max : p.h_max;
   const int64_t c0 = strip * kGradStrip;
-  const int64_t cl = c0 + 8 * lr < C ? c0 + 8 * lr : C - 8;   // lanes past the last column reread it
   const int64_t KB = p.K / 128;
 
+  // the piece's tokens, its padding included (positions are multiples of 32)
+  const int padded = (pc.n + 31) / 32 * 32;
+  for (int i = threadIdx.x; i < padded; i += 64 * kGradWaves) tokens[i] = p.token[pc.pos + i];
+  __syncthreads();
   float scale = 1.f;
   if constexpr (MF) {
     float m = 0.f;
     for (int i = lane; i < pc.n; i += 64) {
       float v = row_max[pc.pos + i];
-      if constexpr (X8) v *= p.steps[int64_t(p.token[pc.pos + i]) * KB + strip];
+      if constexpr (X8) v *= p.steps[int64_t(tokens[i]) * KB + strip];
       m = fmaxf(m, v);
     }
 #pragma unroll
     for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
     if (m > 0.f && m < __builtin_inff()) scale = exp2i(14 - exponent_of(m));
   }
+  // Copy i brings rows 4i .. + 3 (8-bit: 8i .. + 7), 16 (8) lanes to a row; lanes
+  // past the last column reread it.
+  const char* Z = is_a ? static_cast<const char*>(p.X) : reinterpret_cast<const char*>(p.dY);
+  constexpr int kRowLanes = X8 ? 8 : 16, kRows = 64 / kRowLanes, kBytes = X8 ? 1 : 2;
+  const int64_t cb = (c0 + lane % kRowLanes * (16 / kBytes)) * kBytes;
+  const int64_t colb = cb < C * kBytes ? cb : C * kBytes - 16;
+  auto copy = [&](GradStage& st, int s) {
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+      const int tok = tokens[s + kRows * i + lane / kRowLanes];
+      __builtin_amdgcn_global_load_lds(
+          (const __attribute__((address_space(1))) void*)(Z + int64_t(tok) * C * kBytes + colb),
+          AWQ_LORA_LDS(st[wave] + 64 * i), 16, 0, 0);
+    }
+  };
   floatx4 acc[JB][8];
 #pragma unroll
   for (int q = 0; q < JB; ++q)
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[q][i] = floatx4{0.f, 0.f, 0.f, 0.f};
 
-  for (int s = 32 * wave; s < pc.n; s += 32 * kGradWaves) {
-    const int at = pc.pos + s + 8 * lg;
-    const int4 ta = *reinterpret_cast<const int4*>(p.token + at);
-    const int4 tb = *reinterpret_cast<const int4*>(p.token + at + 4);
-    const int tok[8] = {ta.x, ta.y, ta.z, ta.w, tb.x, tb.y, tb.z, tb.w};
+  auto use = [&](const GradStage& st, const float4 (&sv)[JB][2], const float (&step)[8], int s) {
     uint32_t z[8][X8 ? 2 : 4];
-    float step[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       if constexpr (X8) {
-        const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const int8_t*>(p.X) +
-                                                        int64_t(tok[e]) * C + cl);
+        const uint2 x =
+            reinterpret_cast<const uint2*>(st[wave])[(8 * lg + e) * 16 + lr];
         z[e][0] = x.x ^ 0x80808080u;
         z[e][1] = x.y ^ 0x80808080u;
-        step[e] = p.steps[int64_t(tok[e]) * KB + strip];
       } else {
-        const uint16_t* Z = is_a ? static_cast<const uint16_t*>(p.X) : p.dY;
-        const uint4 x = *reinterpret_cast<const uint4*>(Z + int64_t(tok[e]) * C + cl);
+        const uint4 x = st[wave][(8 * lg + e) * 16 + lr];
         z[e][0] = x.x;
         z[e][1] = x.y;
         z[e][2] = x.z;
@@ -95,10 +116,7 @@ __device__ __forceinline__ void grad_piece(const LoraGrad& p, const LoraPiece& p
     V sh[JB], sl[JB];
 #pragma unroll
     for (int q = 0; q < JB; ++q) {
-      const int j = j0 + 16 * q + lr;
-      const float* row = St + int64_t(j < p.r ? j : p.r - 1) * p.Tp + at;
-      const float4 a = *reinterpret_cast<const float4*>(row);
-      const float4 b = *reinterpret_cast<const float4*>(row + 4);
+      const float4 a = sv[q][0], b = sv[q][1];
       float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
       uint32_t hi[4], lo[4];
 #pragma unroll
@@ -142,13 +160,53 @@ __device__ __forceinline__ void grad_piece(const LoraGrad& p, const LoraPiece& p
         acc[q][i] = mfma_16x16x32(sl[q], zv, acc[q][i]);
       }
     }
+  };
+  // One step: S of this one, the copies of the next, a wait for all but the
+  // copies, then the products. (Rank blocks past r read the last one again.)
+  auto step = [&](const GradStage& st, GradStage& other, int s) {
+    float4 sv[JB][2];
+    float stp[8];
+#pragma unroll
+    for (int q = 0; q < JB; ++q) {
+      const int jb = j0 / 16 + q < jbs ? q : jbs - 1 - j0 / 16;
+      const float4* src =
+          reinterpret_cast<const float4*>(S + (int64_t(s / 32) * jbs + jb) * 512) + 2 * lane;
+      sv[q][0] = src[0];
+      sv[q][1] = src[1];
+    }
+    if constexpr (X8)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        stp[e] = p.steps[int64_t(tokens[s + 8 * lg + e]) * KB + strip];
+    wait_lds();
+    fence();
+    const int next = s + 32 * kGradWaves;
+    if (next < pc.n) {
+      copy(other, next);
+      fence();
+      wait_vmem<kCopies>();
+    } else {
+      wait_vmem<0>();
+    }
+    fence();
+    use(st, sv, stp, s);
+  };
+  if (32 * wave < pc.n) {
+    copy(z0, 32 * wave);
+    for (int s = 32 * wave; s < pc.n; s += 64 * kGradWaves) {
+      step(z0, z1, s);
+      if (s + 32 * kGradWaves < pc.n) step(z1, z0, s + 32 * kGradWaves);
+    }
   }
+  __syncthreads();
+  float(*const red[2])[kGradStrip] = {reinterpret_cast<float(*)[kGradStrip]>(&z0),
+                                      reinterpret_cast<float(*)[kGradStrip]>(&z1)};
   // lane l holds channel 8·(l % 16) + i and ranks 16·q + 4·(l / 16) + v
   const float post = pc.n ? p.scaling[pc.a] / scale : 0.f;   // no tokens: zeros
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     if (wave >> 1 == half) {
-      float(*R)[kGradStrip + 4] = red[wave & 1];
+      float(*R)[kGradStrip] = red[wave & 1];
 #pragma unroll
       for (int q = 0; q < JB; ++q)
 #pragma unroll
@@ -203,13 +261,16 @@ __device__ __forceinline__ void grad_piece(const LoraGrad& p, const LoraPiece& p
 // Grid: strips of X then of dY; pieces; blocks of 16·JB ranks.
 template <bool F16, bool X8, int JB>
 __global__ __launch_bounds__(64 * kGradWaves, 2) void lora_grad_kernel(LoraGrad p) {
-  __shared__ float red[2][16 * JB][kGradStrip + 4];
+  // separate arrays, so that the compiler can tell the stage being read from
+  // the one being filled
+  __shared__ GradStage z0, z1;
+  __shared__ int tokens[kLoraMaxPiece];
   if (int(blockIdx.y) >= *p.n_pieces) return;
   const LoraPiece pc = p.pieces[blockIdx.y];
   const int64_t sa = p.K / kGradStrip, strip = blockIdx.x;
   const int j0 = int(blockIdx.z) * 16 * JB;
-  if (strip < sa) grad_piece<F16, X8, JB>(p, pc, true, strip, j0, red);
-  else grad_piece<F16, false, JB>(p, pc, false, strip - sa, j0, red);
+  if (strip < sa) grad_piece<F16, X8, JB>(p, pc, true, strip, j0, z0, z1, tokens);
+  else grad_piece<F16, false, JB>(p, pc, false, strip - sa, j0, z0, z1, tokens);
 }
 
 // The sum of a longer run's pieces, in order; 8 values per thread.

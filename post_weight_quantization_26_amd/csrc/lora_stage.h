@@ -25,6 +25,17 @@ __device__ __forceinline__ void wait_vmem() {
   __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
 }
 
+__device__ __forceinline__ void wait_lds() {   // lgkmcnt(0)
+  __builtin_amdgcn_s_waitcnt(0xF | (3 << 14) | (0x7 << 4));
+}
+
+// Keeps memory operations and instructions on their side of it.
+__device__ __forceinline__ void fence() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // Rows of a matrix with `ld` elements per row, as a buffer resource: offsets
 // past the last row read as zero. rows·ld·2 < 2^31.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const uint16_t* base, int64_t rows,

@@ -572,8 +572,8 @@ LoraBackwardLayout lora_backward_layout(int64_t T, int64_t N, int64_t K, int32_t
   // Pieces as long as still gives 1024 workgroups of 128 columns (4 per CU):
   // each piece of a longer run costs its float32 sums once out and in.
   const int64_t strips = ceil_div(K, 128) + ceil_div(N, 128);
-  l.piece = std::min<int64_t>(2048, ceil_div(ceil_div(T * strips, 1024), 32) * 32);
-  l.piece = std::max<int64_t>({l.piece, 128, ceil_div(ceil_div(T, 32768), 32) * 32});
+  l.piece = ceil_div(ceil_div(T * strips, 1024), 32) * 32;
+  l.piece = std::max<int64_t>(128, std::min<int64_t>(kLoraPieceMax, l.piece));
   l.pieces = T / l.piece + L;
   l.slots = T > l.piece ? 2 * (T / l.piece) + 1 : 0;
   size_t off = 0;
@@ -591,8 +591,8 @@ LoraBackwardLayout lora_backward_layout(int64_t T, int64_t N, int64_t K, int32_t
   l.part = take(size_t(l.runs) * t * r * 4);
   l.q = take(t * size_t(lora_q_width(r)) * 2);
   l.e = take(t * 4);
-  l.gt = take(tp * r * 4);
-  l.ht = take(tp * r * 4);
+  l.gs = take(tp * size_t(ceil_div(r, 16) * 16) * 4);
+  l.hs = take(tp * size_t(ceil_div(r, 16) * 16) * 4);
   l.gmax = take(tp * 4);
   l.hmax = take(tp * 4);
   l.token = take(tp * 4);
