@@ -174,12 +174,24 @@ __device__ __forceinline__ uint4 few_operand(const uint32_t (&w)[8], uint32_t z,
 // vector registers make the allocator spill at two waves per SIMD. The
 // compiler puts no wait states around asm: s_nop 1 covers an operand that the
 // instruction before wrote, and few_settle the reads at the end.
-__device__ __forceinline__ void mfma_few(floatx4& c, const bf16x8_t& a, const bf16x8_t& b) {
-  asm("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
-}
-__device__ __forceinline__ void mfma_few(floatx4& c, const f16x8_t& a, const f16x8_t& b) {
-  asm("s_nop 1\n\tv_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
-}
+#define AWQ_FEW_MFMA(TYPE, V)                                                               \
+  __device__ __forceinline__ void mfma_few(floatx4(&c)[2], const V(&a)[2], const V& b) {   \
+    asm("s_nop 1\n\tv_mfma_f32_16x16x32_" TYPE " %0, %2, %4, %0\n\t"                       \
+        "v_mfma_f32_16x16x32_" TYPE " %1, %3, %4, %1"                                       \
+        : "+a"(c[0]), "+a"(c[1])                                                            \
+        : "v"(a[0]), "v"(a[1]), "v"(b));                                                    \
+  }                                                                                         \
+  __device__ __forceinline__ void mfma_few(floatx4(&c)[4], const V(&a)[4], const V& b) {   \
+    asm("s_nop 1\n\tv_mfma_f32_16x16x32_" TYPE " %0, %4, %8, %0\n\t"                       \
+        "v_mfma_f32_16x16x32_" TYPE " %1, %5, %8, %1\n\t"                                   \
+        "v_mfma_f32_16x16x32_" TYPE " %2, %6, %8, %2\n\t"                                   \
+        "v_mfma_f32_16x16x32_" TYPE " %3, %7, %8, %3"                                       \
+        : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3])                                    \
+        : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "v"(b));                              \
+  }
+AWQ_FEW_MFMA("bf16", bf16x8_t)
+AWQ_FEW_MFMA("f16", f16x8_t)
+#undef AWQ_FEW_MFMA
 template <int MT>
 __device__ __forceinline__ void few_settle(floatx4 (&acc)[8][MT]) {
   asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
@@ -202,7 +214,7 @@ __device__ __forceinline__ void few_block(const FewWords& sl, const FewGroup& gr
 #define AWQ_FEW_NIBBLE(R)                                                              \
   {                                                                                    \
     const V b = __builtin_bit_cast(V, few_operand<F16, R>(sl.w, gr.z, sw, base));      \
-    for (int m = 0; m < MT; ++m) mfma_few(acc[R][m], xv[m], b);                        \
+    mfma_few(acc[R], xv, b);                                                           \
   }
   AWQ_FEW_NIBBLE(0) AWQ_FEW_NIBBLE(1) AWQ_FEW_NIBBLE(2) AWQ_FEW_NIBBLE(3)
   AWQ_FEW_NIBBLE(4) AWQ_FEW_NIBBLE(5) AWQ_FEW_NIBBLE(6) AWQ_FEW_NIBBLE(7)

@@ -502,13 +502,13 @@ static int64_t lora_down_runs(int64_t T, int64_t C) {
 // Tiles past a multiple of 256 take as long as 256 of them. Cut into runs they
 // take 1 / runs of that, and their partial tiles (256 KiB out and in) about
 // 0.09 us each, with 4 us for the kernel that adds them; 64 channels of a tile
-// take 1.6 us. Runs of 8 or more 64-wide steps, as many as fill 256 CUs.
+// take 1.6 us. Runs of 2 or more 64-wide steps, as many as fill 256 CUs.
 LoraCut lora_cut(int64_t M, int64_t N, int64_t C) {
   LoraCut c{};
   const int64_t tiles = ceil_div(M, 256) * ceil_div(N, 256), rest = tiles % 256;
   const double whole = 1.6 * double(C / 64);
   double best = whole;
-  for (int64_t runs = 2; rest && runs <= std::min(256 / rest, C / 512); ++runs) {
+  for (int64_t runs = 2; rest && runs <= std::min(256 / rest, C / 128); ++runs) {
     const double t = whole / double(runs) + 0.09 * double(rest * runs) + 4.0;
     if (t < best) {
       best = t;
