@@ -7,7 +7,6 @@ in section 9 (zero point on, group 128, 4 bits).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional, Sequence
 
@@ -384,18 +383,9 @@ def w4a16_matmul(X: torch.Tensor, qweight: torch.Tensor, qzeros: torch.Tensor,
     return Y
 
 
-def _on_device_of(t: torch.Tensor):
-    """Makes t's GPU the current one, so that the stream and the kernels are its."""
-    if t.get_device() == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(t.device)
-
-
-def _check_on(device: int, **tensors) -> None:
-    """Each tensor (or None) is a contiguous one on GPU number ``device``."""
-    for name, t in tensors.items():
-        if t is None:
-            continue
+def _check_on(device: int, names: Sequence[str], tensors) -> None:
+    """Each tensor is a contiguous one on GPU number ``device``."""
+    for name, t in zip(names, tensors):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise ValueError(f"{name} must be a GPU tensor")
         if not t.is_contiguous():
@@ -407,11 +397,21 @@ def _check_on(device: int, **tensors) -> None:
 def _out(t: Optional[torch.Tensor], shape, dtype, like: torch.Tensor, name: str) -> torch.Tensor:
     """The caller's output buffer, checked, or a new one."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    _check_on(like.get_device(), **{name: t})
+        return like.new_empty(shape, dtype=dtype)
+    _check_on(like.get_device(), (name,), (t,))
     if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name} must be {tuple(shape)} {dtype}")
     return t
+
+
+def _call(device: int, fn, *args) -> None:
+    """One call of the library on the current stream of GPU number ``device``,
+    which need not be the current GPU."""
+    if device == torch.cuda.current_device():
+        L.check(fn(*args, torch._C._cuda_getCurrentRawStream(device)))
+        return
+    with torch.cuda.device(device):
+        L.check(fn(*args, torch._C._cuda_getCurrentRawStream(device)))
 
 
 def _at(t: Optional[torch.Tensor]):
@@ -430,16 +430,14 @@ def w4a16_lora_backward_workspace_bytes(T: int, N: int, K: int, L_: int, r: int,
     return int(L.lib().awq_w4a16_lora_backward_workspace_bytes(T, N, K, L_, r, _DT[dtype]))
 
 
+_LORA_NAMES = ("qweight", "qzeros", "scales", "A", "B", "scaling", "ids")
+
+
 def _lora_args(V: torch.Tensor, V_cols: str, qweight, qzeros, scales, A, B, scaling, ids,
                group: int):
     """Checks what the forward and the backward call share; (T, N, K, L, r)."""
     _dev(V, V_cols)
-    _check_on(V.get_device(), qweight=qweight, qzeros=qzeros, scales=scales, A=A, B=B,
-              scaling=scaling, ids=ids)
-    for name, t in (("qweight", qweight), ("qzeros", qzeros), ("scales", scales), ("A", A),
-                    ("B", B), ("scaling", scaling), ("ids", ids)):
-        if t is None:
-            raise ValueError(f"{name} must be a GPU tensor")
+    _check_on(V.get_device(), _LORA_NAMES, (qweight, qzeros, scales, A, B, scaling, ids))
     if V.dim() != 2 or qweight.dim() != 2 or scales.dim() != 2 or A.dim() != 3:
         raise ValueError(f"{V_cols}, qweight and scales must have 2 dimensions, A 3")
     T, K, N = V.shape[0], qweight.shape[0], scales.shape[1]
@@ -481,13 +479,12 @@ def w4a16_lora_matmul(X: torch.Tensor, qweight: torch.Tensor, qzeros: torch.Tens
         steps = _out(x8[1], (T, K // 128), torch.float32, X, "x8 steps")
     if ws is None:
         ws = _workspace(ws, w4a16_lora_workspace_bytes(T, N, K, n, r, X.dtype), X.device)
-    _check_on(X.get_device(), ws=ws)
-    with _on_device_of(X):
-        L.check(L.lib().awq_w4a16_lora_matmul(
-            X.data_ptr(), _dtype(X), T, N, K, qweight.data_ptr(), qzeros.data_ptr(),
-            scales.data_ptr(), int(group), A.data_ptr(), B.data_ptr(), scaling.data_ptr(),
-            ids.data_ptr(), n, r, Y.data_ptr(), _at(h), _at(codes), _at(steps), ws.data_ptr(),
-            ws.numel() * ws.element_size(), torch.cuda.current_stream().cuda_stream))
+    device = X.get_device()
+    _check_on(device, ("ws",), (ws,))
+    _call(device, L.lib().awq_w4a16_lora_matmul, X.data_ptr(), _dtype(X), T, N, K,
+          qweight.data_ptr(), qzeros.data_ptr(), scales.data_ptr(), int(group), A.data_ptr(),
+          B.data_ptr(), scaling.data_ptr(), ids.data_ptr(), n, r, Y.data_ptr(), _at(h),
+          _at(codes), _at(steps), ws.data_ptr(), ws.nbytes)
     return Y
 
 
@@ -515,7 +512,10 @@ def w4a16_lora_backward(dY: torch.Tensor, X, h: torch.Tensor, qweight: torch.Ten
     if X.shape != (T, K):
         raise ValueError("X must be [T, K]")
     _dev(h, "h")
-    _check_on(dY.get_device(), X=X, steps=steps, h=h)
+    device = dY.get_device()
+    _check_on(device, ("X", "h"), (X, h))
+    if steps is not None:
+        _check_on(device, ("steps",), (steps,))
     if h.shape != (T, r) or h.dtype != torch.float32:
         raise ValueError("h must be [T, r] float32")
     dX, dA, dB = out if out is not None else (None, None, None)
@@ -525,14 +525,11 @@ def w4a16_lora_backward(dY: torch.Tensor, X, h: torch.Tensor, qweight: torch.Ten
     if ws is None:
         ws = _workspace(ws, w4a16_lora_backward_workspace_bytes(T, N, K, n, r, dY.dtype),
                         dY.device)
-    _check_on(dY.get_device(), ws=ws)
-    with _on_device_of(dY):
-        L.check(L.lib().awq_w4a16_lora_backward(
-            dY.data_ptr(), X.data_ptr(), _at(steps), h.data_ptr(), _dtype(dY), T, N, K,
-            qweight.data_ptr(), qzeros.data_ptr(), scales.data_ptr(), int(group), A.data_ptr(),
-            B.data_ptr(), scaling.data_ptr(), ids.data_ptr(), n, r, _at(dX), dA.data_ptr(),
-            dB.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
-            torch.cuda.current_stream().cuda_stream))
+    _check_on(device, ("ws",), (ws,))
+    _call(device, L.lib().awq_w4a16_lora_backward, dY.data_ptr(), X.data_ptr(), _at(steps),
+          h.data_ptr(), _dtype(dY), T, N, K, qweight.data_ptr(), qzeros.data_ptr(),
+          scales.data_ptr(), int(group), A.data_ptr(), B.data_ptr(), scaling.data_ptr(),
+          ids.data_ptr(), n, r, _at(dX), dA.data_ptr(), dB.data_ptr(), ws.data_ptr(), ws.nbytes)
     return dX, dA, dB
 
 
@@ -545,10 +542,8 @@ def act_pack8(X: torch.Tensor, out=None):
     codes, steps = out if out is not None else (None, None)
     codes = _out(codes, (T, K), torch.int8, X, "codes")
     steps = _out(steps, (T, K // 128), torch.float32, X, "steps")
-    with _on_device_of(X):
-        L.check(L.lib().awq_act_pack8(X.data_ptr(), _dtype(X), T, K, codes.data_ptr(),
-                                      steps.data_ptr(),
-                                      torch.cuda.current_stream().cuda_stream))
+    _call(X.get_device(), L.lib().awq_act_pack8, X.data_ptr(), _dtype(X), T, K, codes.data_ptr(),
+          steps.data_ptr())
     return codes, steps
 
 
@@ -561,10 +556,10 @@ def act_unpack8(codes: torch.Tensor, steps: torch.Tensor, dtype: torch.dtype,
     if codes.dtype != torch.int8 or steps.dtype != torch.float32 or steps.shape != (T, K // 128):
         raise ValueError("a checkpoint is (codes [T, K] int8, steps [T, K / 128] float32)")
     X = _out(out, (T, K), dtype, codes, "out")
-    _check_on(codes.get_device(), steps=steps)
-    with _on_device_of(codes):
-        L.check(L.lib().awq_act_unpack8(codes.data_ptr(), steps.data_ptr(), _dtype(X), T, K,
-                                        X.data_ptr(), torch.cuda.current_stream().cuda_stream))
+    device = codes.get_device()
+    _check_on(device, ("steps",), (steps,))
+    _call(device, L.lib().awq_act_unpack8, codes.data_ptr(), steps.data_ptr(), _dtype(X), T, K,
+          X.data_ptr())
     return X
 
 
