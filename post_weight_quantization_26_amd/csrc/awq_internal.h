@@ -216,8 +216,12 @@ struct LoraCut {
   size_t bytes;   // their partial tiles
 };
 LoraCut lora_cut(int64_t M, int64_t N, int64_t C);
-// Token rows up to which the forward call runs without a dequantised layer.
-constexpr int64_t kLoraFewMaxT = 256;
+// Token rows up to which the forward call runs without a dequantised layer: it
+// dequantises for every 64 of them, but in registers, and writes no layer.
+// Without / with one, bf16, rank 16: 256 tokens 40 / 65 us (4096x4096), 72 / 88
+// (11008x4096), 225 / 312 (28672x8192); 384 tokens 50 / 66, 108 / 104, 333 /
+// 388; 512 tokens 58 / 68, 122 / 107, 412 / 395.
+constexpr int64_t kLoraFewMaxT = 384;
 struct LoraLayout {
   size_t partial; // few tokens: [S, T, N] f32 sums of the shared product, ..
   size_t hpart;   // .. and [S2, T, r] f32 of the narrow one
