@@ -32,22 +32,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   else return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, b16x2));
 }
 
-// The least id of this wave's lanes that is above `prev` and below L, or L
-// when there is none (ids < 0 never count: prev starts at -1). The same value
-// in every lane; `id2` is a second id of the lane (or -1).
-__device__ __forceinline__ int next_adapter(int id, int id2, int prev, int L) {
-  int m = id > prev && id < L ? id : L;
-  const int m2 = id2 > prev && id2 < L ? id2 : L;
-  m = m < m2 ? m : m2;
-#pragma unroll
-  for (int o = 32; o; o >>= 1) {
-    const int u = __shfl_xor(m, o);
-    m = m < u ? m : u;
-  }
-  return __builtin_amdgcn_readfirstlane(m);
-}
-
-// 2^e of a float32 magnitude's exponent, clamped to [-60, 60] (0 and values
+// The exponent e of a float32 magnitude in [2^e, 2^(e+1)), clamped to [-60, 60] (0 and values
 // that are not finite: 0).
 __device__ __forceinline__ int exponent_of(float m) {
   if (!(m > 0.f) || !(m < __builtin_inff())) return 0;

@@ -53,18 +53,23 @@ typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 // launch 1: the narrow product
 // ---------------------------------------------------------------------------
 
-// Workgroup (tile of 16 tokens, row, block of 16 ranks, run of k): if `row` is
-// the first of the tile with its adapter, the adapter's 16 x 16 block of P for
-// all rows of the tile that have it, as a float32 partial sum.
-__device__ __forceinline__ void few_down_index(const LoraFew& p, int id, int& tile, int& row,
+// Slots for the distinct adapters of a tile of 16 tokens.
+__host__ __device__ inline int few_slots(const LoraFew& p) {
+  const int rows = p.T < 16 ? int(p.T) : 16;
+  return rows < p.s.L ? rows : p.s.L;
+}
+// Workgroup (tile of 16 tokens, slot, block of 16 ranks, run of k): the 16 x 16
+// block of P of the tile's slot-th adapter for all rows that have it, as a
+// float32 partial sum.
+__device__ __forceinline__ void few_down_index(const LoraFew& p, int id, int& tile, int& slot,
                                                int& jb, int& ks) {
-  const int jbs = (p.s.r + 15) / 16, rows = p.T < 16 ? int(p.T) : 16;
+  const int jbs = (p.s.r + 15) / 16, slots = few_slots(p);
   ks = id % p.S2;
   id /= p.S2;
   jb = id % jbs;
   id /= jbs;
-  row = id % rows;
-  tile = id / rows;
+  slot = id % slots;
+  tile = id / slots;
 }
 
 // A wave's stage: a 16-row tile of X and one of A (lora_stage.h).
@@ -77,15 +82,21 @@ template <bool F16>
 __device__ __forceinline__ void few_down(const LoraFew& p, int id, FewStage s0, FewStage s1,
                                          FewRed& red) {
   typedef typename Operand<F16>::type V;
-  int tile, row, jb, ks;
-  few_down_index(p, id, tile, row, jb, ks);
+  int tile, slot, jb, ks;
+  few_down_index(p, id, tile, slot, jb, ks);
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
   const int64_t t0 = int64_t(tile) * 16, K = p.w.K;
   const int my = t0 + lr < p.T ? p.s.ids[t0 + lr] : -1;
-  const int a = __builtin_amdgcn_readlane(my, row);
-  const uint32_t mine = uint32_t(__ballot(my == a)) & 0xFFFFu;
-  if (a < 0 || a >= p.s.L || int(__builtin_ctz(mine)) != row) return;
+  uint32_t left = uint32_t(__ballot(my >= 0 && my < p.s.L)) & 0xFFFFu, mine;
+  int a;
+  while (true) {
+    if (!left) return;
+    a = __builtin_amdgcn_readlane(my, __builtin_ctz(left));
+    mine = uint32_t(__ballot(my == a)) & 0xFFFFu;
+    if (slot-- == 0) break;
+    left &= ~mine;
+  }
   const int nb = int(K / 128), b0 = int(int64_t(nb) * ks / p.S2),
             b1 = int(int64_t(nb) * (ks + 1) / p.S2);
   const int64_t rows = p.T - t0 < 16 ? p.T - t0 : 16;
@@ -443,8 +454,9 @@ __device__ __forceinline__ void few_product(const LoraFew& p, int id, int blocks
       stage(q1, g1, kb + 64);
     }
     wait_vmem<0>();
+    // here, not behind the branch: there the compiler may copy accumulators first
+    few_settle<MT>(acc);
   }
-  few_settle<MT>(acc);
   // The waves meet in LDS, a quarter of the outputs (nibbles 2u, 2u + 1 of the
   // words) at a time: in step i wave w adds quarter (w + i) % 4, so all four
   // work and an output's order depends on nothing but its column. Lane l holds
@@ -718,8 +730,8 @@ void launch_decode(const LoraFew& p, int downs, int gx, int gy, hipStream_t st) 
 
 template <bool F16>
 hipError_t launch_few(LoraFew p, hipStream_t st) {
-  const int jbs = (p.s.r + 15) / 16, rows = p.T < 16 ? int(p.T) : 16;
-  const int downs = int((p.T + 15) / 16) * rows * jbs * p.S2;
+  const int jbs = (p.s.r + 15) / 16;
+  const int downs = int((p.T + 15) / 16) * few_slots(p) * jbs * p.S2;
   if (p.T <= 16 && p.gemv) {
     const hipError_t e =
         launch_w4a16_gemv(p.X, p.T, p.w.N, p.w.K, p.w.qweight, p.w.qzeros, p.w.scales,
