@@ -401,6 +401,124 @@ def test_search_pack_then_train_adapters(api):
     assert torch.equal(A[1], A1) and not B[1].any() and B[0].any() and B[2].any()
 
 
+# Where one form of the call ends and another begins, and the forms that the
+# sizes above do not reach: 16-byte copies of the words with groups of 32, word
+# by word with groups of 32 and few tokens, the last size without a
+# dequantised layer and the first with one, tiles cut into runs.
+@pytest.mark.parametrize("T,N,K,r,L,dtype,group,kind", [
+    (24, 544, 640, 32, 3, "f16", 32, "tokens"),
+    (32, 512, 1152, 16, 2, "bf16", 32, "tokens"),
+    (20, 264, 384, 24, 2, "bf16", 32, "runs"),
+    (48, 288, 384, 8, 20, "bf16", 32, "tokens"),
+    (384, 520, 896, 48, 3, "f16", 64, "runs"),
+    (385, 520, 896, 48, 3, "f16", 64, "runs"),
+    (640, 512, 1152, 24, 1500, "bf16", 128, "tokens"),
+    (16, 512, 384, 16, 4096, "bf16", 128, "tokens"),
+])
+def test_forward_forms(api, T, N, K, r, L, dtype, group, kind):
+    check_forward(api, Problem(T, N, K, r, L, dtype, group, kind, seed=T + N + 1))
+
+
+# Runs longer than a piece (several pieces and a last short one), thousands of
+# adapters (most without tokens), and both at once.
+@pytest.mark.parametrize("T,N,K,r,L,dtype,kind,x8", [
+    (5000, 264, 128, 8, 1, "bf16", "one", False),
+    (4500, 128, 256, 24, 2, "f16", "runs", True),
+    (3000, 136, 128, 16, 1500, "bf16", "tokens", False),
+    (4099, 128, 128, 8, 4096, "f16", "runs", True),
+])
+def test_backward_pieces_and_adapters(api, T, N, K, r, L, dtype, kind, x8):
+    check_backward(api, Problem(T, N, K, r, L, dtype, kind=kind, seed=T + N), x8)
+
+
+def test_offsets_past_32_bits(api):
+    """Outputs and gradients of more than 2^31 elements: the rows behind the
+    2^31st are those of a call on them alone, within both calls' bounds."""
+    T, N, K, r, L = 70000, 32768, 128, 8, 2
+    p = Problem(512, N, K, r, L, "bf16", kind="tokens", seed=9)
+    p.ids[:] = 1
+    lay, (A, B, c, ids) = p.layer(), p.lora()
+    tail, h1 = p.td(p.Xb), torch.empty(512, r, device="cuda:0")
+    X = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda:0")
+    X[-512:] = tail
+    ids_all = torch.zeros(T, dtype=torch.int32, device="cuda:0")
+    ids_all[-512:] = 1
+    h = torch.empty(T, r, device="cuda:0")
+    Y = api.w4a16_lora_matmul(X, *lay, A, B, c, ids_all, h=h)
+    y = api.w4a16_lora_matmul(tail, *lay, A, B, c, ids, h=h1)
+    torch.cuda.synchronize()
+    want, _, _, ml, mw = R.forward(p.x, p.w, p.A, p.B, p.c.astype(np.float64), p.ids)
+    bound = ((R.UOUT["bf16"] + R.gamma(K)) * mw + (R.LOW["bf16"] + R.gamma(K + r + 4)) * ml +
+             R.UOUT["bf16"] * np.abs(want) + R.TINY["bf16"])
+    assert worst(f64(Y[-512:]), want, bound) <= 1 and worst(f64(y), want, bound) <= 1
+    assert not Y[:512].any() and not Y[34000:34512].any()
+    del Y, y
+    dY = torch.zeros(T, N, dtype=torch.bfloat16, device="cuda:0")
+    dY[-512:] = p.td(p.dYb)
+    dX, dA, dB = api.w4a16_lora_backward(dY, X, h, *lay, A, B, c, ids_all)
+    torch.cuda.synchronize()
+    hr = f64(h1)
+    dx, da, db, mw, mgx, mA, mB = R.backward(p.dy, p.x, hr, p.w, p.A, p.B,
+                                             p.c.astype(np.float64), p.ids)
+    u, low, tiny = R.UOUT["bf16"], R.LOW["bf16"], R.TINY["bf16"]
+    assert torch.equal(h[-512:], h1)
+    assert worst(f64(dX[-512:]), dx, (u + R.gamma(N)) * mw +
+                 (low + R.gamma(N + r + 4)) * mgx + u * np.abs(dx) + tiny) <= 1
+    assert worst(f64(dA), da, (low + R.gamma(N + T + 4)) * mA + u * np.abs(da) + tiny) <= 1
+    assert worst(f64(dB), db, (low + R.gamma(T + 4)) * mB + u * np.abs(db) + tiny) <= 1
+    assert not dX[:-512].any()
+
+
+def test_a_broken_checkpoint_block_stays_in_its_gradient(api):
+    """A block whose activations were not finite (step NaN) makes its adapter's
+    dA of those 128 channels NaN and nothing else."""
+    p = Problem(100, 264, 384, 16, 3, "bf16", kind="tokens", seed=4)
+    p.ids[:3] = [0, 1, 2]
+    X, dY, h = p.td(p.Xb), p.td(p.dYb), dev(np.ones((100, 16), np.float32))
+    lay, lora = p.layer(), p.lora()
+    x8 = api.act_pack8(X)
+    dx0, da0, db0 = api.w4a16_lora_backward(dY, x8, h, *lay, *lora)
+    X[1, 200] = float("inf")
+    x8 = api.act_pack8(X)
+    assert torch.isnan(x8[1][1, 1]) and not x8[0][1, 128:256].any()
+    dx, da, db = api.w4a16_lora_backward(dY, x8, h, *lay, *lora)
+    torch.cuda.synchronize()
+    assert torch.equal(dx, dx0) and torch.equal(db, db0)
+    assert torch.isnan(da[1, :, 128:256]).all()
+    da[1, :, 128:256] = da0[1, :, 128:256]
+    assert torch.equal(da, da0)
+
+
+def test_python_refuses_wrong_tensors(api):
+    p = Problem(20, 264, 384, 16, 3, "bf16", kind="tokens", seed=1)
+    X, lay, (A, B, c, ids) = p.td(p.Xb), p.layer(), p.lora()
+    ok = dict(X=X, A=A, B=B, c=c, ids=ids, ws=None, h=None, x8=None)
+
+    def call(**kw):
+        a = {**ok, **kw}
+        return api.w4a16_lora_matmul(a["X"], *lay, a["A"], a["B"], a["c"], a["ids"], ws=a["ws"],
+                                     h=a["h"], x8=a["x8"])
+    call()
+    z = lambda *s, dt=torch.float32: torch.zeros(*s, dtype=dt, device="cuda:0")
+    for bad in (dict(X=X.half()), dict(X=X[:, :256]), dict(X=X.cpu()), dict(A=A[:, :, :256]),
+                dict(B=B[:2]), dict(A=A.half()), dict(c=c[:2]), dict(c=c.double()),
+                dict(ids=ids.long()), dict(ids=ids[:-1]), dict(ids=ids.cpu()),
+                dict(h=z(20, 8)), dict(h=z(20, 16, dt=torch.bfloat16)),
+                dict(x8=(z(20, 384, dt=torch.int8), z(20, 2))),
+                dict(ws=z(16, dt=torch.uint8))):
+        with pytest.raises(Exception) as e:
+            call(**bad)
+        assert not isinstance(e.value, (AttributeError, IndexError, KeyError)), (bad, e.value)
+    h = z(20, 16)
+    dY = p.td(p.dYb)
+    for bad in (dict(dY=dY[:-1]), dict(dY=dY.half()), dict(h=h[:, :8]), dict(h=h.half())):
+        a = {"dY": dY, "h": h, **bad}
+        with pytest.raises(Exception) as e:
+            api.w4a16_lora_backward(a["dY"], X, a["h"], *lay, A, B, c, ids)
+        assert not isinstance(e.value, (AttributeError, IndexError, KeyError)), (bad, e.value)
+    torch.cuda.synchronize()
+
+
 # ------------------------------------------------------------- checkpoints
 
 def special_rows(T, K, rng):
