@@ -405,8 +405,12 @@ awq_status awq_w4a16_matmul(const void* X, awq_dtype dtype, int64_t T, int64_t N
  * H [T, r] f32 receives the h_t, and x8_codes [T, K] int8 with x8_steps
  * [T, K/128] f32 the 8-bit checkpoint of X that awq_act_pack8 would write
  * (both or neither).
- * Sums are float32 and each output is rounded once; an adapter's NaN or
- * infinity reaches its own tokens only. N a multiple of 8, K of 128, both
+ * Sums are float32 and each output is rounded once. T <= 16 uses the exact Ŵ
+ * in float32, larger T Ŵ rounded once to X's type; h_t meets B_a as the sum of
+ * two 16-bit halves (2^-16 of it is lost with bf16, 2^-22 with fp16). An
+ * adapter's NaN or infinity reaches its own tokens only, whose outputs in the
+ * rows of B_a (columns of A_a, in the gradient) that hold it are then NaN or
+ * infinite. N a multiple of 8, K of 128, both
  * and T within awq_w4a16_matmul's limits. X, qweight, qzeros, scales, A, B,
  * Y, H, x8_codes and ws 16-byte aligned, scaling, ids and x8_steps 4-byte.
  * Outputs may not overlap inputs. ws: at least
