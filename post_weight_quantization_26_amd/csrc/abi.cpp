@@ -847,9 +847,9 @@ extern "C" awq_status awq_w4a16_lora_backward(
   pr.piece = int(l.piece);
   pr.f16 = f16;
   pr.dY = static_cast<const uint16_t*>(dY);
-  pr.Wt = dX ? at<uint16_t>(ws, l.wt) : nullptr;
+  pr.Wt = dX && !l.few ? at<uint16_t>(ws, l.wt) : nullptr;
   pr.Bt = at<uint16_t>(ws, l.bt);
-  pr.At = at<uint16_t>(ws, l.at);
+  pr.At = dX ? at<uint16_t>(ws, l.at) : nullptr;
   pr.dYp = padded ? at<uint16_t>(ws, l.dyp) : nullptr;
   pr.token = at<int>(ws, l.token);
   pr.pos = at<int>(ws, l.pos);
@@ -874,15 +874,38 @@ extern "C" awq_status awq_w4a16_lora_backward(
   d.Ps = at<float>(ws, l.gs);
   d.row_max = at<float>(ws, l.gmax);
   d.pos = pr.pos;
-  d.Q = at<uint16_t>(ws, l.q);
-  d.RW = lora_q_width(r);
-  d.E = at<float>(ws, l.e);
+  if (dX && !l.few) {
+    d.Q = at<uint16_t>(ws, l.q);
+    d.RW = lora_q_width(r);
+    d.E = at<float>(ws, l.e);
+  }
   d.Hin = H;
   d.Hs = at<float>(ws, l.hs);
   d.h_max = at<float>(ws, l.hmax);
 
   const LoraUp u{d.Q, d.E, ids, pr.At, L, r, d.RW};
   const LoraSplit cut{int(l.cut.full), int(l.cut.runs), at<float>(ws, l.tiles_part)};
+
+  LoraFewBack f{};
+  LoraFew up{};      // Aᵀ in B's place
+  if (l.few) {
+    f.dY = d.V;
+    f.T = up.T = T;
+    f.Np = l.Np;
+    f.w = pr.w;
+    f.partial = up.partial = at<float>(ws, l.sums);
+    f.S = up.S = int(l.S);
+    f.npw = int(l.npw);
+    f.tiles = int(l.tiles);
+    f.col_blocks = int(l.col_blocks);
+    f.gshift = group_size == 32 ? 5 : group_size == 64 ? 6 : 7;
+    f.f16 = up.f16 = f16;
+    up.w.N = K;
+    up.s = {nullptr, pr.At, scaling, ids, L, r};
+    up.hpart = d.part;
+    up.S2 = d.S;
+    up.Y = static_cast<uint16_t*>(dX);
+  }
 
   LoraGrad g{};
   g.dY = pr.dY;
@@ -911,7 +934,10 @@ extern "C" awq_status awq_w4a16_lora_backward(
                 [&] {
                   hipError_t e = launch_lora_prep(pr, st);
                   if (e == hipSuccess) e = launch_lora_down(d, st);
-                  if (e == hipSuccess && dX)
+                  if (e == hipSuccess && dX && l.few) {
+                    e = launch_lora_few_back(f, st);
+                    if (e == hipSuccess) e = launch_lora_few_finish(up, st);
+                  } else if (e == hipSuccess && dX)
                     e = launch_lora_gemm(d.V, l.Np, pr.Wt, l.Np, T, K, l.Np, u, cut, f16,
                                          static_cast<uint16_t*>(dX), st);
                   if (e == hipSuccess)

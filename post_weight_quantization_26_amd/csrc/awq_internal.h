@@ -222,6 +222,10 @@ LoraCut lora_cut(int64_t M, int64_t N, int64_t C);
 // (11008x4096), 225 / 312 (28672x8192); 384 tokens 50 / 66, 108 / 104, 333 /
 // 388; 512 tokens 58 / 68, 122 / 107, 412 / 395.
 constexpr int64_t kLoraFewMaxT = 384;
+// The same for the whole gradient: 64 tokens 38 / 55 us (4096x4096), 50 / 74
+// (11008x4096), 91 / 265 (28672x8192); 256 tokens 57 / 62, 78 / 88, 197 / 283;
+// 320 tokens 65 / 65, 87 / 95, 302 / 339; 384 tokens 69 / 66, 101 / 95, 309 / 339.
+constexpr int64_t kLoraFewBackMaxT = 320;
 struct LoraLayout {
   size_t partial; // few tokens: [S, T, N] f32 sums of the shared product, ..
   size_t hpart;   // .. and [S2, T, r] f32 of the narrow one
@@ -240,6 +244,9 @@ LoraLayout lora_layout(int64_t T, int64_t N, int64_t K, int32_t L, int32_t r);
 // at most `pieces` of them; runs of more than one leave partial sums.
 struct LoraBackwardLayout {
   int64_t Np, Tp;             // N padded to 128; sorted positions
+  bool few;                   // no dequantised layer; else S .. col_blocks are 0
+  int64_t S, npw, tiles, col_blocks;
+  size_t sums;                // few: [S, T, K] f32 sums of the shared product
   int64_t piece, pieces, slots;
   size_t wt, bt, at, dyp;     // 16-bit: Ŵᵀ [K, Np], Bᵀ [L, r, Np], Aᵀ [L, K, r], dY [T, Np]
   int64_t runs;

@@ -41,7 +41,7 @@ struct LoraDown {
   float* row_max;         // [Tp] max_j |P| at pos[t]
   float* h_max;           // [Tp] max_j |Hin|
   const int32_t* pos;
-  uint16_t* Q;            // [T, RW]: c·P as halves hi [r], lo [r], zeros up to RW
+  uint16_t* Q;            // [T, RW]: c·P as halves hi [r], lo [r], zeros up to RW, or NULL
   int RW;                 // 2r rounded up to 64
   float* E;               // [T] the power of two that Q is scaled down by
   int8_t* codes;          // [T, C] 8-bit checkpoint of V, or NULL
@@ -93,6 +93,20 @@ struct LoraFew {
   int gshift, gemv, f16;  // log2 of the group; T <= 16: the float32 decode
 };
 hipError_t launch_lora_few(const LoraFew& p, hipStream_t st);
+// Its second launch alone.
+hipError_t launch_lora_few_finish(const LoraFew& p, hipStream_t st);
+
+// Few tokens, the shared product of the gradient (lora_few_back.hip).
+struct LoraFewBack {
+  const uint16_t* dY;     // [T, Np], zeros past N
+  int64_t T, Np;
+  LoraLayer w;
+  float* partial;         // [S, T, K]
+  int S, npw;             // runs of n; n per wave
+  int tiles, col_blocks;
+  int gshift, f16;
+};
+hipError_t launch_lora_few_back(const LoraFewBack& p, hipStream_t st);
 
 // A piece of one adapter's run of sorted tokens: positions pos .. pos + n - 1;
 // slot of its partial sums, or -1 where it is the whole run.
@@ -108,9 +122,9 @@ struct LoraPrep {
   int64_t T, Np;          // Np: N rounded up to 128
   int piece, f16;
   const uint16_t* dY;
-  uint16_t* Wt;           // [K, Np], or NULL (no dX: then no At either)
+  uint16_t* Wt;           // [K, Np], or NULL
   uint16_t* Bt;           // [L, r, Np]
-  uint16_t* At;           // [L, K, r]
+  uint16_t* At;           // [L, K, r], or NULL
   uint16_t* dYp;          // [T, Np], or NULL where N = Np
   int* token;             // [Tp] token at each position
   int* pos;               // [T] position of each token with an adapter

@@ -162,8 +162,8 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(LoraDown p) {
 }
 
 // A wave per token: the sum of its partial sums, in order, as H, in the
-// gradients' operand order (with Hin in the same), and as the wide product's operand c_a·P in two 16-bit halves hi = rnd(v), lo =
-// rnd(v - hi), which lose at most u² (bf16: 2^-16) of v. fp16 halves are
+// gradients' operand order (with Hin in the same), and as the wide product's
+// operand c_a·P in two 16-bit halves hi = rnd(v), lo = rnd(v - hi), which lose at most u² (bf16: 2^-16) of v. fp16 halves are
 // scaled by a power of two where a row's largest value lies outside [2^-3,
 // 2^14), so that neither half overflows and lo keeps 2^-22 of the largest.
 template <bool F16>
@@ -214,14 +214,16 @@ __global__ __launch_bounds__(256) void lora_combine_kernel(LoraDown p) {
       p.Ps[at] = v[k];
       p.Hs[at] = h[k];
     }
+    if (!p.Q) continue;
     const float s = c * v[k] * down;
     const uint16_t hi = round16<F16>(s);
     q[j] = hi;
     q[p.r + j] = round16<F16>(s - widen16<F16>(hi));
   }
-  for (int j = 2 * p.r + lane; j < p.RW; j += 64) q[j] = 0;
+  if (p.Q)
+    for (int j = 2 * p.r + lane; j < p.RW; j += 64) q[j] = 0;
   if (lane == 0) {
-    p.E[t] = exp2i(e);
+    if (p.Q) p.E[t] = exp2i(e);
     if (p.Ps) {
       p.row_max[pos] = m;
       p.h_max[pos] = mh;

@@ -35,19 +35,12 @@
 // (55 against 44 us for 200 tokens of 4096x11008).
 #include <type_traits>
 
-#include "gemm_types.h"
 #include "lora.h"
-#include "lora_common.h"
-#include "lora_stage.h"
+#include "lora_few.h"
 #include "w4a16_mgemv.h"
 
 namespace awq {
 namespace {
-
-constexpr int kFewWaves = 4;
-constexpr int kFewCols = 128;     // outputs per workgroup (T > 16)
-
-typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 
 // ---------------------------------------------------------------------------
 // launch 1: the narrow product
@@ -145,12 +138,9 @@ __device__ __forceinline__ void few_down(const LoraFew& p, int id, FewStage s0, 
 // launch 1: the shared product, T > 16
 // ---------------------------------------------------------------------------
 
-// Stages of 64 k rows. Per wave: 16·MT tokens x 64 channels of X (rows of 8
-// chunks of 16 bytes, chunk c of row i at c ^ (i / 2) % 8), and the packed
-// words, for each block of 32 k rows in the order of their use: word e of lane
-// l (k row 8·(l / 16) + e, word column l % 16) at 64·e + l.
-template <int MT>
-using FewX = uint4[kFewWaves][16 * MT * 8];
+// Stages of 64 k rows. The packed words of a wave lie, for each block of 32 k
+// rows, in the order of their use: word e of lane l (k row 8·(l / 16) + e, word
+// column l % 16) at 64·e + l.
 typedef uint4 FewQ[kFewWaves][2 * 128];
 
 // The zero points and scales of the group that one (group size 32) or two (64,
@@ -187,109 +177,26 @@ __device__ __forceinline__ void few_zeros(FewZeros<F16>& n, const FewGroup& gr,
     few_zeros<F16, R + 1>(n, gr, base);
   }
 }
-// Pair E of nibble R's operand (k rows 2E, 2E + 1) before its rounding: two
-// float32 numbers, or (fp16) what it is.
-template <bool F16, int R, int E>
-__device__ __forceinline__ void few_pair(uint32_t& lo, uint32_t& hi, const uint32_t (&w)[8],
-                                         const FewZeros<F16>& n, const FewGroup& gr,
-                                         const uint32_t (&base)[2]) {
-  const f16x2_t q = few_code<R>(w[2 * E], w[2 * E + 1], base);
-  const _Float16 s = few_scale<R>(gr);
-  if constexpr (F16) {
-    lo = __builtin_bit_cast(uint32_t, (q - n.v[R]) * f16x2_t{s, s});
-  } else {
-    lo = __builtin_bit_cast(uint32_t, __builtin_fmaf(float(q[0]), float(s), n.v[R]));
-    hi = __builtin_bit_cast(uint32_t, __builtin_fmaf(float(q[1]), float(s), n.v[R]));
-  }
-}
+// The operands of a block: nibble R of the 8 words, pair E of k rows 2E, 2E + 1.
 template <bool F16>
-__device__ __forceinline__ uint32_t few_round(uint32_t lo, uint32_t hi) {
-  if constexpr (F16) return lo;
-  else return pack2<false>(__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi));
-}
-
-// The accumulators stay in AGPRs through inline asm: 128 of them among the
-// vector registers make the allocator spill at two waves per SIMD. The
-// compiler puts no wait states around asm: FIRST (the operand was just
-// written) waits for two, and few_settle for the reads at the end.
-template <bool FIRST>
-__device__ __forceinline__ void mfma_few(floatx4& c, const bf16x8_t& a, const bf16x8_t& b) {
-  if constexpr (FIRST)
-    asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
-  else asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
-}
-template <bool FIRST>
-__device__ __forceinline__ void mfma_few(floatx4& c, const f16x8_t& a, const f16x8_t& b) {
-  if constexpr (FIRST)
-    asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
-  else asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
-}
-template <int MT>
-__device__ __forceinline__ void few_settle(floatx4 (&acc)[8][MT]) {
-  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
-#pragma unroll
-  for (int r = 0; r < 8; ++r)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) asm volatile("" : "+a"(acc[r][m]));
-}
-
-// Nibble R's MFMAs, E of 4 / MT pairs of nibble R + 1's operand before each: a
-// matrix instruction takes as long as four vector instructions, which go on
-// beside it. A pair is rounded a step after it is made (the wait between the
-// two would be a cycle lost).
-template <bool F16, int MT, int R, int M, class V>
-__device__ __forceinline__ void few_mfmas(const uint32_t (&w)[8], const FewGroup& gr,
-                                          const FewZeros<F16>& n, const uint32_t (&base)[2],
-                                          const V (&xv)[MT], const V& b, uint32_t (&nb)[4],
-                                          uint32_t (&f)[2], floatx4 (&acc)[MT]) {
-  if constexpr (M < MT) {
-    if constexpr (R < 7) {
-      constexpr int kE = 4 / MT;
-      uint32_t g[2];
-      few_pair<F16, R + 1, M * kE>(g[0], g[1], w, n, gr, base);
-      if constexpr (M > 0) nb[M * kE - 1] = few_round<F16>(f[0], f[1]);
-      if constexpr (kE == 2) {
-        few_pair<F16, R + 1, M * kE + 1>(f[0], f[1], w, n, gr, base);
-        nb[M * kE] = few_round<F16>(g[0], g[1]);
-      } else {
-        f[0] = g[0];
-        f[1] = g[1];
-      }
+struct FewBlock {
+  const uint32_t (&w)[8];
+  const FewGroup& gr;
+  const FewZeros<F16>& n;
+  const uint32_t (&base)[2];
+  __device__ static constexpr int word(int e) { return e; }
+  template <int R, int E>
+  __device__ __forceinline__ void pair(uint32_t& lo, uint32_t& hi) const {
+    const f16x2_t q = few_code<R>(w[2 * E], w[2 * E + 1], base);
+    const _Float16 s = few_scale<R>(gr);
+    if constexpr (F16) {
+      lo = __builtin_bit_cast(uint32_t, (q - n.v[R]) * f16x2_t{s, s});
+    } else {
+      lo = __builtin_bit_cast(uint32_t, __builtin_fmaf(float(q[0]), float(s), n.v[R]));
+      hi = __builtin_bit_cast(uint32_t, __builtin_fmaf(float(q[1]), float(s), n.v[R]));
     }
-    __builtin_amdgcn_sched_barrier(0);
-    mfma_few<M == 0>(acc[M], xv[M], b);
-    __builtin_amdgcn_sched_barrier(0);
-    if constexpr (R < 7 && M == MT - 1) nb[3] = few_round<F16>(f[0], f[1]);
-    few_mfmas<F16, MT, R, M + 1>(w, gr, n, base, xv, b, nb, f, acc);
   }
-}
-template <bool F16, int MT, int R, class V>
-__device__ __forceinline__ void few_nibbles(const uint32_t (&w)[8], const FewGroup& gr,
-                                            const FewZeros<F16>& n, const uint32_t (&base)[2],
-                                            const V (&xv)[MT], uint32_t (&b)[4],
-                                            floatx4 (&acc)[8][MT]) {
-  if constexpr (R < 8) {
-    uint32_t nb[4] = {}, f[2] = {};
-    few_mfmas<F16, MT, R, 0>(w, gr, n, base, xv,
-                             __builtin_bit_cast(V, make_uint4(b[0], b[1], b[2], b[3])), nb, f,
-                             acc[R]);
-    few_nibbles<F16, MT, R + 1>(w, gr, n, base, xv, nb, acc);
-  }
-}
-// A block of 32 k rows.
-template <bool F16, int MT, class V>
-__device__ __forceinline__ void few_block(const uint32_t (&w)[8], const FewGroup& gr,
-                                          const FewZeros<F16>& n, const uint32_t (&base)[2],
-                                          const V (&xv)[MT], floatx4 (&acc)[8][MT]) {
-  uint32_t b[4], f[4][2];
-  few_pair<F16, 0, 0>(f[0][0], f[0][1], w, n, gr, base);
-  few_pair<F16, 0, 1>(f[1][0], f[1][1], w, n, gr, base);
-  few_pair<F16, 0, 2>(f[2][0], f[2][1], w, n, gr, base);
-  few_pair<F16, 0, 3>(f[3][0], f[3][1], w, n, gr, base);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) b[e] = few_round<F16>(f[e][0], f[e][1]);
-  few_nibbles<F16, MT, 0>(w, gr, n, base, xv, b, acc);
-}
+};
 
 // WIDE: N a multiple of 32, rows of packed words 16-byte aligned.
 template <bool F16, int MT, bool G32, bool WIDE>
@@ -322,27 +229,9 @@ __device__ __forceinline__ void few_product(const LoraFew& p, int id, int blocks
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[r][m] = floatx4{0.f, 0.f, 0.f, 0.f};
   if (kw0 < kw1) {
-    // X: copy i takes rows 8i .. + 7 of the tile; the swizzle repeats every 16
-    // rows. Rows past T are zero, or, in a 16-row block past T, the last
-    // block's: they are never stored. Offsets in scalar registers stay inside
-    // the buffer, and so do those in k: stages past the run read its last one.
-    const int rows = int(p.T - t0 < R ? p.T - t0 : R), last = (rows - 1) / 16;
-    const auto rsX = rows_rsrc(p.X + t0 * K, rows, K);
-    uint32_t xoff[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = 8 * i + (lane >> 3);
-      xoff[i] = uint32_t((row * K + ((lane & 7) ^ (row >> 1)) * 8) * 2);
-    }
-    const int xstep = int(16 * K * 2);
-    auto copy_x = [&](int kb) {
-      const int k = kb < kw1 ? kb : kw1 - 64;
-#pragma unroll
-      for (int i = 0; i < 2 * MT; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rsX, AWQ_LORA_LDS(sx[wave] + 64 * i), 16, xoff[i & 1],
-            (i / 2 < last ? i / 2 : last) * xstep + 2 * k, 0, 0);
-    };
+    const FewRows x = few_rows<MT>(p.X, t0, p.T, K);
+    // (stages past the run read its last one)
+    auto copy_x = [&](int kb) { few_copy_rows<MT>(x, sx[wave], kb < kw1 ? kb : kw1 - 64); };
     // The wave's rows of packed words (at most a quarter of N·K / 2 <= 2^33
     // bytes). WIDE: four words a lane; words past the row are the next row's
     // (or, past the last row, zero), and never stored. Else one word a lane,
@@ -396,10 +285,6 @@ __device__ __forceinline__ void few_product(const LoraFew& p, int id, int blocks
     // a scalar one, and-or is one instruction)
     uint32_t base[2] = {0x64006400u, 0x54005400u};
     asm volatile("" : "+v"(base[0]), "+v"(base[1]));
-    // where the lane's operand of block h lies in a stage of X
-    uint32_t xat[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) xat[h] = uint32_t(lr * 8 + ((4 * h + lg) ^ (lr >> 1)));
     FewGroup g0[kGroups], g1[kGroups];
     // A stage's X is copied a stage ahead, its words and groups two. A wave
     // reads only what it copied itself: waits, no barriers. The order of the
@@ -428,7 +313,7 @@ __device__ __forceinline__ void few_product(const LoraFew& p, int id, int blocks
           w[h][e] = reinterpret_cast<const uint32_t*>(st[wave])[512 * h + 64 * e + lane];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
-          xv[h][m] = __builtin_bit_cast(V, sx[wave][xat[h] + 128 * m]);
+          xv[h][m] = __builtin_bit_cast(V, sx[wave][x.at[h] + 128 * m]);
       }
       fence();
       wait_lds();      // read before they are copied over
@@ -441,7 +326,8 @@ __device__ __forceinline__ void few_product(const LoraFew& p, int id, int blocks
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (G32 || h == 0) few_zeros<F16>(n, gr[G32 ? h : 0], base);
-        few_block<F16, MT>(w[h], gr[G32 ? h : 0], n, base, xv[h], acc);
+        FewBlock<F16> b{w[h], gr[G32 ? h : 0], n, base};
+        few_block<F16, MT>(b, xv[h], acc);
       }
       fence();
       load_groups(gr, kb + 128);
@@ -457,41 +343,18 @@ __device__ __forceinline__ void few_product(const LoraFew& p, int id, int blocks
     // here, not behind the branch: there the compiler may copy accumulators first
     few_settle<MT>(acc);
   }
-  // The waves meet in LDS, a quarter of the outputs (nibbles 2u, 2u + 1 of the
-  // words) at a time: in step i wave w adds quarter (w + i) % 4, so all four
-  // work and an output's order depends on nothing but its column. Lane l holds
-  // outputs 8·(l % 16) + r, tokens 16·m + 4·(l / 16) + v.
-  floatx4* const red = reinterpret_cast<floatx4*>(&sx);
+  // lane l holds outputs 8·(l % 16) + r, tokens 16·m + 4·(l / 16) + v
   float* const out = p.partial + (int64_t(s) * p.T + t0 + 4 * lg) * N + n0 + 8 * lr;
   const int64_t left = p.T - t0 - 4 * lg;
   const bool in = n0 + 8 * lr < N;
-  __syncthreads();
+  auto store = [&](int u, int m, const floatx4 (&x)[2]) {
+    if (!in) return;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (((wave + i) & 3) != u) continue;
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        floatx4 x[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          floatx4* const at = red + ((2 * u + r) * MT + m) * 64 + lane;
-          x[r] = acc[2 * u + r][m];
-          if (i) x[r] += *at;
-          if (i < 3) *at = x[r];
-        }
-        if (i == 3 && in) {
-#pragma unroll
-          for (int v = 0; v < 4; ++v)
-            if (16 * m + v < left)
-              *reinterpret_cast<float2*>(out + (16 * m + v) * N + 2 * u) =
-                  make_float2(x[0][v], x[1][v]);
-        }
-      }
-    }
-    if (i < 3) __syncthreads();
-  }
+    for (int v = 0; v < 4; ++v)
+      if (16 * m + v < left)
+        *reinterpret_cast<float2*>(out + (16 * m + v) * N + 2 * u) = make_float2(x[0][v], x[1][v]);
+  };
+  AWQ_FEW_MEET(acc, sx, wave, lane, MT, store)
 }
 
 // One stage of X and two of packed words in LDS, in arrays of their own so that
@@ -729,6 +592,15 @@ void launch_decode(const LoraFew& p, int downs, int gx, int gy, hipStream_t st) 
 }
 
 template <bool F16>
+hipError_t launch_finish(const LoraFew& p, hipStream_t st) {
+  const dim3 grid(unsigned((p.w.N + kFinishCols - 1) / kFinishCols), unsigned((p.T + 15) / 16));
+  if (p.s.r <= 32) lora_few_finish_kernel<F16, 1><<<grid, 256, 0, st>>>(p);
+  else if (p.s.r <= 64) lora_few_finish_kernel<F16, 2><<<grid, 256, 0, st>>>(p);
+  else lora_few_finish_kernel<F16, 4><<<grid, 256, 0, st>>>(p);
+  return hipGetLastError();
+}
+
+template <bool F16>
 hipError_t launch_few(LoraFew p, hipStream_t st) {
   const int jbs = (p.s.r + 15) / 16;
   const int downs = int((p.T + 15) / 16) * few_slots(p) * jbs * p.S2;
@@ -748,17 +620,17 @@ hipError_t launch_few(LoraFew p, hipStream_t st) {
     if (p.T <= 32) launch_few<F16, 2>(p, downs, grid, st);
     else launch_few<F16, 4>(p, downs, grid, st);
   }
-  const dim3 grid(unsigned((p.w.N + kFinishCols - 1) / kFinishCols), unsigned((p.T + 15) / 16));
-  if (p.s.r <= 32) lora_few_finish_kernel<F16, 1><<<grid, 256, 0, st>>>(p);
-  else if (p.s.r <= 64) lora_few_finish_kernel<F16, 2><<<grid, 256, 0, st>>>(p);
-  else lora_few_finish_kernel<F16, 4><<<grid, 256, 0, st>>>(p);
-  return hipGetLastError();
+  return launch_finish<F16>(p, st);
 }
 
 }  // namespace
 
 hipError_t launch_lora_few(const LoraFew& p, hipStream_t st) {
   return p.f16 ? launch_few<true>(p, st) : launch_few<false>(p, st);
+}
+
+hipError_t launch_lora_few_finish(const LoraFew& p, hipStream_t st) {
+  return p.f16 ? launch_finish<true>(p, st) : launch_finish<false>(p, st);
 }
 
 }  // namespace awq

@@ -253,10 +253,8 @@ hipError_t launch_lora_prep(const LoraPrep& p, hipStream_t st) {
   while (g.waves * L > 15 * 1024) g.waves /= 2;
   auto blocks = [](int64_t n) { return uint32_t((n + kPrepThreads - 1) / kPrepThreads); };
   g.tb = uint32_t(L * (p.Np / 64));
-  if (p.Wt) {
-    g.ta = uint32_t(L * (p.w.K / 64));
-    g.dq = blocks(p.w.K / 8 * (p.Np / 8));
-  }
+  if (p.At) g.ta = uint32_t(L * (p.w.K / 64));
+  if (p.Wt) g.dq = blocks(p.w.K / 8 * (p.Np / 8));
   g.pad = p.dYp ? blocks(p.T * (p.Np / 8)) : 0;
   size_t lds = size_t(g.waves) * L * 4;
   const size_t tr = size_t(64) * (r + 2) * 2 > size_t(r) * 66 * 2 ? size_t(64) * (r + 2) * 2

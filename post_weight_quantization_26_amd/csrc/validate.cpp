@@ -522,6 +522,18 @@ LoraCut lora_cut(int64_t M, int64_t N, int64_t C) {
   return c;
 }
 
+// The few-token product of T tokens, O outputs and C channels: runs of C for two
+// workgroups per CU, each wave with 128 channels or more.
+static void lora_few_split(int64_t T, int64_t O, int64_t C, int64_t& tiles, int64_t& col_blocks,
+                           int64_t& per_wave, int64_t& S) {
+  tiles = ceil_div(T, T <= 32 ? 32 : 64);
+  col_blocks = ceil_div(O, 128);
+  const int64_t runs =
+      std::max<int64_t>(1, std::min(512 / (tiles * col_blocks), ceil_div(C, 512)));
+  per_wave = ceil_div(C, 4 * runs * 128) * 128;
+  S = ceil_div(C, 4 * per_wave);
+}
+
 LoraLayout lora_layout(int64_t T, int64_t N, int64_t K, int32_t, int32_t r) {
   LoraLayout l{};
   size_t off = 0;
@@ -538,13 +550,7 @@ LoraLayout lora_layout(int64_t T, int64_t N, int64_t K, int32_t, int32_t r) {
       l.kpw = w4a16_mgemv_kpw(N, K);
       l.S = w4a16_mgemv_chunks(N, K);
     } else {
-      // runs of k for two workgroups per CU, each wave with 128 rows or more
-      l.tiles = ceil_div(T, T <= 32 ? 32 : 64);
-      l.col_blocks = ceil_div(N, 128);
-      const int64_t runs = std::max<int64_t>(
-          1, std::min(512 / (l.tiles * l.col_blocks), ceil_div(K, 512)));
-      l.kpw = ceil_div(K, 4 * runs * 128) * 128;
-      l.S = ceil_div(K, 4 * l.kpw);
+      lora_few_split(T, N, K, l.tiles, l.col_blocks, l.kpw, l.S);
     }
     // runs of the narrow product: 2 blocks of 128 rows or more per wave, and
     // at most 16 KiB of partial sums for the second launch's workgroups to add
@@ -583,14 +589,22 @@ LoraBackwardLayout lora_backward_layout(int64_t T, int64_t N, int64_t K, int32_t
     return at;
   };
   const size_t t = size_t(T), n = size_t(l.Np), k = size_t(K), tp = size_t(l.Tp), a = size_t(L);
-  l.wt = take(k * n * 2);
+  l.few = T <= kLoraFewBackMaxT;
+  if (l.few) {
+    lora_few_split(T, K, l.Np, l.tiles, l.col_blocks, l.npw, l.S);
+    l.sums = take(size_t(l.S) * t * k * 4);
+  } else {
+    l.wt = take(k * n * 2);
+  }
   l.bt = take(a * r * n * 2);
   l.at = take(a * r * k * 2);
   l.dyp = take(l.Np == N ? 0 : t * n * 2);
   l.runs = lora_down_runs(T, l.Np);
   l.part = take(size_t(l.runs) * t * r * 4);
-  l.q = take(t * size_t(lora_q_width(r)) * 2);
-  l.e = take(t * 4);
+  if (!l.few) {
+    l.q = take(t * size_t(lora_q_width(r)) * 2);
+    l.e = take(t * 4);
+  }
   l.gs = take(tp * size_t(ceil_div(r, 16) * 16) * 4);
   l.hs = take(tp * size_t(ceil_div(r, 16) * 16) * 4);
   l.gmax = take(tp * 4);
@@ -603,8 +617,10 @@ LoraBackwardLayout lora_backward_layout(int64_t T, int64_t N, int64_t K, int32_t
   l.first_slot = take(a * 4);
   l.last_pos = take(a * 4);
   l.partial = take(size_t(l.slots) * (k + size_t(N)) * r * 4);
-  l.cut = lora_cut(T, K, l.Np);
-  l.tiles_part = take(l.cut.bytes);
+  if (!l.few) {
+    l.cut = lora_cut(T, K, l.Np);
+    l.tiles_part = take(l.cut.bytes);
+  }
   l.total = off;
   return l;
 }

@@ -419,6 +419,24 @@ def test_forward_forms(api, T, N, K, r, L, dtype, group, kind):
     check_forward(api, Problem(T, N, K, r, L, dtype, group, kind, seed=T + N + 1))
 
 
+# The gradient with and without a transposed layer (320 and 321 tokens), every
+# group size, words by 4 and by 16 bytes, 32 and 64 tokens a wave, N that is no
+# multiple of 128 (zero columns behind it) and one 128 long.
+@pytest.mark.parametrize("T,N,K,r,L,dtype,group,kind,x8", [
+    (5, 128, 128, 8, 1, "bf16", 128, "one", False),
+    (30, 544, 640, 32, 3, "f16", 32, "tokens", False),
+    (32, 1032, 384, 16, 2, "bf16", 32, "tokens", True),
+    (33, 1032, 256, 24, 2, "bf16", 32, "runs", False),
+    (64, 672, 896, 128, 20, "f16", 64, "tokens", True),
+    (100, 1040, 384, 64, 5, "f16", 32, "tokens", False),
+    (150, 2184, 512, 72, 150, "bf16", 64, "tokens", False),
+    (320, 520, 896, 48, 3, "f16", 64, "runs", True),
+    (321, 520, 896, 48, 3, "f16", 64, "runs", True),
+])
+def test_backward_forms(api, T, N, K, r, L, dtype, group, kind, x8):
+    check_backward(api, Problem(T, N, K, r, L, dtype, group, kind, seed=T + N + 2), x8)
+
+
 # Runs longer than a piece (several pieces and a last short one), thousands of
 # adapters (most without tokens), and both at once.
 @pytest.mark.parametrize("T,N,K,r,L,dtype,kind,x8", [

@@ -23,6 +23,8 @@ from test_asm_mfma_isa import _hipcc, _operands, _regs
 KERNELS = {
     "lora_few.hip": [f"lora_few_kernelILb{f}ELi{mt}ELb{g}ELb{w}E"
                      for f in (0, 1) for mt in (2, 4) for g in (0, 1) for w in (0, 1)],
+    "lora_few_back.hip": [f"lora_few_back_kernelILb{f}ELi{mt}ELi{g}ELb{w}E"
+                          for f in (0, 1) for mt in (2, 4) for g in (1, 2, 4) for w in (0, 1)],
     "lora_gemm.hip": [f"lora_gemm_kernelILb{f}ELb{s}E" for f in (0, 1) for s in (0, 1)],
 }
 
