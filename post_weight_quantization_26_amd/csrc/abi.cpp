@@ -789,6 +789,13 @@ extern "C" awq_status awq_w4a16_lora_matmul(
     return AWQ_OK;
   }
   LoraDown d{};
+  // The narrow product's sums beside the dequantisation: 512 tokens of 4096x4096
+  // 67 instead of 70 us, 1777 of 11008x4096 202 instead of 204. With many tokens
+  // their workgroups take the CUs first and nothing is gained: 4096 of
+  // 28672x8192 1655 both ways, 8192 of 4096x11008 737 instead of 727.
+  d.after = T <= 2048 ? LoraAfter::kSumsAndLayer : LoraAfter::kSums;
+  d.w = layer;
+  d.Wd = at<uint16_t>(ws, l.wd);
   d.V = x;
   d.M = set.A;
   d.scaling = scaling;
@@ -806,17 +813,16 @@ extern "C" awq_status awq_w4a16_lora_matmul(
   d.E = at<float>(ws, l.e);
   d.codes = x8_codes;
   d.steps = x8_steps;
-  uint16_t* Wd = at<uint16_t>(ws, l.wd);
   const LoraUp u{d.Q, d.E, ids, set.B, L, r, d.RW};
   const LoraSplit cut{int(l.cut.full), int(l.cut.runs), at<float>(ws, l.tiles_part)};
   AWQ_HIP(timed(AWQ_K_LORA, st,
                 [&] {
                   hipError_t e = launch_lora_down(d, st);
-                  if (e == hipSuccess)
-                    e = launch_w4a16_dequant(qweight, qzeros, scales, N, K, group_size, f16, Wd,
+                  if (e == hipSuccess && d.after == LoraAfter::kSums)
+                    e = launch_w4a16_dequant(qweight, qzeros, scales, N, K, group_size, f16, d.Wd,
                                              st);
                   if (e == hipSuccess)
-                    e = launch_lora_gemm(x, K, Wd, K, T, N, K, u, cut, f16, y, st);
+                    e = launch_lora_gemm(x, K, d.Wd, K, T, N, K, u, cut, f16, y, st);
                   return e;
                 }),
           "lora_matmul");
@@ -860,6 +866,7 @@ extern "C" awq_status awq_w4a16_lora_backward(
   pr.last_pos = at<int>(ws, l.last_pos);
 
   LoraDown d{};
+  d.after = dX && l.few ? LoraAfter::kNothing : LoraAfter::kSums;
   d.V = padded ? pr.dYp : pr.dY;
   d.M = pr.Bt;
   d.scaling = scaling;
@@ -900,6 +907,7 @@ extern "C" awq_status awq_w4a16_lora_backward(
     f.col_blocks = int(l.col_blocks);
     f.gshift = group_size == 32 ? 5 : group_size == 64 ? 6 : 7;
     f.f16 = up.f16 = f16;
+    f.down = d;
     up.w.N = K;
     up.s = {nullptr, pr.At, scaling, ids, L, r};
     up.hpart = d.part;

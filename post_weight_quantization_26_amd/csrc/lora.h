@@ -25,8 +25,14 @@ struct LoraSet {
   int L, r;
 };
 
+// What follows the narrow product's partial sums: nothing (another launch adds
+// them up), their sums, or these beside the dequantisation of w into Wd.
+enum class LoraAfter { kNothing, kSums, kSumsAndLayer };
 // The narrow product P[t][j] = Σ_c V[t][c]·M_a[j][c] (lora_down.hip).
 struct LoraDown {
+  LoraAfter after;
+  LoraLayer w;
+  uint16_t* Wd;           // [N, K]
   const uint16_t* V;      // [T, ldv]
   const uint16_t* M;      // [L, r, ldm]
   const float* scaling;
@@ -67,11 +73,6 @@ hipError_t launch_lora_gemm(const uint16_t* V, int64_t ldv, const uint16_t* Wd, 
                             int64_t M, int64_t N, int64_t C, const LoraUp& u,
                             const LoraSplit& sp, int f16, uint16_t* O, hipStream_t st);
 
-// The dequantisation pass of the W4A16 GEMM (w4a16.hip): Ŵ [N, K], rounded.
-hipError_t launch_w4a16_dequant(const int32_t* qweight, const int32_t* qzeros,
-                                const uint16_t* scales, int64_t N, int64_t K, int group, int f16,
-                                uint16_t* Wd, hipStream_t st);
-
 // The float32 decode for N not a multiple of 16 (w4a16.hip).
 hipError_t launch_w4a16_gemv(const uint16_t* X, int64_t T, int64_t N, int64_t K,
                              const int32_t* qweight, const int32_t* qzeros,
@@ -105,6 +106,7 @@ struct LoraFewBack {
   int S, npw;             // runs of n; n per wave
   int tiles, col_blocks;
   int gshift, f16;
+  LoraDown down;          // its sums are added up beside the product
 };
 hipError_t launch_lora_few_back(const LoraFewBack& p, hipStream_t st);
 

@@ -19,8 +19,10 @@
 // neither a token's nor an adapter's NaN reaches another.
 #include "act8.h"
 #include "lora.h"
+#include "lora_combine.h"
 #include "lora_common.h"
 #include "lora_stage.h"
+#include "w4a16_dequant.h"
 
 namespace awq {
 namespace {
@@ -161,74 +163,21 @@ __global__ __launch_bounds__(kDownThreads) void lora_down_kernel(LoraDown p) {
   }
 }
 
-// A wave per token: the sum of its partial sums, in order, as H, in the
-// gradients' operand order (with Hin in the same), and as the wide product's
-// operand c_a·P in two 16-bit halves hi = rnd(v), lo = rnd(v - hi), which lose at most u² (bf16: 2^-16) of v. fp16 halves are
-// scaled by a power of two where a row's largest value lies outside [2^-3,
-// 2^14), so that neither half overflows and lo keeps 2^-22 of the largest.
 template <bool F16>
 __global__ __launch_bounds__(256) void lora_combine_kernel(LoraDown p) {
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
-  const int64_t t = int64_t(blockIdx.x) * 4 + wave;
-  if (t >= p.T) return;
-  const int a = p.ids[t];
-  const bool has = a >= 0 && a < p.L;
-  if (!has && !p.H) return;
-  float v[2] = {0.f, 0.f}, h[2] = {0.f, 0.f};
-  if (has)
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int j = lane + 64 * k;
-      if (j >= p.r) continue;
-      const float* src = p.part + t * p.r + j;
-#pragma unroll 4
-      for (int s = 0; s < p.S; ++s) v[k] += src[int64_t(s) * p.T * p.r];
-      if (p.Hin) h[k] = p.Hin[t * p.r + j];
-    }
-  if (p.H)
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (lane + 64 * k < p.r) p.H[t * p.r + lane + 64 * k] = v[k];
-  if (!has) return;
-  float m = fmaxf(fabsf(v[0]), fabsf(v[1])), mh = fmaxf(fabsf(h[0]), fabsf(h[1]));
-#pragma unroll
-  for (int o = 32; o; o >>= 1) {
-    m = fmaxf(m, __shfl_xor(m, o));
-    mh = fmaxf(mh, __shfl_xor(mh, o));
-  }
-  const float c = p.scaling[a], cm = fabsf(c) * m;
-  int e = 0;
-  if (F16 && !(cm >= 0x1p-3f && cm < 0x1p14f)) e = exponent_of(cm);
-  const float down = exp2i(-e);
-  uint16_t* q = p.Q + t * p.RW;
-  const int pos = p.Ps ? p.pos[t] : 0;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int j = lane + 64 * k;
-    if (j >= p.r) continue;
-    if (p.Ps) {
-      // [step of 32 positions][16 ranks][lane][8 positions] (lora_grad.hip)
-      const int64_t at = ((int64_t(pos >> 5) * ((p.r + 15) / 16) + (j >> 4)) * 64 +
-                          ((pos >> 3) & 3) * 16 + (j & 15)) * 8 + (pos & 7);
-      p.Ps[at] = v[k];
-      p.Hs[at] = h[k];
-    }
-    if (!p.Q) continue;
-    const float s = c * v[k] * down;
-    const uint16_t hi = round16<F16>(s);
-    q[j] = hi;
-    q[p.r + j] = round16<F16>(s - widen16<F16>(hi));
-  }
-  if (p.Q)
-    for (int j = 2 * p.r + lane; j < p.RW; j += 64) q[j] = 0;
-  if (lane == 0) {
-    if (p.Q) p.E[t] = exp2i(e);
-    if (p.Ps) {
-      p.row_max[pos] = m;
-      p.h_max[pos] = mh;
-    }
-  }
+  lora_combine<F16>(p, blockIdx.x);
+}
+// The layer's dequantisation beside it: both come before the wide product and
+// neither needs the other.
+template <bool F16, bool WIDE>
+__global__ __launch_bounds__(256, 8) void lora_combine_dequant_kernel(LoraDown p, LoraLayer w,
+                                                                   uint16_t* __restrict__ Wd,
+                                                                   int combines) {
+  if (int(blockIdx.x) < combines) return lora_combine<F16>(p, blockIdx.x);
+  const int64_t t = int64_t(int(blockIdx.x) - combines) * 256 + threadIdx.x;
+  if constexpr (WIDE)
+    dequant_words4<F16>(t, w.qweight, w.qzeros, w.scales, w.N, w.K, w.group, Wd);
+  else dequant_words<F16>(t, w.qweight, w.qzeros, w.scales, w.N, w.K, w.group, Wd);
 }
 
 template <bool F16, int JB>
@@ -238,13 +187,27 @@ void launch_jb(const LoraDown& p, dim3 grid, hipStream_t st) {
 }
 
 template <bool F16>
+void launch_sums(const LoraDown& p, hipStream_t st) {
+  const unsigned combines = unsigned((p.T + 31) / 32 * 8);   // a multiple of the 8 XCDs
+  if (p.after == LoraAfter::kSums) {
+    lora_combine_kernel<F16><<<combines, 256, 0, st>>>(p);
+  } else if (p.w.N % 32 == 0) {
+    const unsigned grid = combines + unsigned((p.w.K / 8 * (p.w.N / 32) + 255) / 256);
+    lora_combine_dequant_kernel<F16, true><<<grid, 256, 0, st>>>(p, p.w, p.Wd, int(combines));
+  } else {
+    const unsigned grid = combines + unsigned((p.w.K / 8 * (p.w.N / 8) + 255) / 256);
+    lora_combine_dequant_kernel<F16, false><<<grid, 256, 0, st>>>(p, p.w, p.Wd, int(combines));
+  }
+}
+
+template <bool F16>
 hipError_t launch_f(const LoraDown& p, hipStream_t st) {
   const dim3 grid(unsigned((p.T + 63) / 64), unsigned(p.S), unsigned(p.L < 4 ? p.L : 4));
   if (p.r <= 16) launch_jb<F16, 1>(p, grid, st);
   else if (p.r <= 32) launch_jb<F16, 2>(p, grid, st);
   else if (p.r <= 64) launch_jb<F16, 4>(p, grid, st);
   else launch_jb<F16, 8>(p, grid, st);
-  lora_combine_kernel<F16><<<unsigned((p.T + 3) / 4), 256, 0, st>>>(p);
+  if (p.after != LoraAfter::kNothing) launch_sums<F16>(p, st);
   return hipGetLastError();
 }
 

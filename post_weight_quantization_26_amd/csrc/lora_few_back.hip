@@ -22,6 +22,7 @@
 // a pass that writes Ŵᵀ and 256x256 tiles: the whole gradient of 64 tokens, bf16,
 // rank 16, 91 instead of 265 us at 28672x8192, 38 instead of 55 at 4096x4096.
 #include "lora.h"
+#include "lora_combine.h"
 #include "lora_few.h"
 
 namespace awq {
@@ -120,6 +121,10 @@ struct BackBlock {
 // WIDE: N a multiple of 32, rows of packed words 16-byte aligned.
 template <bool F16, int MT, int NG, bool WIDE>
 __global__ __launch_bounds__(64 * kFewWaves, 2) void lora_few_back_kernel(LoraFewBack p) {
+  // the narrow product's sums, by the workgroups behind (the last launch but
+  // one has left their parts; a launch of its own took 4 us)
+  const int blocks = p.tiles * p.col_blocks * p.S;
+  if (int(blockIdx.x) >= blocks) return lora_combine<F16>(p.down, int(blockIdx.x) - blocks);
   typedef typename Operand<F16>::type V;
   constexpr uint32_t kOob = 0x80000000u;
   __shared__ uint4 xs[kFewWaves * 16 * MT * 8];
@@ -132,7 +137,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void lora_few_back_kernel(LoraFe
   // indices, token tiles fastest, as the forward product
   int tt, cb, s;
   {
-    const int blocks = int(gridDim.x), id = int(blockIdx.x);
+    const int id = int(blockIdx.x);
     const int q = blocks / 8, rem = blocks % 8, xi = id % 8;
     int l = xi * q + (xi < rem ? xi : rem) + id / 8;
     tt = l % p.tiles;
@@ -268,7 +273,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void lora_few_back_kernel(LoraFe
 
 template <bool F16, int MT, int NG>
 void launch_ng(const LoraFewBack& p, hipStream_t st) {
-  const unsigned grid = unsigned(p.tiles * p.col_blocks * p.S);
+  const unsigned grid = unsigned(p.tiles * p.col_blocks * p.S + (p.T + 3) / 4);
   if (p.w.N % 32 == 0) lora_few_back_kernel<F16, MT, NG, true><<<grid, 256, 0, st>>>(p);
   else lora_few_back_kernel<F16, MT, NG, false><<<grid, 256, 0, st>>>(p);
 }
