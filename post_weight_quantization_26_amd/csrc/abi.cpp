@@ -763,7 +763,7 @@ extern "C" awq_status awq_w4a16_lora_matmul(
   const uint16_t* x = static_cast<const uint16_t*>(X);
   uint16_t* y = static_cast<uint16_t*>(Y);
   const int f16 = dtype == AWQ_F16;
-  if (T <= kLoraFewMaxT) {
+  if (l.few) {
     LoraFew p{};
     p.X = x;
     p.T = T;

@@ -227,6 +227,7 @@ constexpr int64_t kLoraFewMaxT = 384;
 // 320 tokens 65 / 65, 87 / 95, 302 / 339; 384 tokens 69 / 66, 101 / 95, 309 / 339.
 constexpr int64_t kLoraFewBackMaxT = 320;
 struct LoraLayout {
+  bool few;       // no dequantised layer
   size_t partial; // few tokens: [S, T, N] f32 sums of the shared product, ..
   size_t hpart;   // .. and [S2, T, r] f32 of the narrow one
   int64_t S, S2, kpw, tiles, col_blocks;

@@ -232,10 +232,9 @@ __device__ __forceinline__ void few_product(const LoraFew& p, int id, int blocks
     const FewRows x = few_rows<MT>(p.X, t0, p.T, K);
     // (stages past the run read its last one)
     auto copy_x = [&](int kb) { few_copy_rows<MT>(x, sx[wave], kb < kw1 ? kb : kw1 - 64); };
-    // The wave's rows of packed words (at most a quarter of N·K / 2 <= 2^33
-    // bytes). WIDE: four words a lane; words past the row are the next row's
-    // (or, past the last row, zero), and never stored. Else one word a lane,
-    // column 0's past N.
+    // The wave's rows of packed words (less than 2^31 bytes). WIDE: four words
+    // a lane; words past the row are the next row's (or, past the last row,
+    // zero), and never stored. Else one word a lane, column 0's past N.
     const int rowb = int(N8 * 4);
     const auto rsQ = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<int32_t*>(p.w.qweight) + int64_t(kw0) * N8, 0,
@@ -413,6 +412,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void lora_few_down_kernel(LoraFew p
 // they add up in LDS in order. The rows' h (summed over the runs of k) become
 // two 16-bit halves in LDS, as in lora_down.hip; an adapter takes one pass of
 // MFMAs whose rows are kept where they belong to it.
+// Bound by the reads of B and of the partial sums: 64 tokens of 48 adapters,
+// rank 32, 28672 outputs (88 MB of B, 15 MB of sums) 21 us; 200 tokens of 6
+// adapters, rank 8, 4096 outputs (13 MB of sums) 9.8 us. Partial sums read in
+// the MFMA's layout, a dword a lane: 27 and 13 us. B through LDS: 35 and 17.5.
 constexpr int kFinishCols = 32;
 
 template <bool F16, int NC>
@@ -424,6 +427,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void lora_few_finish_kernel(LoraFew
     float y[kFewWaves][16][kFinishCols + 1];
   } sm;
   __shared__ __align__(16) uint16_t q[2][16][RP + 8];
+  __shared__ __align__(16) float part[kFewWaves][16][kFinishCols + 4];
   __shared__ float se[16];
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -489,22 +493,24 @@ __global__ __launch_bounds__(64 * kFewWaves) void lora_few_finish_kernel(LoraFew
     sm.h[i][j] = h;
     if (p.H && blockIdx.x == 0 && t < p.T && j < r) p.H[t * r + j] = h;
   }
-  // this wave's runs of the shared product (rows past T read the last one)
-  float y[2][4] = {};
+  // this wave's runs of the shared product: lane l takes 8 outputs of row l / 4
+  // (rows past T read the last one, columns past N the first ones)
   {
-    const float* src[4];
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int64_t t = t0 + 4 * lg + v;
-      src[v] = p.partial + (t < p.T ? t : p.T - 1) * N;
-    }
+    const int row = lane >> 2, c = (lane & 3) * 8;
+    const int64_t t = t0 + row < p.T ? t0 + row : p.T - 1;
+    const float* src = p.partial + t * N + (n0 + c < N ? n0 + c : 0);
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), z = x;
 #pragma unroll 4
-    for (int s = wave; s < p.S; s += kFewWaves)
-#pragma unroll
-      for (int v = 0; v < 4; ++v)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) y[c][v] += src[v][int64_t(s) * p.T * N + col[c]];
+    for (int s = wave; s < p.S; s += kFewWaves) {
+      const float4 a0 = *reinterpret_cast<const float4*>(src + int64_t(s) * p.T * N);
+      const float4 a1 = *reinterpret_cast<const float4*>(src + int64_t(s) * p.T * N + 4);
+      x = make_float4(x.x + a0.x, x.y + a0.y, x.z + a0.z, x.w + a0.w);
+      z = make_float4(z.x + a1.x, z.y + a1.y, z.z + a1.z, z.w + a1.w);
+    }
+    *reinterpret_cast<float4*>(&part[wave][row][c]) = x;
+    *reinterpret_cast<float4*>(&part[wave][row][c + 4]) = z;
   }
+  float y[2][4] = {};
   __syncthreads();
   for (int i = wave; i < 16; i += kFewWaves) {
     const int id = __builtin_amdgcn_readlane(my, i);
@@ -563,7 +569,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void lora_few_finish_kernel(LoraFew
   __syncthreads();
   for (int e = tid; e < 16 * kFinishCols; e += 64 * kFewWaves) {
     const int i = e / kFinishCols, c = e % kFinishCols;
-    const float s = ((sm.y[0][i][c] + sm.y[1][i][c]) + sm.y[2][i][c]) + sm.y[3][i][c];
+    const float s = (((part[0][i][c] + part[1][i][c]) + part[2][i][c]) + part[3][i][c]) +
+                    (((sm.y[0][i][c] + sm.y[1][i][c]) + sm.y[2][i][c]) + sm.y[3][i][c]);
     if (t0 + i < p.T && n0 + c < N) p.Y[(t0 + i) * N + n0 + c] = round16<F16>(s);
   }
 }

@@ -542,15 +542,19 @@ LoraLayout lora_layout(int64_t T, int64_t N, int64_t K, int32_t, int32_t r) {
     off += align_up(bytes);
     return at;
   };
-  if (T <= kLoraFewMaxT) {
+  l.few = T <= kLoraFewMaxT;
+  if (l.few && T > kW4A16GemvMaxT) {
+    // a wave's packed words lie within 32-bit offsets
+    lora_few_split(T, N, K, l.tiles, l.col_blocks, l.kpw, l.S);
+    l.few = l.kpw * (N / 2) < (int64_t(1) << 31);
+  }
+  if (l.few) {
     if (T <= kW4A16GemvMaxT && N % 16) {
       l.kpw = w4a16_gemv_kpw(N, K);
       l.S = w4a16_gemv_chunks(N, K);
     } else if (T <= kW4A16GemvMaxT) {
       l.kpw = w4a16_mgemv_kpw(N, K);
       l.S = w4a16_mgemv_chunks(N, K);
-    } else {
-      lora_few_split(T, N, K, l.tiles, l.col_blocks, l.kpw, l.S);
     }
     // runs of the narrow product: 2 blocks of 128 rows or more per wave, and
     // at most 16 KiB of partial sums for the second launch's workgroups to add

@@ -206,6 +206,8 @@ def test_backward(api, T, N, K, r, L, dtype, group, kind, x8):
 def test_backward_without_dx(api):
     p = Problem(300, 264, 384, 16, 3, "bf16", seed=5)
     check_backward(api, p, want_dx=False)
+    p = Problem(400, 264, 384, 16, 3, "f16", seed=6)
+    check_backward(api, p, want_dx=False)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])

@@ -103,6 +103,19 @@ def test_workspace_sizes(L):
             assert f(*bad) == 0
 
 
+def test_few_tokens_keep_no_layer_unless_offsets_need_one(L):
+    """Up to 384 (gradient: 320) tokens no 16-bit layer is kept; a layer whose
+    packed words pass 2^31 bytes in one run of k takes the other form."""
+    f = L.lib().awq_w4a16_lora_workspace_bytes
+    b = L.lib().awq_w4a16_lora_backward_workspace_bytes
+    layer = 28672 * 8192 * 2
+    assert f(384, 28672, 8192, 4, 16, L.AWQ_BF16) < layer <= f(385, 28672, 8192, 4, 16, L.AWQ_BF16)
+    assert b(320, 28672, 8192, 1, 16, L.AWQ_BF16) < layer <= b(321, 28672, 8192, 1, 16, L.AWQ_BF16)
+    for N, K, kept in ((1 << 25, 128, True), ((1 << 25) - 8, 128, False), (1 << 24, 512, False),
+                       (1 << 23, 2048, True)):
+        assert (f(17, N, K, 1, 8, L.AWQ_F16) >= N * K * 2) == kept
+
+
 def test_checkpoint_refusals(L):
     lib = L.lib()
     INV, UNS = L.AWQ_E_INVALID, L.AWQ_E_UNSUPPORTED
