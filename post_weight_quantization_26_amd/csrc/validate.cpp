@@ -579,11 +579,21 @@ LoraBackwardLayout lora_backward_layout(int64_t T, int64_t N, int64_t K, int32_t
   l.Np = ceil_div(N, 128) * 128;
   const int64_t runs = std::min<int64_t>(L, T);
   l.Tp = ceil_div(T, 32) * 32 + 32 * runs;
-  // Pieces as long as still gives 1024 workgroups of 128 columns (4 per CU):
-  // each piece of a longer run costs its float32 sums once out and in.
+  // Pieces of the tokens: a workgroup per piece and 128 columns, 512 at a time.
+  // Few pieces leave the last round of them empty, each one more writes and
+  // reads its float32 sums once; X and dY take as long to read as they have
+  // bytes. (One run is assumed; where the tokens of several adapters end is
+  // known on the device only.)
   const int64_t strips = ceil_div(K, 128) + ceil_div(N, 128);
-  l.piece = ceil_div(ceil_div(T * strips, 1024), 32) * 32;
-  l.piece = std::max<int64_t>(128, std::min<int64_t>(kLoraPieceMax, l.piece));
+  double best = 0;
+  const int64_t least = ceil_div(T, kLoraPieceMax);
+  for (int64_t n = least; n <= std::min(ceil_div(T, 128), least + 32); ++n) {
+    const double rounds = double(ceil_div(strips * n, 512)) * 512 / double(strips * n);
+    const double t = rounds * double(T) * double(K + N) * 2 + double(n) * double(K + N) * r * 8;
+    if (best && t >= best) continue;
+    best = t;
+    l.piece = ceil_div(ceil_div(T, n), 32) * 32;
+  }
   l.pieces = T / l.piece + L;
   l.slots = T > l.piece ? 2 * (T / l.piece) + 1 : 0;
   size_t off = 0;
