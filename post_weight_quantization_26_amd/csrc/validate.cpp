@@ -504,8 +504,7 @@ static int64_t lora_down_runs(int64_t T, int64_t C) {
 // 0.09 us each, with 4 us for the kernel that adds them; 64 channels of a tile
 // take 1.6 us. Runs of 2 or more 64-wide steps, as many as fill 256 CUs. Whole
 // calls with / without the cut: 1777 tokens of 11008x4096 204 / 248 us, 512 of
-// 4096x11008 106 / 241, 1024 of 8192x28672 605 / 891; 2100 of 28672x8192, where
-// the formula cuts for nothing, 1033 / 1021.
+// 4096x11008 106 / 241, 1024 of 8192x28672 605 / 891.
 LoraCut lora_cut(int64_t M, int64_t N, int64_t C) {
   LoraCut c{};
   const int64_t tiles = ceil_div(M, 256) * ceil_div(N, 256), rest = tiles % 256;
