@@ -386,12 +386,13 @@ def w4a16_matmul(X: torch.Tensor, qweight: torch.Tensor, qzeros: torch.Tensor,
 def _check_on(device: int, names: Sequence[str], tensors) -> None:
     """Each tensor is a contiguous one on GPU number ``device``."""
     for name, t in zip(names, tensors):
+        if isinstance(t, torch.Tensor) and t.get_device() == device and t.is_contiguous():
+            continue
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise ValueError(f"{name} must be a GPU tensor")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        if t.get_device() != device:
-            raise ValueError(f"{name} is on {t.device}, not on GPU {device}")
+        raise ValueError(f"{name} is on {t.device}, not on GPU {device}")
 
 
 def _out(t: Optional[torch.Tensor], shape, dtype, like: torch.Tensor, name: str) -> torch.Tensor:
@@ -438,17 +439,18 @@ def _lora_args(V: torch.Tensor, V_cols: str, qweight, qzeros, scales, A, B, scal
     """Checks what the forward and the backward call share; (T, N, K, L, r)."""
     _dev(V, V_cols)
     _check_on(V.get_device(), _LORA_NAMES, (qweight, qzeros, scales, A, B, scaling, ids))
-    if V.dim() != 2 or qweight.dim() != 2 or scales.dim() != 2 or A.dim() != 3:
+    vs, qs, ss, az = V.shape, qweight.shape, scales.shape, A.shape
+    if len(vs) != 2 or len(qs) != 2 or len(ss) != 2 or len(az) != 3:
         raise ValueError(f"{V_cols}, qweight and scales must have 2 dimensions, A 3")
-    T, K, N = V.shape[0], qweight.shape[0], scales.shape[1]
-    n, r = A.shape[0], A.shape[1]
-    if qweight.shape[1] * 8 != N or qzeros.shape != (K // group, N // 8) or \
-            scales.shape[0] != K // group or V.shape[1] != (K if V_cols == "X" else N):
+    T, K, N = vs[0], qs[0], ss[1]
+    n, r = az[0], az[1]
+    if qs[1] * 8 != N or qzeros.shape != (K // group, N // 8) or \
+            ss[0] != K // group or vs[1] != (K if V_cols == "X" else N):
         raise ValueError(f"packed layer shapes do not match {V_cols} and the group size")
     if qweight.dtype != torch.int32 or qzeros.dtype != torch.int32 or \
             scales.dtype != torch.float16:
         raise ValueError("qweight and qzeros must be int32, scales float16")
-    if A.shape != (n, r, K) or B.shape != (n, N, r) or scaling.shape != (n,) or ids.shape != (T,):
+    if az[2] != K or B.shape != (n, N, r) or scaling.shape != (n,) or ids.shape != (T,):
         raise ValueError("adapters must be A [L, r, K], B [L, N, r], scaling [L], ids [T]")
     if A.dtype != V.dtype or B.dtype != V.dtype:
         raise ValueError(f"A and B must share {V_cols}'s dtype")
@@ -477,10 +479,11 @@ def w4a16_lora_matmul(X: torch.Tensor, qweight: torch.Tensor, qzeros: torch.Tens
     if x8 is not None:
         codes = _out(x8[0], (T, K), torch.int8, X, "x8 codes")
         steps = _out(x8[1], (T, K // 128), torch.float32, X, "x8 steps")
+    device = X.get_device()
     if ws is None:
         ws = _workspace(ws, w4a16_lora_workspace_bytes(T, N, K, n, r, X.dtype), X.device)
-    device = X.get_device()
-    _check_on(device, ("ws",), (ws,))
+    else:
+        _check_on(device, ("ws",), (ws,))
     _call(device, L.lib().awq_w4a16_lora_matmul, X.data_ptr(), _dtype(X), T, N, K,
           qweight.data_ptr(), qzeros.data_ptr(), scales.data_ptr(), int(group), A.data_ptr(),
           B.data_ptr(), scaling.data_ptr(), ids.data_ptr(), n, r, Y.data_ptr(), _at(h),
@@ -525,7 +528,8 @@ def w4a16_lora_backward(dY: torch.Tensor, X, h: torch.Tensor, qweight: torch.Ten
     if ws is None:
         ws = _workspace(ws, w4a16_lora_backward_workspace_bytes(T, N, K, n, r, dY.dtype),
                         dY.device)
-    _check_on(device, ("ws",), (ws,))
+    else:
+        _check_on(device, ("ws",), (ws,))
     _call(device, L.lib().awq_w4a16_lora_backward, dY.data_ptr(), X.data_ptr(), _at(steps),
           h.data_ptr(), _dtype(dY), T, N, K, qweight.data_ptr(), qzeros.data_ptr(),
           scales.data_ptr(), int(group), A.data_ptr(), B.data_ptr(), scaling.data_ptr(),
