@@ -22,8 +22,10 @@
 // of two per piece that takes the piece's largest |S| to 2^14: a value 2^-17
 // times as large still keeps 2^-22 of itself.
 //
-// An 8-bit checkpoint of X enters as fp16 numbers (code, exact) and its steps
-// go into S: a strip of 128 channels has one step per token.
+// An 8-bit checkpoint of X enters as its codes, exact in either 16-bit type, and
+// its steps go into S: a strip of 128 channels has one step per token. The
+// operands have the adapters' type: with fp16 ones under bf16 adapters g·step
+// would leave their range where g itself does not.
 //
 // The waves add up in LDS in a fixed order. A run of one piece is finished
 // here; pieces of a longer run leave float32 sums that lora_grad_sum_kernel adds
@@ -46,14 +48,15 @@ typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef uint4 GradStage[kGradWaves][512];
 static_assert(sizeof(GradStage) == 64 * kGradStrip * 4, "half of the waves' meeting place");
 
-// MF: fp16 matrix-core operands (fp16 Z, or 8-bit codes); else bf16.
+// Byte b of a word as a float32 number (a conversion with a byte select).
+__device__ __forceinline__ float code_of(uint32_t w, int b) { return float(int8_t(w >> (8 * b))); }
+
 template <bool F16, bool X8, int JB>
 __device__ __forceinline__ void grad_piece(const LoraGrad& p, const LoraPiece& pc, bool is_a,
                                            int64_t strip, int j0, GradStage& z0, GradStage& z1,
                                            int* tokens) {
-  constexpr bool MF = F16 || X8;
   constexpr int kCopies = X8 ? 4 : 8;          // 1 KiB each
-  typedef typename Operand<MF>::type V;
+  typedef typename Operand<F16>::type V;
   const int lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
   const int64_t C = is_a ? p.K : p.N;
@@ -68,7 +71,7 @@ __device__ __forceinline__ void grad_piece(const LoraGrad& p, const LoraPiece& p
   for (int i = threadIdx.x; i < padded; i += 64 * kGradWaves) tokens[i] = p.token[pc.pos + i];
   __syncthreads();
   float scale = 1.f;
-  if constexpr (MF) {
+  if constexpr (F16) {
     float m = 0.f;
     for (int i = lane; i < pc.n; i += 64) {
       float v = row_max[pc.pos + i];
@@ -107,8 +110,8 @@ __device__ __forceinline__ void grad_piece(const LoraGrad& p, const LoraPiece& p
       if constexpr (X8) {
         const uint2 x =
             reinterpret_cast<const uint2*>(st[wave])[(8 * lg + e) * 16 + lr];
-        z[e][0] = x.x ^ 0x80808080u;
-        z[e][1] = x.y ^ 0x80808080u;
+        z[e][0] = F16 ? x.x ^ 0x80808080u : x.x;
+        z[e][1] = F16 ? x.y ^ 0x80808080u : x.y;
       } else {
         const uint4 x = st[wave][(8 * lg + e) * 16 + lr];
         z[e][0] = x.x;
@@ -126,14 +129,14 @@ __device__ __forceinline__ void grad_piece(const LoraGrad& p, const LoraPiece& p
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         if constexpr (X8) v[e] *= step[e];
-        if constexpr (MF) v[e] *= scale;
+        if constexpr (F16) v[e] *= scale;
         if (s + 8 * lg + e >= pc.n) v[e] = 0.f;
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        hi[e] = pack2<MF>(v[2 * e], v[2 * e + 1]);
-        lo[e] = pack2<MF>(v[2 * e] - widen16<MF>(uint16_t(hi[e])),
-                          v[2 * e + 1] - widen16<MF>(uint16_t(hi[e] >> 16)));
+        hi[e] = pack2<F16>(v[2 * e], v[2 * e + 1]);
+        lo[e] = pack2<F16>(v[2 * e] - widen16<F16>(uint16_t(hi[e])),
+                          v[2 * e + 1] - widen16<F16>(uint16_t(hi[e] >> 16)));
       }
       sh[q] = __builtin_bit_cast(V, make_uint4(hi[0], hi[1], hi[2], hi[3]));
       sl[q] = __builtin_bit_cast(V, make_uint4(lo[0], lo[1], lo[2], lo[3]));
@@ -143,7 +146,12 @@ __device__ __forceinline__ void grad_piece(const LoraGrad& p, const LoraPiece& p
       uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if constexpr (X8) {
+        if constexpr (X8 && !F16) {
+          // the upper halves of two float32 codes
+          w[e] = __builtin_amdgcn_perm(__float_as_uint(code_of(z[2 * e + 1][i >> 2], i & 3)),
+                                       __float_as_uint(code_of(z[2 * e][i >> 2], i & 3)),
+                                       0x07060302u);
+        } else if constexpr (X8) {
           constexpr uint32_t kZero = 0x0C000C00u;
           const uint32_t b = i & 3;
           const uint32_t x = __builtin_amdgcn_perm(z[2 * e + 1][i >> 2], z[2 * e][i >> 2],

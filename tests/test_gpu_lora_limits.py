@@ -1,0 +1,82 @@
+"""GPU: the adapter calls where magnitudes differ or values are not finite.
+Bounds as derived in test_gpu_lora.py."""
+import numpy as np
+import pytest
+import torch
+
+import lora_reference as R
+from test_gpu_lora import Problem, check_backward, dev, f64, worst
+from test_gpu_w4a16 import _dec, _enc
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def api():
+    if not torch.cuda.is_available():
+        raise RuntimeError("GPU tests need a GPU")
+    from post_weight_quantization_26_amd import api as A
+    return A
+
+
+def scale_by(p, name, factor):
+    """Multiplies p's A, B or dy by `factor` (broadcast), rounded to p's type."""
+    field, bits = {"A": ("A", "Ab"), "B": ("B", "Bb"), "dy": ("dy", "dYb")}[name]
+    b = _enc((getattr(p, field) * factor).astype(np.float32), p.dtype)
+    setattr(p, bits, b)
+    setattr(p, field, _dec(b, p.dtype).astype(np.float64).reshape(b.shape))
+
+
+@pytest.mark.parametrize("x8", [False, True])
+@pytest.mark.parametrize("T", [100, 400, 2500])
+def test_gradients_of_ranks_of_any_size(api, T, x8):
+    """bf16: g of one rank is 2^-60 of another's, and dA keeps each to the
+    type's accuracy, from the activations and from their checkpoint."""
+    p = Problem(T, 264, 384, 16, 2, "bf16", kind="runs", seed=T)
+    scale_by(p, "B", 2.0 ** (-4.0 * np.arange(16)))
+    check_backward(api, p, x8)
+
+
+def test_small_gradients_from_a_checkpoint(api):
+    """bf16: every g·step lies far below the clamp that fp16 halves would need."""
+    p = Problem(300, 264, 384, 16, 2, "bf16", kind="runs", seed=8)
+    scale_by(p, "dy", 2.0 ** -85)
+    check_backward(api, p, True)
+
+
+@pytest.mark.parametrize("dtype,x8", [("bf16", False), ("bf16", True)])
+@pytest.mark.parametrize("T", [100, 2500])
+def test_an_infinite_rank_leaves_the_others(api, T, dtype, x8):
+    """One infinity in a column of B_a makes that rank of g infinite, one in H
+    that rank of h: the adapter's other ranks keep their accuracy where g and
+    h are small."""
+    p = Problem(T, 264, 384, 16, 2, dtype, kind="one", seed=T + 3)
+    p.c[:] = 2.0 ** 20 if dtype == "f16" else 1.0
+    scale_by(p, "dy", 2.0 ** -8 if dtype == "f16" else 2.0 ** -16)
+    scale_by(p, "B", 2.0 ** -12 if dtype == "f16" else 1.0)
+    rng = np.random.default_rng(T)
+    h = (rng.standard_normal((T, 16)) * 1e-7).astype(np.float32)
+    broken_h = h.copy()
+    broken_h[T // 2, 5] = np.inf
+    A, B, c, ids = p.lora()
+    B[1, 7, 5] = float("inf")
+    if x8:
+        codes, steps = R.pack8(_dec(p.Xb, dtype).astype(np.float32).reshape(T, p.K))
+        X = (dev(codes), dev(steps))
+        x = codes.astype(np.float64) * np.repeat(steps.astype(np.float64), 128, axis=1)
+    else:
+        X, x = p.td(p.Xb), p.x
+    _, dA, dB = api.w4a16_lora_backward(p.td(p.dYb), X, dev(broken_h), *p.layer(), A, B, c, ids,
+                                        want_dx=False)
+    torch.cuda.synchronize()
+    _, da, db, _, _, mA, mB = R.backward(p.dy, x, h.astype(np.float64), p.w, p.A, p.B,
+                                         p.c.astype(np.float64), p.ids)
+    u, tiny, low = R.UOUT[dtype], R.TINY[dtype], R.LOW[dtype]
+    keep = np.arange(16) != 5
+    assert not torch.isfinite(dA[1, 5]).any() and not torch.isfinite(dB[1, :, 5]).any()
+    bA = (low + R.gamma(p.N + T + 4)) * mA + u * np.abs(da) + tiny
+    bB = (low + R.gamma(T + 4)) * mB + u * np.abs(db) + tiny
+    eA = worst(f64(dA)[:, keep], da[:, keep], bA[:, keep])
+    eB = worst(f64(dB)[:, :, keep], db[:, :, keep], bB[:, :, keep])
+    print(f"T={T} {dtype} x8={x8}: dA {eA:.3f}, dB {eB:.3f} of the bounds", flush=True)
+    assert eA <= 1 and eB <= 1
