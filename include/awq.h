@@ -438,7 +438,7 @@ awq_status awq_w4a16_lora_matmul(const void* X, awq_dtype dtype, int64_t T, int6
  * gets zeros. Sums run in an order that the arguments fix: equal calls give
  * equal bits. Alignment as above (dX, dA, dB 16-byte); ws: at least
  * awq_w4a16_lora_backward_workspace_bytes(T, N, K, L, r, dtype) bytes. N
- * also below 2^22. Does not synchronise. */
+ * at most 2^22 - 128. Does not synchronise. */
 size_t awq_w4a16_lora_backward_workspace_bytes(int64_t T, int64_t N, int64_t K, int32_t L,
                                                int32_t r, awq_dtype dtype);
 awq_status awq_w4a16_lora_backward(const void* dY, const void* X, const float* x8_steps,

@@ -720,10 +720,10 @@ awq_status check_lora_backward(const void* dY, const void* X, const float* x8_st
   const awq_status st = check_lora_common(name, dY, d, T, N, K, qweight, qzeros, scales, group, A,
                                           B, scaling, ids, L, r);
   if (st != AWQ_OK) return st;
-  if (!tile_rows_fit(N))
-    return set_error(AWQ_E_UNSUPPORTED, "%s: N=%lld exceeds the 32-bit offsets (512 * N must "
-                     "stay below 2^31)", name, (long long)N);
   const LoraBackwardLayout l = lora_backward_layout(T, N, K, L, r);
+  if (!tile_rows_fit(l.Np))
+    return set_error(AWQ_E_UNSUPPORTED, "%s: N=%lld exceeds the 32-bit offsets (512 * N, N "
+                     "rounded up to 128, must stay below 2^31)", name, (long long)N);
   const int64_t prep = 1 + L * (l.Np + K) / 64 + ceil_div(K / 8 * (l.Np / 8), 1024) +
                        ceil_div(T * (l.Np / 8), 1024);
   const int64_t grad = (K / 128 + ceil_div(N, 128)) * l.pieces * 2;
