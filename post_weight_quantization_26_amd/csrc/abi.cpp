@@ -879,7 +879,6 @@ extern "C" awq_status awq_w4a16_lora_backward(
   d.S = int(l.runs);
   d.part = at<float>(ws, l.part);
   d.Ps = at<float>(ws, l.gs);
-  d.row_max = at<float>(ws, l.gmax);
   d.pos = pr.pos;
   if (dX && !l.few) {
     d.Q = at<uint16_t>(ws, l.q);
@@ -888,7 +887,6 @@ extern "C" awq_status awq_w4a16_lora_backward(
   }
   d.Hin = H;
   d.Hs = at<float>(ws, l.hs);
-  d.h_max = at<float>(ws, l.hmax);
 
   const LoraUp u{d.Q, d.E, ids, pr.At, L, r, d.RW};
   const LoraSplit cut{int(l.cut.full), int(l.cut.runs), at<float>(ws, l.tiles_part)};
@@ -921,8 +919,6 @@ extern "C" awq_status awq_w4a16_lora_backward(
   g.steps = x8_steps;
   g.Gs = d.Ps;
   g.Hs = d.Hs;
-  g.g_max = d.row_max;
-  g.h_max = d.h_max;
   g.scaling = scaling;
   g.token = pr.token;
   g.pieces = pr.pieces;

@@ -252,7 +252,7 @@ struct LoraBackwardLayout {
   size_t wt, bt, at, dyp;     // 16-bit: Ŵᵀ [K, Np], Bᵀ [L, r, Np], Aᵀ [L, K, r], dY [T, Np]
   int64_t runs;
   size_t part, q, e;          // as in LoraLayout
-  size_t gs, hs, gmax, hmax;  // f32: [Tp, ranks padded to 16] twice, [Tp] twice
+  size_t gs, hs;              // f32 [Tp, ranks padded to 16]
   size_t token, pos, table, n_pieces, n_slots, first_slot, last_pos;
   size_t partial;             // f32 [slots, (K + N)·r]
   LoraCut cut;

@@ -44,8 +44,6 @@ struct LoraDown {
   const float* Hin;       // [T, r], with Ps
   float* Ps;              // P in the gradients' operand order, sorted by pos, or NULL
   float* Hs;              // Hin likewise
-  float* row_max;         // [Tp] max_j |P| at pos[t]
-  float* h_max;           // [Tp] max_j |Hin|
   const int32_t* pos;
   uint16_t* Q;            // [T, RW]: c·P as halves hi [r], lo [r], zeros up to RW, or NULL
   int RW;                 // 2r rounded up to 64
@@ -149,8 +147,6 @@ struct LoraGrad {
   const float* steps;     // [T, K / 128] or NULL
   const float* Gs;        // dY·B and H in operand order: [Tp / 32][16 ranks][lane][8]
   const float* Hs;
-  const float* g_max;     // [Tp] largest |value| of each token
-  const float* h_max;
   const float* scaling;
   const int* token;
   const LoraPiece* pieces;

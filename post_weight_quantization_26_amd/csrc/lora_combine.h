@@ -37,15 +37,15 @@ __device__ __forceinline__ void lora_combine(const LoraDown& p, int64_t block) {
     for (int k = 0; k < 2; ++k)
       if (lane + 64 * k < p.r) p.H[t * p.r + lane + 64 * k] = v[k];
   if (!has) return;
-  float m = fmaxf(fabsf(v[0]), fabsf(v[1])), mh = fmaxf(fabsf(h[0]), fabsf(h[1]));
-#pragma unroll
-  for (int o = 32; o; o >>= 1) {
-    m = fmaxf(m, __shfl_xor(m, o));
-    mh = fmaxf(mh, __shfl_xor(mh, o));
-  }
-  const float c = p.scaling[a], cm = fabsf(c) * m;
+  const float c = p.scaling[a];
   int e = 0;
-  if (F16 && !(cm >= 0x1p-3f && cm < 0x1p14f)) e = exponent_of(cm);
+  if constexpr (F16) {
+    float m = fmaxf(fabsf(v[0]), fabsf(v[1]));
+#pragma unroll
+    for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    const float cm = fabsf(c) * m;
+    if (!(cm >= 0x1p-3f && cm < 0x1p14f)) e = exponent_of(cm);
+  }
   const float down = exp2i(-e);
   uint16_t* q = p.Q + t * p.RW;
   const int pos = p.Ps ? p.pos[t] : 0;
@@ -68,13 +68,7 @@ __device__ __forceinline__ void lora_combine(const LoraDown& p, int64_t block) {
   }
   if (p.Q)
     for (int j = 2 * p.r + lane; j < p.RW; j += 64) q[j] = 0;
-  if (lane == 0) {
-    if (p.Q) p.E[t] = exp2i(e);
-    if (p.Ps) {
-      p.row_max[pos] = m;
-      p.h_max[pos] = mh;
-    }
-  }
+  if (lane == 0 && p.Q) p.E[t] = exp2i(e);
 }
 
 }  // namespace

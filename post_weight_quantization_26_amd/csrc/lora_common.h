@@ -32,12 +32,12 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   else return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, b16x2));
 }
 
-// The exponent e of a float32 magnitude in [2^e, 2^(e+1)), clamped to [-60, 60] (0 and values
-// that are not finite: 0).
+// The exponent e of a float32 magnitude in [2^e, 2^(e+1)), clamped to what leaves
+// 2^(14-e), 2^-e and 2^e normal numbers (0: the least, what is not finite: the largest).
+constexpr int kLeastExponent = -112, kLargestExponent = 126;
 __device__ __forceinline__ int exponent_of(float m) {
-  if (!(m > 0.f) || !(m < __builtin_inff())) return 0;
   const int e = int((__float_as_uint(m) >> 23) & 0xFFu) - 127;
-  return e < -60 ? -60 : e > 60 ? 60 : e;
+  return e < kLeastExponent ? kLeastExponent : e > kLargestExponent ? kLargestExponent : e;
 }
 
 __device__ __forceinline__ float exp2i(int e) {   // 2^e, -126 <= e <= 127

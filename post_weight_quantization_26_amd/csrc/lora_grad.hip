@@ -18,9 +18,11 @@
 // 8·(l % 16) + i for operand i. S lies in operand order ([step][16 ranks][lane]
 // [8 tokens], lora_down.hip), so its loads are contiguous.
 // S comes as float32 and is split in registers into two 16-bit halves, so
-// that its rounding is u² (bf16 2^-16). fp16 halves are scaled by one power
-// of two per piece that takes the piece's largest |S| to 2^14: a value 2^-17
-// times as large still keeps 2^-22 of itself.
+// that its rounding is u² (bf16 2^-16). fp16 halves are scaled by a power of two
+// that takes the largest |S| of their rank so far to 2^14 (a value 2^-17 times
+// as large still keeps 2^-22 of itself); where a step's is larger, the rank's
+// sums are scaled down to match. Each rank has its own: a small one beside a
+// large one, or beside one that is infinite, keeps its bits.
 //
 // An 8-bit checkpoint of X enters as its codes, exact in either 16-bit type, and
 // its steps go into S: a strip of 128 channels has one step per token. The
@@ -62,7 +64,6 @@ __device__ __forceinline__ void grad_piece(const LoraGrad& p, const LoraPiece& p
   const int64_t C = is_a ? p.K : p.N;
   const int jbs = (p.r + 15) / 16;
   const float* S = (is_a ? p.Gs : p.Hs) + int64_t(pc.pos / 32) * jbs * 512 + j0 / 16 * 512;
-  const float* row_max = is_a ? p.g_max : p.h_max;
   const int64_t c0 = strip * kGradStrip;
   const int64_t KB = p.K / 128;
 
@@ -70,18 +71,6 @@ __device__ __forceinline__ void grad_piece(const LoraGrad& p, const LoraPiece& p
   const int padded = (pc.n + 31) / 32 * 32;
   for (int i = threadIdx.x; i < padded; i += 64 * kGradWaves) tokens[i] = p.token[pc.pos + i];
   __syncthreads();
-  float scale = 1.f;
-  if constexpr (F16) {
-    float m = 0.f;
-    for (int i = lane; i < pc.n; i += 64) {
-      float v = row_max[pc.pos + i];
-      if constexpr (X8) v *= p.steps[int64_t(tokens[i]) * KB + strip];
-      m = fmaxf(m, v);
-    }
-#pragma unroll
-    for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-    if (m > 0.f && m < __builtin_inff()) scale = exp2i(14 - exponent_of(m));
-  }
   // Copy i brings rows 4i .. + 3 (8-bit: 8i .. + 7), 16 (8) lanes to a row; lanes
   // past the last column reread it.
   const char* Z = is_a ? static_cast<const char*>(p.X) : reinterpret_cast<const char*>(p.dY);
@@ -102,8 +91,53 @@ __device__ __forceinline__ void grad_piece(const LoraGrad& p, const LoraPiece& p
   for (int q = 0; q < JB; ++q)
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[q][i] = floatx4{0.f, 0.f, 0.f, 0.f};
+  // fp16: the exponent of the largest |S| so far of rank 16·q + lr
+  int top[JB];
+#pragma unroll
+  for (int q = 0; q < JB; ++q) top[q] = kLeastExponent;
 
   auto use = [&](const GradStage& st, const float4 (&sv)[JB][2], const float (&step)[8], int s) {
+    V sh[JB], sl[JB];
+#pragma unroll
+    for (int q = 0; q < JB; ++q) {
+      const float4 a = sv[q][0], b = sv[q][1];
+      float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if constexpr (X8) v[e] *= step[e];
+        if (s + 8 * lg + e >= pc.n) v[e] = 0.f;
+      }
+      if constexpr (F16) {
+        float m = fabsf(v[0]);
+#pragma unroll
+        for (int e = 1; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
+        m = fmaxf(m, __shfl_xor(m, 16));
+        m = fmaxf(m, __shfl_xor(m, 32));
+        const int now = exponent_of(m);
+        if (__ballot(now > top[q])) {
+          const int to = now > top[q] ? now : top[q];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int down = __shfl(top[q] - to, 4 * lg + u);   // of the sums' rank
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[q][i][u] = __builtin_ldexpf(acc[q][i][u], down);
+          }
+          top[q] = to;
+        }
+        const float scale = exp2i(14 - top[q]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= scale;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        hi[e] = pack2<F16>(v[2 * e], v[2 * e + 1]);
+        lo[e] = pack2<F16>(v[2 * e] - widen16<F16>(uint16_t(hi[e])),
+                          v[2 * e + 1] - widen16<F16>(uint16_t(hi[e] >> 16)));
+      }
+      sh[q] = __builtin_bit_cast(V, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+      sl[q] = __builtin_bit_cast(V, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+    }
     uint32_t z[8][X8 ? 2 : 4];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -119,27 +153,6 @@ __device__ __forceinline__ void grad_piece(const LoraGrad& p, const LoraPiece& p
         z[e][2] = x.z;
         z[e][3] = x.w;
       }
-    }
-    V sh[JB], sl[JB];
-#pragma unroll
-    for (int q = 0; q < JB; ++q) {
-      const float4 a = sv[q][0], b = sv[q][1];
-      float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if constexpr (X8) v[e] *= step[e];
-        if constexpr (F16) v[e] *= scale;
-        if (s + 8 * lg + e >= pc.n) v[e] = 0.f;
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        hi[e] = pack2<F16>(v[2 * e], v[2 * e + 1]);
-        lo[e] = pack2<F16>(v[2 * e] - widen16<F16>(uint16_t(hi[e])),
-                          v[2 * e + 1] - widen16<F16>(uint16_t(hi[e] >> 16)));
-      }
-      sh[q] = __builtin_bit_cast(V, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-      sl[q] = __builtin_bit_cast(V, make_uint4(lo[0], lo[1], lo[2], lo[3]));
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -214,7 +227,7 @@ __device__ __forceinline__ void grad_piece(const LoraGrad& p, const LoraPiece& p
   float(*const red[2])[kGradStrip] = {reinterpret_cast<float(*)[kGradStrip]>(&z0),
                                       reinterpret_cast<float(*)[kGradStrip]>(&z1)};
   // lane l holds channel 8·(l % 16) + i and ranks 16·q + 4·(l / 16) + v
-  const float post = pc.n ? p.scaling[pc.a] / scale : 0.f;   // no tokens: zeros
+  const float post = pc.n ? p.scaling[pc.a] : 0.f;   // no tokens: zeros
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     if (wave >> 1 == half) {
@@ -224,10 +237,14 @@ __device__ __forceinline__ void grad_piece(const LoraGrad& p, const LoraPiece& p
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           float* row = &R[16 * q + 4 * lg + v][8 * lr];
+          const int up = F16 ? __shfl(top[q], 4 * lg + v) - 14 : 0;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float4 x = make_float4(acc[q][4 * h][v], acc[q][4 * h + 1][v], acc[q][4 * h + 2][v],
                                    acc[q][4 * h + 3][v]);
+            if constexpr (F16)
+              x = make_float4(__builtin_ldexpf(x.x, up), __builtin_ldexpf(x.y, up),
+                              __builtin_ldexpf(x.z, up), __builtin_ldexpf(x.w, up));
             if (half) {
               const float4 y = *reinterpret_cast<const float4*>(row + 4 * h);
               x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);

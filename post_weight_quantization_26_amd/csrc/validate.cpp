@@ -623,8 +623,6 @@ LoraBackwardLayout lora_backward_layout(int64_t T, int64_t N, int64_t K, int32_t
   }
   l.gs = take(tp * size_t(ceil_div(r, 16) * 16) * 4);
   l.hs = take(tp * size_t(ceil_div(r, 16) * 16) * 4);
-  l.gmax = take(tp * 4);
-  l.hmax = take(tp * 4);
   l.token = take(tp * 4);
   l.pos = take(t * 4);
   l.table = take(size_t(l.pieces) * 16);

@@ -44,7 +44,8 @@ def test_small_gradients_from_a_checkpoint(api):
     check_backward(api, p, True)
 
 
-@pytest.mark.parametrize("dtype,x8", [("bf16", False), ("bf16", True)])
+@pytest.mark.parametrize("dtype,x8", [("bf16", False), ("bf16", True), ("f16", False),
+                                      ("f16", True)])
 @pytest.mark.parametrize("T", [100, 2500])
 def test_an_infinite_rank_leaves_the_others(api, T, dtype, x8):
     """One infinity in a column of B_a makes that rank of g infinite, one in H
@@ -80,3 +81,15 @@ def test_an_infinite_rank_leaves_the_others(api, T, dtype, x8):
     eB = worst(f64(dB)[:, :, keep], db[:, :, keep], bB[:, :, keep])
     print(f"T={T} {dtype} x8={x8}: dA {eA:.3f}, dB {eB:.3f} of the bounds", flush=True)
     assert eA <= 1 and eB <= 1
+
+
+@pytest.mark.parametrize("x8", [False, True])
+@pytest.mark.parametrize("order", [1, -1])
+def test_gradients_of_growing_and_shrinking_tokens(api, order, x8):
+    """fp16: dY (so g) and h of the tokens of one run span 2^20."""
+    T = 1100
+    p = Problem(T, 264, 384, 24, 2, "f16", kind="one", seed=31)
+    p.c[:] = 3.0
+    scale_by(p, "dy", (2.0 ** (10 * np.arange(T) / T - 5)[::order])[:, None])
+    scale_by(p, "B", 2.0 ** (np.arange(24) % 11 - 5.0))
+    check_backward(api, p, x8)
