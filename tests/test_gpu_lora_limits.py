@@ -1,11 +1,12 @@
-"""GPU: the adapter calls where magnitudes differ or values are not finite.
-Bounds as derived in test_gpu_lora.py."""
+"""GPU: the adapter calls where magnitudes differ or values are not finite, and
+where the 256x256 kernel takes whole and cut tiles together. Bounds as derived
+in test_gpu_lora.py; what a broken value does not reach is equal bit for bit."""
 import numpy as np
 import pytest
 import torch
 
 import lora_reference as R
-from test_gpu_lora import Problem, check_backward, dev, f64, worst
+from test_gpu_lora import Problem, check_backward, check_forward, dev, f64, worst
 from test_gpu_w4a16 import _dec, _enc
 
 pytestmark = pytest.mark.gpu
@@ -93,3 +94,67 @@ def test_gradients_of_growing_and_shrinking_tokens(api, order, x8):
     scale_by(p, "dy", (2.0 ** (10 * np.arange(T) / T - 5)[::order])[:, None])
     scale_by(p, "B", 2.0 ** (np.arange(24) % 11 - 5.0))
     check_backward(api, p, x8)
+
+
+# One broken value of B (forward) or A (gradient) alone reaches exactly the
+# outputs in its row (column). K (N) = 128 leaves the last 256x256 tiles whole,
+# 640 cuts them; rank 40 and 128 take more than one 64-column chunk; up to 384
+# (320) tokens take the other form.
+@pytest.mark.parametrize("T,C,r,dtype", [
+    (12, 640, 16, "bf16"), (200, 640, 40, "f16"), (700, 128, 16, "f16"), (700, 640, 16, "bf16"),
+    (700, 128, 128, "bf16"), (700, 640, 40, "f16"),
+])
+def test_a_broken_value_reaches_its_own_outputs(api, T, C, r, dtype):
+    bad = {7: (2, "nan"), 100: (0, "-inf"), 300: (r - 1, "inf"), 511: (r // 2, "inf")}
+
+    def compare(got, want, ids):
+        own = torch.from_numpy(ids == 1).to("cuda:0")
+        hit = torch.zeros_like(want, dtype=torch.bool)
+        hit[:, list(bad)] = own[:, None]
+        assert own.any() and not torch.isfinite(got[hit]).any()
+        assert torch.equal(got[~hit].view(torch.int16), want[~hit].view(torch.int16))
+
+    p = Problem(T, 520, C, r, 4, dtype, kind="tokens", seed=T + C)
+    p.ids[:4] = [0, 1, 2, 3]
+    A, B, c, ids = p.lora()
+    X, lay = p.td(p.Xb), p.layer()
+    y0 = api.w4a16_lora_matmul(X, *lay, A, B, c, ids)
+    for n, (j, v) in bad.items():
+        B[1, n, j] = float(v)
+    y = api.w4a16_lora_matmul(X, *lay, A, B, c, ids)
+    torch.cuda.synchronize()
+    compare(y, y0, p.ids)
+
+    p = Problem(T, C, 640, r, 4, dtype, kind="tokens", seed=T + C + 1)
+    p.ids[:4] = [0, 1, 2, 3]
+    A, B, c, ids = p.lora()
+    X, dY, lay, h = p.td(p.Xb), p.td(p.dYb), p.layer(), dev(np.ones((T, r), np.float32))
+    dx0, da0, db0 = api.w4a16_lora_backward(dY, X, h, *lay, A, B, c, ids)
+    for k, (j, v) in bad.items():
+        A[1, j, k] = float(v)
+    dx, da, db = api.w4a16_lora_backward(dY, X, h, *lay, A, B, c, ids)
+    torch.cuda.synchronize()
+    compare(dx, dx0, p.ids)
+    assert torch.equal(da, da0) and torch.equal(db, db0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_whole_and_cut_tiles_together(api, dtype):
+    """272 tiles of 256x256: 256 whole ones and 16 cut into runs, every column
+    tile and both kinds with real data, and a broken value in each kind."""
+    p = Problem(4300, 4000, 640, 16, 5, dtype, kind="runs", seed=2)
+    check_forward(api, p)
+    A, B, c, ids = p.lora()
+    X, lay = p.td(p.Xb), p.layer()
+    y0 = api.w4a16_lora_matmul(X, *lay, A, B, c, ids)
+    a = int(p.ids[p.ids >= 0][-1])
+    cols = [3, 3999]
+    for n in cols:
+        B[a, n, 1] = float("nan")
+    y = api.w4a16_lora_matmul(X, *lay, A, B, c, ids)
+    torch.cuda.synchronize()
+    hit = torch.zeros_like(y0, dtype=torch.bool)
+    hit[:, cols] = torch.from_numpy(p.ids == a).to("cuda:0")[:, None]
+    assert torch.isnan(y[hit]).all()
+    assert torch.equal(y[~hit].view(torch.int16), y0[~hit].view(torch.int16))
+    check_backward(api, Problem(4300, 584, 4096, 16, 3, dtype, kind="runs", seed=4))
