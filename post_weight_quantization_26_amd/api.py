@@ -44,6 +44,11 @@ def _dtype(t: torch.Tensor) -> int:
     return _DT[t.dtype]
 
 
+def _check_group(group: int) -> None:
+    if group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128, not {group}")
+
+
 def workspace_bytes(op: int, T: int, N: int, K: int, n_grid: int, dtype: torch.dtype) -> int:
     return int(L.lib().awq_workspace_bytes(op, T, N, K, n_grid, _DT[dtype]))
 
@@ -327,6 +332,7 @@ def quantize_pack(W: torch.Tensor, s: torch.Tensor, ratio: Optional[torch.Tensor
     _dev(W, "W"), _dev(s, "s")
     if ratio is not None:
         _dev(ratio, "ratio")
+    _check_group(group)
     N, K = W.shape
     if out is None:
         nw = N * int(bits) // 32
@@ -362,6 +368,7 @@ def w4a16_matmul(X: torch.Tensor, qweight: torch.Tensor, qzeros: torch.Tensor,
     _dev(X, "X"), _dev(qweight, "qweight"), _dev(qzeros, "qzeros"), _dev(scales, "scales")
     if bits not in (3, 4):
         raise ValueError("bits must be 3 or 4")
+    _check_group(group)
     T, K = X.shape
     N = scales.shape[1]
     cols = N * bits // 32
@@ -442,6 +449,7 @@ def _lora_args(V: torch.Tensor, V_cols: str, qweight, qzeros, scales, A, B, scal
     vs, qs, ss, az = V.shape, qweight.shape, scales.shape, A.shape
     if len(vs) != 2 or len(qs) != 2 or len(ss) != 2 or len(az) != 3:
         raise ValueError(f"{V_cols}, qweight and scales must have 2 dimensions, A 3")
+    _check_group(group)
     T, K, N = vs[0], qs[0], ss[1]
     n, r = az[0], az[1]
     if qs[1] * 8 != N or qzeros.shape != (K // group, N // 8) or \

@@ -158,3 +158,20 @@ def test_whole_and_cut_tiles_together(api, dtype):
     assert torch.isnan(y[hit]).all()
     assert torch.equal(y[~hit].view(torch.int16), y0[~hit].view(torch.int16))
     check_backward(api, Problem(4300, 584, 4096, 16, 3, dtype, kind="runs", seed=4))
+
+
+def test_a_group_size_that_is_none_is_refused(api):
+    """0 and sizes the layout does not have, by name, in every call that takes a
+    packed layer."""
+    p = Problem(20, 264, 384, 16, 2, "bf16", kind="tokens", seed=1)
+    X, dY, h = p.td(p.Xb), p.td(p.dYb), torch.zeros(20, 16, device="cuda:0")
+    lay, lora = p.layer(), p.lora()
+    s = torch.ones(384, device="cuda:0")
+    W = torch.zeros(264, 384, dtype=torch.bfloat16, device="cuda:0")
+    for group in (0, -128, 16, 256):
+        for call in (lambda: api.w4a16_lora_matmul(X, *lay, *lora, group=group),
+                     lambda: api.w4a16_lora_backward(dY, X, h, *lay, *lora, group=group),
+                     lambda: api.w4a16_matmul(X, *lay, group=group),
+                     lambda: api.quantize_pack(W, s, group=group)):
+            with pytest.raises(ValueError, match="group must be 32, 64 or 128"):
+                call()
