@@ -400,17 +400,25 @@ awq_status awq_w4a16_matmul(const void* X, awq_dtype dtype, int64_t T, int64_t N
  * ids [T] int32. An id outside [0, L) means no adapter (y_t = Ŵ·x_t, h_t =
  * 0); ids may come in any order. r is a multiple of 8, 8..128 (pad shorter
  * adapters with zeros); 1 <= L <= 4096. A, B, scaling and ids stay on the
- * device: nothing is read back.
+ * device: nothing is read back. 4-bit layers only (3-bit ones: awq_w3a16_matmul,
+ * without adapters).
+ * The layer holds W·diag(s) and X comes divided by s. An adapter trained beside
+ * the unquantised W therefore joins it as A_a·diag(s) (dA times s, channel by
+ * channel, is then the gradient of the A_a it came from), one trained through
+ * these calls is used as it is; where awq_fold_linear divided the rows of a layer,
+ * the rows of its adapters' B_a are divided too.
  * Y [T, N] in X's type. For training, optionally (NULL = not wanted):
  * H [T, r] f32 receives the h_t, and x8_codes [T, K] int8 with x8_steps
  * [T, K/128] f32 the 8-bit checkpoint of X that awq_act_pack8 would write
  * (both or neither).
  * Sums are float32 and each output is rounded once. T <= 16 uses the exact Ŵ
  * in float32, larger T Ŵ rounded once to X's type; h_t meets B_a as the sum of
- * two 16-bit halves (2^-16 of it is lost with bf16, 2^-22 with fp16). An
+ * two 16-bit halves (2^-16 of it is lost with bf16, 2^-22 of the token's largest
+ * with fp16). An
  * adapter's NaN or infinity reaches its own tokens only, whose outputs in the
  * rows of B_a (columns of A_a, in the gradient) that hold it are then NaN or
- * infinite. N a multiple of 8, K of 128, both
+ * infinite, and all of whose outputs may be where A_a (B_a) holds it.
+ * N a multiple of 8, K of 128, both
  * and T within awq_w4a16_matmul's limits. X, qweight, qzeros, scales, A, B,
  * Y, H, x8_codes and ws 16-byte aligned, scaling, ids and x8_steps 4-byte.
  * Outputs may not overlap inputs. ws: at least
@@ -435,7 +443,12 @@ awq_status awq_w4a16_lora_matmul(const void* X, awq_dtype dtype, int64_t T, int6
  * read for dA only. dX [T, K] (NULL = not wanted: neither the packed layer
  * nor A is read then), dA [L, r, K] and dB [L, N, r] are overwritten, in dY's type,
  * each value summed in float32 and rounded once; an adapter without tokens
- * gets zeros. Sums run in an order that the arguments fix: equal calls give
+ * gets zeros. dX takes Ŵ rounded once to dY's type at every T, also up to 16, where
+ * the forward call has the exact one. g_t meets A_a as h_t meets B_a above. For dA
+ * and dB each rank of g_t (with a checkpoint times the block's step) and of h_t
+ * enters as the sum of two 16-bit halves too: 2^-16 of a value is lost with bf16,
+ * with fp16 2^-22 of it or 2^-39 of the rank's largest over the adapter's tokens,
+ * whichever is more. Sums run in an order that the arguments fix: equal calls give
  * equal bits. Alignment as above (dX, dA, dB 16-byte); ws: at least
  * awq_w4a16_lora_backward_workspace_bytes(T, N, K, L, r, dtype) bytes. N
  * at most 2^22 - 128. Does not synchronise. */

@@ -474,9 +474,10 @@ def w4a16_lora_matmul(X: torch.Tensor, qweight: torch.Tensor, qzeros: torch.Tens
                       h: Optional[torch.Tensor] = None, x8=None) -> torch.Tensor:
     """Low-rank adapters of many requests beside a packed 4-bit layer:
     Y[t] = Ŵ·x_t + scaling[a]·B[a]·(A[a]·x_t) with a = ids[t]; an id outside
-    [0, L) means no adapter. X [T, K] and the layer as in w4a16_matmul, A
-    [L, r, K] and B [L, N, r] in X's dtype, scaling [L] float32, ids [T]
-    int32. For training: ``h`` [T, r] float32 receives A[a]·x_t and ``x8`` =
+    [0, L) means no adapter. X [T, K] (already divided by s) and the 4-bit
+    layer as in w4a16_matmul, A [L, r, K] and B [L, N, r] in X's dtype,
+    scaling [L] float32, ids [T] int32. Adapters of the unquantised layer
+    enter with A times s, channel by channel. For training: ``h`` [T, r] float32 receives A[a]·x_t and ``x8`` =
     (codes, steps) the checkpoint of X that act_pack8 would make, both for
     w4a16_lora_backward. Returns Y [T, N] in X's dtype."""
     T, N, K, n, r = _lora_args(X, "X", qweight, qzeros, scales, A, B, scaling, ids, group)
@@ -506,8 +507,9 @@ def w4a16_lora_backward(dY: torch.Tensor, X, h: torch.Tensor, qweight: torch.Ten
                         want_dx: bool = True):
     """The gradient of w4a16_lora_matmul: (dX [T, K], dA [L, r, K], dB
     [L, N, r]) in dY's dtype from dY [T, N], the ``h`` that the forward call
-    wrote and X, its input or that input's checkpoint (codes, steps). dX is
-    None with want_dx False. ``out`` = (dX, dA, dB) gives the buffers."""
+    wrote and X, its input or that input's checkpoint (codes, steps). dX
+    takes Ŵ rounded to dY's dtype at every T; it is None with want_dx False.
+    ``out`` = (dX, dA, dB) gives the buffers."""
     T, N, K, n, r = _lora_args(dY, "dY", qweight, qzeros, scales, A, B, scaling, ids, group)
     steps = None
     if isinstance(X, (tuple, list)):
