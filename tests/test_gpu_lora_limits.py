@@ -206,3 +206,37 @@ def test_adapters_of_the_unquantised_layer(api):
     want = g.T @ x
     bound = (u + low + R.gamma(N + T + 4)) * (mg.T @ np.abs(x)) + u * np.abs(want)
     assert worst(f64(dA[0]) * f64(s), want, bound) <= 1
+
+
+# The least layers: one word of outputs (most of each tile past the end), and
+# the steps up to whole 16-byte copies of the words.
+@pytest.mark.parametrize("T", [1, 16, 17, 33, 321, 400])
+@pytest.mark.parametrize("N", [8, 16, 24, 32, 40])
+def test_least_layers(api, T, N):
+    dtype = "bf16" if (T + N // 8) % 2 else "f16"
+    group = (32, 64, 128)[(T + N // 8) % 3]
+    p = Problem(T, N, 128, 8, 2, dtype, group, "tokens", seed=T * N)
+    check_forward(api, p)
+    check_backward(api, p, x8=bool(N & 8))
+
+
+@pytest.mark.parametrize("T", [5, 200, 500])
+def test_each_output_by_itself(api, T):
+    """H without a checkpoint, a checkpoint without H, gradients without dX
+    from a checkpoint: the same bits as with everything asked for."""
+    p = Problem(T, 264, 384, 24, 3, "bf16", kind="tokens", seed=T)
+    X, dY, lay, lora = p.td(p.Xb), p.td(p.dYb), p.layer(), p.lora()
+    new = lambda: (torch.empty(T, 24, device="cuda:0"),
+                   (torch.empty(T, 384, dtype=torch.int8, device="cuda:0"),
+                    torch.empty(T, 3, device="cuda:0")))
+    h, x8 = new()
+    y = api.w4a16_lora_matmul(X, *lay, *lora, h=h, x8=x8)
+    h1, x81 = new()
+    y1 = api.w4a16_lora_matmul(X, *lay, *lora, h=h1)
+    y2 = api.w4a16_lora_matmul(X, *lay, *lora, x8=x81)
+    _, da, db = api.w4a16_lora_backward(dY, x8, h, *lay, *lora)
+    none, da1, db1 = api.w4a16_lora_backward(dY, x8, h, *lay, *lora, want_dx=False)
+    torch.cuda.synchronize()
+    assert none is None
+    for a, b in ((y, y1), (y, y2), (h, h1), (x8[0], x81[0]), (x8[1], x81[1]), (da, da1), (db, db1)):
+        assert torch.equal(a, b)
