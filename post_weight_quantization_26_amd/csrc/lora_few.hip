@@ -412,8 +412,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void lora_few_down_kernel(LoraFew p
 // they add up in LDS in order. The rows' h (summed over the runs of k) become
 // two 16-bit halves in LDS, as in lora_down.hip; an adapter takes one pass of
 // MFMAs whose rows are kept where they belong to it.
-// Bound by the reads of B and of the partial sums: 64 tokens of 48 adapters,
-// rank 32, 28672 outputs (88 MB of B, 15 MB of sums) 21 us; 200 tokens of 6
+// Bound by the reads of B, once per 16 tokens, and of the partial sums: 64 tokens
+// with any of 48 adapters, rank 32, 28672 outputs (about 88 MB of B for the 62 MB
+// that the 34 adapters in use hold, 15 MB of sums) 21 us; 200 tokens of 6
 // adapters, rank 8, 4096 outputs (13 MB of sums) 9.8 us. Partial sums read in
 // the MFMA's layout, a dword a lane: 27 and 13 us. B through LDS: 35 and 17.5.
 constexpr int kFinishCols = 32;
@@ -578,8 +579,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void lora_few_finish_kernel(LoraFew
 template <bool F16, int MT>
 void launch_few(const LoraFew& p, int downs, unsigned grid, hipStream_t st) {
   // copies of 16 bytes a lane where rows of words allow it, else of 4 bytes:
-  // 70.6 against 73 us for the call with 64 tokens of 28672x8192, 48 against 50
-  // with 32
+  // 91.1 against 94.6 us for a call of 64 tokens of 28672x8192, bf16, rank 32, 48
+  // adapters, 67.0 against 69.6 with 32 tokens
   const bool wide = p.w.N % 32 == 0;
   if (p.w.group == 32) {
     if (wide) lora_few_kernel<F16, MT, true, true><<<grid, 256, 0, st>>>(p, downs);

@@ -6,8 +6,8 @@
 // and one narrow side (r). Both are Zᵀ·S with Z = X or dY, read once, and S
 // the narrow side in the plan's sorted order. Bound by the reads of Z, with S,
 // which every workgroup reads for its 128 columns, from L2: fp16, 2051 tokens of
-// 4096x11008, rank 32: 20 us for 62 MB of Z; bf16, 8192 tokens of 11008x4096,
-// rank 64, 8-bit X: 78 us for 213 MB. (S as halves from memory, and S loaded a
+// 4096x11008, rank 32: 21 us for 62 MB of Z; bf16, 8192 tokens of 11008x4096,
+// rank 64, 8-bit X: 61 to 67 us for 213 MB. (S as halves from memory, and S loaded a
 // step ahead, were no faster.)
 //
 // A workgroup takes 128 columns of Z, up to 64 ranks and one piece of a run;
