@@ -44,9 +44,11 @@ def _dtype(t: torch.Tensor) -> int:
     return _DT[t.dtype]
 
 
-def _check_group(group: int) -> None:
-    if group not in (32, 64, 128):
-        raise ValueError(f"group must be 32, 64 or 128, not {group}")
+def _groups(K: int, group: int) -> int:
+    """Groups of K channels; a size the library would refuse before it divides."""
+    if group < 1:
+        raise L.AwqError(L.AWQ_E_UNSUPPORTED, f"group_size {group} not supported (32, 64 or 128)")
+    return K // group
 
 
 def workspace_bytes(op: int, T: int, N: int, K: int, n_grid: int, dtype: torch.dtype) -> int:
@@ -332,13 +334,12 @@ def quantize_pack(W: torch.Tensor, s: torch.Tensor, ratio: Optional[torch.Tensor
     _dev(W, "W"), _dev(s, "s")
     if ratio is not None:
         _dev(ratio, "ratio")
-    _check_group(group)
     N, K = W.shape
     if out is None:
         nw = N * int(bits) // 32
         qweight = torch.empty((K, nw), dtype=torch.int32, device=W.device)
-        qzeros = torch.empty((K // group, nw), dtype=torch.int32, device=W.device)
-        scales = torch.empty((K // group, N), dtype=torch.float16, device=W.device)
+        qzeros = torch.empty((_groups(K, group), nw), dtype=torch.int32, device=W.device)
+        scales = torch.empty((_groups(K, group), N), dtype=torch.float16, device=W.device)
     else:
         qweight, qzeros, scales = out
     ws = _workspace(ws, workspace_bytes(L.AWQ_OP_PACK, 1, N, K, 1, W.dtype), W.device)
@@ -368,12 +369,11 @@ def w4a16_matmul(X: torch.Tensor, qweight: torch.Tensor, qzeros: torch.Tensor,
     _dev(X, "X"), _dev(qweight, "qweight"), _dev(qzeros, "qzeros"), _dev(scales, "scales")
     if bits not in (3, 4):
         raise ValueError("bits must be 3 or 4")
-    _check_group(group)
     T, K = X.shape
     N = scales.shape[1]
     cols = N * bits // 32
-    if qweight.shape != (K, cols) or qzeros.shape != (K // group, cols) or \
-            scales.shape != (K // group, N):
+    G = _groups(K, group)
+    if qweight.shape != (K, cols) or qzeros.shape != (G, cols) or scales.shape != (G, N):
         raise ValueError("packed layer shapes do not match X and the group size")
     Y = out if out is not None else torch.empty((T, N), dtype=X.dtype, device=X.device)
     if bits == 4:
@@ -449,11 +449,11 @@ def _lora_args(V: torch.Tensor, V_cols: str, qweight, qzeros, scales, A, B, scal
     vs, qs, ss, az = V.shape, qweight.shape, scales.shape, A.shape
     if len(vs) != 2 or len(qs) != 2 or len(ss) != 2 or len(az) != 3:
         raise ValueError(f"{V_cols}, qweight and scales must have 2 dimensions, A 3")
-    _check_group(group)
     T, K, N = vs[0], qs[0], ss[1]
     n, r = az[0], az[1]
-    if qs[1] * 8 != N or qzeros.shape != (K // group, N // 8) or \
-            ss[0] != K // group or vs[1] != (K if V_cols == "X" else N):
+    G = _groups(K, group)
+    if qs[1] * 8 != N or qzeros.shape != (G, N // 8) or \
+            ss[0] != G or vs[1] != (K if V_cols == "X" else N):
         raise ValueError(f"packed layer shapes do not match {V_cols} and the group size")
     if qweight.dtype != torch.int32 or qzeros.dtype != torch.int32 or \
             scales.dtype != torch.float16:
