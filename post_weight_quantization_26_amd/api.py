@@ -477,9 +477,9 @@ def w4a16_lora_matmul(X: torch.Tensor, qweight: torch.Tensor, qzeros: torch.Tens
     [0, L) means no adapter. X [T, K] (already divided by s) and the 4-bit
     layer as in w4a16_matmul, A [L, r, K] and B [L, N, r] in X's dtype,
     scaling [L] float32, ids [T] int32. Adapters of the unquantised layer
-    enter with A times s, channel by channel. For training: ``h`` [T, r] float32 receives A[a]·x_t and ``x8`` =
-    (codes, steps) the checkpoint of X that act_pack8 would make, both for
-    w4a16_lora_backward. Returns Y [T, N] in X's dtype."""
+    enter with A times s, channel by channel. For training: ``h`` [T, r]
+    float32 receives A[a]·x_t and ``x8`` = (codes, steps) the checkpoint of X
+    that act_pack8 would make, both for w4a16_lora_backward. Returns Y [T, N] in X's dtype."""
     T, N, K, n, r = _lora_args(X, "X", qweight, qzeros, scales, A, B, scaling, ids, group)
     Y = _out(out, (T, N), X.dtype, X, "out")
     codes = steps = None
