@@ -476,6 +476,104 @@ awq_status awq_act_pack8(const void* X, awq_dtype dtype, int64_t T, int64_t K, i
 awq_status awq_act_unpack8(const int8_t* codes, const float* steps, awq_dtype dtype, int64_t T,
                            int64_t K, void* X, void* stream);
 
+/* Rows in 8 bits, one step per row: the operands of the 8-bit products below.
+ * IEEE float32 with one rounding per operation,
+ *   x' = x·s_k (s NULL: x);  m = max(max_k |x'|, 2^-100);  step = m / 127;
+ *   code = rint(x'·(127 / m)),
+ * codes [T, K] int8 in -127..127 and steps [T] f32. A row that holds a NaN or
+ * an infinity gets the step NaN and codes 0. With tokens as rows it quantises
+ * activations (one step per token); with output channels as rows, [N, K]
+ * weights, and s, the 8-bit layer of W·diag(s), whose input is divided by s as
+ * the packed layer's is. awq_dequantize_rows8 writes x^ = code·step, one
+ * float32 product rounded once to `dtype` (a value within a rounding of the
+ * type's largest may come back as an infinity). X bf16, f16 or f32, K any up to
+ * 65536, at most 2^34 elements; X, s, codes and steps aligned to their
+ * elements (rows of a multiple of 8 values with 16-byte aligned buffers run
+ * faster). Outputs must not overlap inputs. Neither synchronises. */
+awq_status awq_quantize_rows8(const void* X, awq_dtype dtype, int64_t T, int64_t K,
+                              const float* s, int8_t* codes, float* steps, void* stream);
+awq_status awq_dequantize_rows8(const int8_t* codes, const float* steps, awq_dtype dtype,
+                                int64_t T, int64_t K, void* X, void* stream);
+
+/* Layer norm of every row of X [T, K], or its root-mean-square form (rms not 0:
+ * mean 0):
+ *   r = 1 / sqrt(mean_k (x - mean)^2 + eps);  y = (x - mean)·r·gamma + beta
+ * in float32. gamma and beta (NULL: none) [K] are of `dtype` or float32
+ * (weight_dtype); what awq_fold_norm leaves in them joins here. Outputs, each
+ * NULL if not wanted but not all: Y [T, K] in X's type; stats [T, 2] f32, mean
+ * (0 if rms) and r, for the gradient; codes [T, K] with steps [T], the 8-bit
+ * rows of the float32 y (not of the rounded Y). K any up to 16384, at most
+ * 2^34 elements, eps finite and not negative. Alignment as above (stats 8
+ * bytes); outputs must not overlap inputs. Does not synchronise.
+ *
+ * The gradient, from dY and the forward call's X and stats:
+ *   xh = (x - mean)·r;  d = dy·gamma;
+ *   dx = r·(d - mean_k d - xh·mean_k(d·xh))   (rms: without mean_k d, and the
+ *                                              mean in stats is not read)
+ *   dgamma = Σ_t dy·xh;  dbeta = Σ_t dy       (dbeta NULL: not wanted)
+ * dX in X's type, dgamma and dbeta in weight_dtype, each overwritten, summed
+ * in float32 in an order that the arguments fix and rounded once. ws: at least
+ * awq_layer_norm_backward_workspace_bytes(T, K) bytes, 16-byte aligned. */
+awq_status awq_layer_norm(const void* X, awq_dtype dtype, int64_t T, int64_t K,
+                          const void* gamma, const void* beta, awq_dtype weight_dtype, float eps,
+                          int32_t rms, void* Y, float* stats, int8_t* codes, float* steps,
+                          void* stream);
+size_t awq_layer_norm_backward_workspace_bytes(int64_t T, int64_t K);
+awq_status awq_layer_norm_backward(const void* dY, const void* X, const float* stats,
+                                   awq_dtype dtype, int64_t T, int64_t K, const void* gamma,
+                                   awq_dtype weight_dtype, int32_t rms, void* dX, void* dgamma,
+                                   void* dbeta, void* ws, size_t ws_bytes, void* stream);
+
+/* Products of 8-bit rows with an 8-bit layer (codes [N, K] int8, steps [N] f32,
+ * both as awq_quantize_rows8 writes them):
+ *   Y[t][n] = steps_t·wsteps_n·Σ_k codes[t][k]·qweight[n][k] + bias[n]
+ * The sum is exact (int32); it is rounded to float32, multiplied by steps_t and
+ * by wsteps_n, the bias (NULL: none; in `dtype`) is added, and the result is
+ * rounded once to `dtype` (bf16 or f16). A step that is NaN makes its row or
+ * column NaN. K a multiple of 128 below 131072 (the sum fits 32 bits with codes
+ * down to -128), N and T any, N*K at most 2^34. codes, qweight, Y, G and U
+ * 16-byte aligned, bias 2, steps 4. ws: at least awq_w8a8_workspace_bytes(T, N,
+ * K, layers) bytes, 16-byte aligned (NULL where that is 0), layers 1, or 2 for
+ * a gated pair. Does not synchronise.
+ *
+ * awq_w8a8_gated_matmul takes two layers of one input (gate and up):
+ *   H = act(G)·U,  act AWQ_ACT_SILU g / (1 + e^-g) or AWQ_ACT_GELU g·Phi(g),
+ * G and U the products above in float32; H is rounded once. G and U [T, N]
+ * (both NULL: not kept) receive them in `dtype`, for the gradient.
+ *
+ * Gradients with respect to the input, taken as the values that its 8-bit rows
+ * stand for (the rounding to codes counts as the identity), from dY [T, N] in
+ * `dtype` (bf16 or f16):
+ *   dx = Σ_n (dy_n·wsteps_n)·qweight[n],
+ * and of a pair, from dH and the forward call's G and U:
+ *   dg = dh·u·act'(g);  du = dh·act(g);
+ *   dx = Σ_n (dg_n·gsteps_n)·gate[n] + Σ_n (du_n·usteps_n)·up[n].
+ * dX [T, K], dG and dU [T, N] are overwritten in `dtype`. The products with the
+ * steps are rounded to 16 bits before they meet the codes (fp16: with a power
+ * of two per row, so that 2^-24 of a row's largest survives); sums are
+ * float32. The layers are not trained. N below 2^21; ws: at least
+ * awq_w8a8_backward_workspace_bytes(T, N, K, layers) bytes. */
+enum { AWQ_ACT_SILU = 0, AWQ_ACT_GELU = 1 };
+size_t awq_w8a8_workspace_bytes(int64_t T, int64_t N, int64_t K, int32_t layers);
+awq_status awq_w8a8_matmul(const int8_t* codes, const float* steps, int64_t T, int64_t N,
+                           int64_t K, const int8_t* qweight, const float* wsteps,
+                           const void* bias, awq_dtype dtype, void* Y, void* ws, size_t ws_bytes,
+                           void* stream);
+awq_status awq_w8a8_gated_matmul(const int8_t* codes, const float* steps, int64_t T, int64_t N,
+                                 int64_t K, const int8_t* gate, const float* gsteps,
+                                 const int8_t* up, const float* usteps, int32_t act,
+                                 awq_dtype dtype, void* H, void* G, void* U, void* ws,
+                                 size_t ws_bytes, void* stream);
+size_t awq_w8a8_backward_workspace_bytes(int64_t T, int64_t N, int64_t K, int32_t layers);
+awq_status awq_w8a8_backward(const void* dY, awq_dtype dtype, int64_t T, int64_t N, int64_t K,
+                             const int8_t* qweight, const float* wsteps, void* dX, void* ws,
+                             size_t ws_bytes, void* stream);
+awq_status awq_w8a8_gated_backward(const void* dH, const void* G, const void* U, awq_dtype dtype,
+                                   int64_t T, int64_t N, int64_t K, const int8_t* gate,
+                                   const float* gsteps, const int8_t* up, const float* usteps,
+                                   int32_t act, void* dX, void* dG, void* dU, void* ws,
+                                   size_t ws_bytes, void* stream);
+
 /* Message for the last non-OK status returned on the calling thread. */
 const char* awq_last_error(void);
 
@@ -487,11 +585,12 @@ const char* awq_last_error(void);
  * candidates), 3 search GEMM, 4 reductions, 5 pack, 6 fold, 7 W4A16
  * dequantisation, 8 W4A16 GEMM or GEMV, 9 W4A16 GEMV reduction, 10 Gram
  * matrix build (transpose + G), 11 Gram-path candidate GEMM, 12 low-rank
- * adapter calls (all kernels of a call as one), 13 8-bit checkpoints. */
+ * adapter calls (all kernels of a call as one), 13 8-bit checkpoints, 14 8-bit
+ * rows, 15 norms and 16 8-bit products (all kernels of a call as one). */
 enum { AWQ_K_STATS = 0, AWQ_K_SCALE = 1, AWQ_K_TRANSFORM = 2, AWQ_K_GEMM = 3, AWQ_K_REDUCE = 4,
        AWQ_K_PACK = 5, AWQ_K_FOLD = 6, AWQ_K_DEQUANT = 7, AWQ_K_W4A16 = 8,
        AWQ_K_W4A16_REDUCE = 9, AWQ_K_GRAM_BUILD = 10, AWQ_K_GRAM_SEARCH = 11, AWQ_K_LORA = 12,
-       AWQ_K_ACT8 = 13, AWQ_K_COUNT = 14 };
+       AWQ_K_ACT8 = 13, AWQ_K_ROWS8 = 14, AWQ_K_NORM = 15, AWQ_K_W8A8 = 16, AWQ_K_COUNT = 17 };
 void awq_profile_enable(int on);
 void awq_profile_reset(void);
 awq_status awq_profile_read(int kind, double* total_ms, int64_t* launches);

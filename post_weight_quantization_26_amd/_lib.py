@@ -25,9 +25,10 @@ AWQ_OP_SEARCH_SCALE_SPLIT_E, AWQ_OP_SEARCH_CLIP_SPLIT_E = 9, 10
 AWQ_OP_SEARCH_SCALE_FUSED, AWQ_OP_SEARCH_CLIP_FUSED = 11, 12
 AWQ_SEARCH_SPLIT_E = 1
 AWQ_SEARCH_FUSED = 2
+AWQ_ACT_SILU, AWQ_ACT_GELU = 0, 1
 KERNEL_KINDS = {"stats": 0, "scale": 1, "transform": 2, "gemm": 3, "reduce": 4, "pack": 5,
                 "fold": 6, "dequant": 7, "w4a16": 8, "w4a16_reduce": 9, "gram_build": 10,
-                "gram_search": 11, "lora": 12, "act8": 13}
+                "gram_search": 11, "lora": 12, "act8": 13, "rows8": 14, "norm": 15, "w8a8": 16}
 
 
 class QConfig(ctypes.Structure):
@@ -105,6 +106,27 @@ SIGNATURES = {
                                                c_vp]),
     "awq_act_pack8": (ctypes.c_int, [c_vp, ctypes.c_int, c_i64, c_i64, c_vp, c_vp, c_vp]),
     "awq_act_unpack8": (ctypes.c_int, [c_vp, c_vp, ctypes.c_int, c_i64, c_i64, c_vp, c_vp]),
+    "awq_quantize_rows8": (ctypes.c_int, [c_vp, ctypes.c_int, c_i64, c_i64, c_vp, c_vp, c_vp,
+                                          c_vp]),
+    "awq_dequantize_rows8": (ctypes.c_int, [c_vp, c_vp, ctypes.c_int, c_i64, c_i64, c_vp, c_vp]),
+    "awq_layer_norm": (ctypes.c_int, [c_vp, ctypes.c_int, c_i64, c_i64, c_vp, c_vp, ctypes.c_int,
+                                      ctypes.c_float, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "awq_layer_norm_backward_workspace_bytes": (c_sz, [c_i64, c_i64]),
+    "awq_layer_norm_backward": (ctypes.c_int, [c_vp, c_vp, c_vp, ctypes.c_int, c_i64, c_i64, c_vp,
+                                               ctypes.c_int, c_i32, c_vp, c_vp, c_vp, c_vp, c_sz,
+                                               c_vp]),
+    "awq_w8a8_workspace_bytes": (c_sz, [c_i64, c_i64, c_i64, c_i32]),
+    "awq_w8a8_matmul": (ctypes.c_int, [c_vp, c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp,
+                                       ctypes.c_int, c_vp, c_vp, c_sz, c_vp]),
+    "awq_w8a8_gated_matmul": (ctypes.c_int, [c_vp, c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp,
+                                             c_vp, c_i32, ctypes.c_int, c_vp, c_vp, c_vp, c_vp,
+                                             c_sz, c_vp]),
+    "awq_w8a8_backward_workspace_bytes": (c_sz, [c_i64, c_i64, c_i64, c_i32]),
+    "awq_w8a8_backward": (ctypes.c_int, [c_vp, ctypes.c_int, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp,
+                                         c_vp, c_sz, c_vp]),
+    "awq_w8a8_gated_backward": (ctypes.c_int, [c_vp, c_vp, c_vp, ctypes.c_int, c_i64, c_i64, c_i64,
+                                               c_vp, c_vp, c_vp, c_vp, c_i32, c_vp, c_vp, c_vp,
+                                               c_vp, c_sz, c_vp]),
     "awq_last_error": (ctypes.c_char_p, []),
     "awq_profile_enable": (None, [ctypes.c_int]),
     "awq_profile_reset": (None, []),

@@ -577,6 +577,258 @@ def act_unpack8(codes: torch.Tensor, steps: torch.Tensor, dtype: torch.dtype,
     return X
 
 
+def quantize_rows8(X: torch.Tensor, s: Optional[torch.Tensor] = None, out=None):
+    """Rows of X [T, K] (bf16, float16 or float32) in 8 bits with one step per
+    row: (codes [T, K] int8, steps [T] float32), x·s ≈ code·step, step = max
+    |x·s| / 127. A token's activations for w8a8_matmul, or, with output
+    channels as rows and the scales ``s`` [K] float32 of a search, the 8-bit
+    layer of W·diag(s) (its input is divided by s, as for the packed layer)."""
+    _dev(X, "X")
+    if X.dim() != 2:
+        raise ValueError("X must be [T, K]")
+    T, K = X.shape
+    device = X.get_device()
+    if s is not None:
+        _check_on(device, ("s",), (s,))
+        if s.dtype != torch.float32 or s.shape != (K,):
+            raise ValueError("s must be float32 with one value per channel")
+    codes, steps = out if out is not None else (None, None)
+    codes = _out(codes, (T, K), torch.int8, X, "codes")
+    steps = _out(steps, (T,), torch.float32, X, "steps")
+    _call(device, L.lib().awq_quantize_rows8, X.data_ptr(), _dtype(X), T, K, _at(s),
+          codes.data_ptr(), steps.data_ptr())
+    return codes, steps
+
+
+def _rows8(codes: torch.Tensor, steps: torch.Tensor, names=("codes", "steps")):
+    """Checks 8-bit rows (codes [R, K] int8, steps [R] float32); (R, K, GPU number)."""
+    _dev(codes, names[0])
+    device = codes.get_device()
+    _check_on(device, names[1:], (steps,))
+    shape = codes.shape
+    if len(shape) != 2 or codes.dtype != torch.int8 or steps.dtype != torch.float32 or \
+            steps.shape != shape[:1]:
+        raise ValueError(f"{names[0]} must be [rows, K] int8 and {names[1]} [rows] float32")
+    return shape[0], shape[1], device
+
+
+def dequantize_rows8(codes: torch.Tensor, steps: torch.Tensor, dtype: torch.dtype,
+                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values that 8-bit rows stand for, code·step rounded once to ``dtype``."""
+    T, K, device = _rows8(codes, steps)
+    X = _out(out, (T, K), dtype, codes, "out")
+    _call(device, L.lib().awq_dequantize_rows8, codes.data_ptr(), steps.data_ptr(), _dtype(X), T,
+          K, X.data_ptr())
+    return X
+
+
+def _norm_weight(X: torch.Tensor, gamma: torch.Tensor, beta: Optional[torch.Tensor]) -> None:
+    K = X.shape[1]
+    _check_on(X.get_device(), ("gamma",), (gamma,))
+    if gamma.shape != (K,) or (gamma.dtype != X.dtype and gamma.dtype != torch.float32):
+        raise ValueError("gamma must be [K] in X's dtype or float32")
+    if beta is not None:
+        _check_on(X.get_device(), ("beta",), (beta,))
+        if beta.shape != (K,) or beta.dtype != gamma.dtype:
+            raise ValueError("beta must match gamma")
+
+
+def layer_norm(X: torch.Tensor, gamma: torch.Tensor, beta: Optional[torch.Tensor] = None,
+               eps: float = 1e-5, rms: bool = False, out: Optional[torch.Tensor] = None,
+               stats: Optional[torch.Tensor] = None, rows8=None, want_y: bool = True):
+    """The norm that precedes a layer (whose gamma and beta fold_norm divides):
+    y = (x - mean)·r·gamma + beta with r = 1 / sqrt(mean (x - mean)² + eps)
+    over each row of X [T, K]; with ``rms`` the mean is taken as 0. gamma and
+    beta [K] in X's dtype or float32. ``stats`` [T, 2] float32 receives (mean,
+    r) for layer_norm_backward, ``rows8`` = (codes [T, K] int8, steps [T]
+    float32) the 8-bit rows of y for w8a8_matmul. Returns Y in X's dtype, or
+    None with want_y False."""
+    _dev(X, "X")
+    if X.dim() != 2:
+        raise ValueError("X must be [T, K]")
+    T, K = X.shape
+    _norm_weight(X, gamma, beta)
+    Y = _out(out, (T, K), X.dtype, X, "out") if want_y else None
+    codes = steps = None
+    if stats is not None:
+        _out(stats, (T, 2), torch.float32, X, "stats")
+    if rows8 is not None:
+        codes = _out(rows8[0], (T, K), torch.int8, X, "rows8 codes")
+        steps = _out(rows8[1], (T,), torch.float32, X, "rows8 steps")
+    _call(X.get_device(), L.lib().awq_layer_norm, X.data_ptr(), _dtype(X), T, K, gamma.data_ptr(),
+          _at(beta), _dtype(gamma), float(eps), int(bool(rms)), _at(Y), _at(stats), _at(codes),
+          _at(steps))
+    return Y
+
+
+def layer_norm_backward_workspace_bytes(T: int, K: int) -> int:
+    return int(L.lib().awq_layer_norm_backward_workspace_bytes(T, K))
+
+
+def layer_norm_backward(dY: torch.Tensor, X: torch.Tensor, stats: torch.Tensor,
+                        gamma: torch.Tensor, rms: bool = False, want_beta: bool = True,
+                        ws: Optional[torch.Tensor] = None, out=None):
+    """The gradient of layer_norm: (dX [T, K] in X's dtype, dgamma [K], dbeta
+    [K] in gamma's dtype) from dY, the X and the ``stats`` of the forward call;
+    dbeta is None with want_beta False. ``out`` = (dX, dgamma, dbeta) gives
+    the buffers."""
+    _dev(dY, "dY")
+    if dY.dim() != 2:
+        raise ValueError("dY must be [T, K]")
+    T, K = dY.shape
+    device = dY.get_device()
+    _check_on(device, ("X", "stats"), (X, stats))
+    if X.shape != dY.shape or X.dtype != dY.dtype:
+        raise ValueError("X must share dY's shape and dtype")
+    if stats.shape != (T, 2) or stats.dtype != torch.float32:
+        raise ValueError("stats must be [T, 2] float32")
+    _norm_weight(X, gamma, None)
+    dX, dgamma, dbeta = out if out is not None else (None, None, None)
+    dX = _out(dX, (T, K), dY.dtype, dY, "dX")
+    dgamma = _out(dgamma, (K,), gamma.dtype, dY, "dgamma")
+    dbeta = _out(dbeta, (K,), gamma.dtype, dY, "dbeta") if want_beta else None
+    if ws is None:
+        ws = _workspace(ws, layer_norm_backward_workspace_bytes(T, K), dY.device)
+    else:
+        _check_on(device, ("ws",), (ws,))
+    _call(device, L.lib().awq_layer_norm_backward, dY.data_ptr(), X.data_ptr(), stats.data_ptr(),
+          _dtype(dY), T, K, gamma.data_ptr(), _dtype(gamma), int(bool(rms)), dX.data_ptr(),
+          dgamma.data_ptr(), _at(dbeta), ws.data_ptr(), ws.nbytes)
+    return dX, dgamma, dbeta
+
+
+_ACTS = {"silu": L.AWQ_ACT_SILU, "gelu": L.AWQ_ACT_GELU}
+
+
+def _act(act: str) -> int:
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {tuple(_ACTS)}")
+    return _ACTS[act]
+
+
+def w8a8_workspace_bytes(T: int, N: int, K: int, layers: int = 1) -> int:
+    """Workspace of w8a8_matmul (layers 1) or w8a8_gated_matmul (2)."""
+    return int(L.lib().awq_w8a8_workspace_bytes(T, N, K, layers))
+
+
+def w8a8_backward_workspace_bytes(T: int, N: int, K: int, layers: int = 1) -> int:
+    """Workspace of w8a8_backward (layers 1) or w8a8_gated_backward (2)."""
+    return int(L.lib().awq_w8a8_backward_workspace_bytes(T, N, K, layers))
+
+
+def _w8_ws(ws: Optional[torch.Tensor], need: int, like: torch.Tensor):
+    """(address, bytes) of the caller's workspace or of a new one, kept alive by the third."""
+    if ws is not None:
+        _check_on(like.get_device(), ("ws",), (ws,))
+    elif need:
+        ws = torch.empty(need, dtype=torch.uint8, device=like.device)
+    return (None, 0, None) if ws is None else (ws.data_ptr(), ws.nbytes, ws)
+
+
+def _pair(gate, up, K: Optional[int], device: int):
+    """Checks a gated pair's layers; (N, K)."""
+    N, Kg, on = _rows8(*gate, ("gate codes", "gate steps"))
+    Nu, Ku, on_u = _rows8(*up, ("up codes", "up steps"))
+    if on != device or on_u != device:
+        raise ValueError(f"the layers are not on GPU {device}")
+    if Nu != N or Ku != Kg or (K is not None and K != Kg):
+        raise ValueError("gate and up must be [N, K] with the input's K")
+    return N, Kg
+
+
+def w8a8_matmul(codes: torch.Tensor, steps: torch.Tensor, qweight: torch.Tensor,
+                wsteps: torch.Tensor, dtype: torch.dtype, bias: Optional[torch.Tensor] = None,
+                ws: Optional[torch.Tensor] = None,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y[t][n] = steps[t]·wsteps[n]·Σ_k codes[t][k]·qweight[n][k] + bias[n] for
+    8-bit rows (quantize_rows8 or layer_norm's rows8) and an 8-bit layer
+    (quantize_rows8 of W [N, K]). The sum is exact; Y [T, N] is rounded once to
+    ``dtype`` (bf16 or float16), which bias [N] shares."""
+    T, K, device = _rows8(codes, steps)
+    N, Kw, on = _rows8(qweight, wsteps, ("qweight", "wsteps"))
+    if on != device:
+        raise ValueError(f"qweight is not on GPU {device}")
+    if Kw != K:
+        raise ValueError("qweight must be [N, K] with the rows' K")
+    if bias is not None:
+        _check_on(device, ("bias",), (bias,))
+        if bias.shape != (N,) or bias.dtype != dtype:
+            raise ValueError("bias must be [N] in dtype")
+    Y = _out(out, (T, N), dtype, codes, "out")
+    at, nbytes, _keep = _w8_ws(ws, w8a8_workspace_bytes(T, N, K), codes)
+    _call(device, L.lib().awq_w8a8_matmul, codes.data_ptr(), steps.data_ptr(), T, N, K,
+          qweight.data_ptr(), wsteps.data_ptr(), _at(bias), _dtype(Y), Y.data_ptr(), at, nbytes)
+    return Y
+
+
+def w8a8_gated_matmul(codes: torch.Tensor, steps: torch.Tensor, gate, up, dtype: torch.dtype,
+                      act: str = "silu", ws: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None, pre=None) -> torch.Tensor:
+    """H = act(G)·U of two 8-bit layers of one input, ``gate`` and ``up`` =
+    (codes [N, K] int8, steps [N] float32), G and U their products as in
+    w8a8_matmul, held in float32 until H is rounded once. act "silu" or "gelu"
+    (g·Φ(g)). ``pre`` = (G, U) [T, N] buffers in ``dtype`` receive the
+    products, for w8a8_gated_backward."""
+    T, K, device = _rows8(codes, steps)
+    N, _ = _pair(gate, up, K, device)
+    kind = _act(act)
+    H = _out(out, (T, N), dtype, codes, "out")
+    G = U = None
+    if pre is not None:
+        G = _out(pre[0], (T, N), dtype, codes, "pre G")
+        U = _out(pre[1], (T, N), dtype, codes, "pre U")
+    at, nbytes, _keep = _w8_ws(ws, w8a8_workspace_bytes(T, N, K, 2), codes)
+    _call(device, L.lib().awq_w8a8_gated_matmul, codes.data_ptr(), steps.data_ptr(), T, N, K,
+          gate[0].data_ptr(), gate[1].data_ptr(), up[0].data_ptr(), up[1].data_ptr(), kind,
+          _dtype(H), H.data_ptr(), _at(G), _at(U), at, nbytes)
+    return H
+
+
+def w8a8_backward(dY: torch.Tensor, qweight: torch.Tensor, wsteps: torch.Tensor,
+                  ws: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient of w8a8_matmul with respect to the values that its 8-bit
+    rows stand for: dX [T, K] in dY's dtype from dY [T, N]."""
+    N, K, device = _rows8(qweight, wsteps, ("qweight", "wsteps"))
+    _check_on(device, ("dY",), (dY,))
+    if dY.dim() != 2 or dY.shape[1] != N:
+        raise ValueError("dY must be [T, N]")
+    T = dY.shape[0]
+    dX = _out(out, (T, K), dY.dtype, dY, "out")
+    at, nbytes, _keep = _w8_ws(ws, w8a8_backward_workspace_bytes(T, N, K), dY)
+    _call(device, L.lib().awq_w8a8_backward, dY.data_ptr(), _dtype(dY), T, N, K,
+          qweight.data_ptr(), wsteps.data_ptr(), dX.data_ptr(), at, nbytes)
+    return dX
+
+
+def w8a8_gated_backward(dH: torch.Tensor, pre, gate, up, act: str = "silu",
+                        ws: Optional[torch.Tensor] = None, out=None):
+    """The gradient of w8a8_gated_matmul: (dX [T, K], dG, dU [T, N]) in dH's
+    dtype from dH [T, N] and the ``pre`` = (G, U) that the forward call kept; dX
+    with respect to the values that the 8-bit rows stand for, dG and dU those
+    of the two products. ``out`` = (dX, dG, dU) gives the buffers."""
+    _dev(dH, "dH")
+    device = dH.get_device()
+    N, K = _pair(gate, up, None, device)
+    if dH.dim() != 2 or dH.shape[1] != N:
+        raise ValueError("dH must be [T, N]")
+    T = dH.shape[0]
+    G, U = pre
+    _check_on(device, ("pre G", "pre U"), (G, U))
+    if G.shape != dH.shape or U.shape != dH.shape or G.dtype != dH.dtype or U.dtype != dH.dtype:
+        raise ValueError("pre must be (G, U), each [T, N] in dH's dtype")
+    kind = _act(act)
+    dX, dG, dU = out if out is not None else (None, None, None)
+    dX = _out(dX, (T, K), dH.dtype, dH, "dX")
+    dG = _out(dG, (T, N), dH.dtype, dH, "dG")
+    dU = _out(dU, (T, N), dH.dtype, dH, "dU")
+    at, nbytes, _keep = _w8_ws(ws, w8a8_backward_workspace_bytes(T, N, K, 2), dH)
+    _call(device, L.lib().awq_w8a8_gated_backward, dH.data_ptr(), G.data_ptr(), U.data_ptr(),
+          _dtype(dH), T, N, K, gate[0].data_ptr(), gate[1].data_ptr(), up[0].data_ptr(),
+          up[1].data_ptr(), kind, dX.data_ptr(), dG.data_ptr(), dU.data_ptr(), at, nbytes)
+    return dX, dG, dU
+
+
 def profile_enable(on: bool = True) -> None:
     L.lib().awq_profile_enable(1 if on else 0)
 

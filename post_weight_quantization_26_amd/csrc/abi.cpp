@@ -9,6 +9,7 @@
 
 #include "awq_internal.h"
 #include "lora.h"
+#include "w8.h"
 
 namespace awq {
 // Launchers (HIP translation units).
@@ -972,6 +973,196 @@ extern "C" awq_status awq_act_unpack8(const int8_t* codes, const float* steps, a
                 [&] { return launch_act_unpack8(codes, steps, dt(dtype), T, K, X, st); }),
           "act_unpack8");
   return AWQ_OK;
+}
+
+extern "C" awq_status awq_quantize_rows8(const void* X, awq_dtype dtype, int64_t T, int64_t K,
+                                         const float* s, int8_t* codes, float* steps,
+                                         void* stream) {
+  awq_status st_ = check_rows8("quantize_rows8", X, dtype, T, K, s, codes, steps);
+  if (st_ != AWQ_OK) return st_;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const QuantizeRows8 p{X, s, T, K, codes, steps, rows_vec(K, {X, s, codes})};
+  AWQ_HIP(timed(AWQ_K_ROWS8, st, [&] { return launch_quantize_rows8(p, dt(dtype), st); }),
+          "quantize_rows8");
+  return AWQ_OK;
+}
+
+extern "C" awq_status awq_dequantize_rows8(const int8_t* codes, const float* steps,
+                                           awq_dtype dtype, int64_t T, int64_t K, void* X,
+                                           void* stream) {
+  awq_status st_ = check_rows8("dequantize_rows8", X, dtype, T, K, nullptr, codes, steps);
+  if (st_ != AWQ_OK) return st_;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const bool vec = rows_vec(K, {X, codes});
+  AWQ_HIP(timed(AWQ_K_ROWS8, st,
+                [&] {
+                  return launch_dequantize_rows8(codes, steps, dt(dtype), T, K, vec, X, st);
+                }),
+          "dequantize_rows8");
+  return AWQ_OK;
+}
+
+extern "C" awq_status awq_layer_norm(const void* X, awq_dtype dtype, int64_t T, int64_t K,
+                                     const void* gamma, const void* beta, awq_dtype weight_dtype,
+                                     float eps, int32_t rms, void* Y, float* stats, int8_t* codes,
+                                     float* steps, void* stream) {
+  awq_status st_ = check_norm(X, dtype, T, K, gamma, beta, weight_dtype, eps, Y, stats, codes,
+                              steps);
+  if (st_ != AWQ_OK) return st_;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  Norm p{};
+  p.X = X;
+  p.gamma = gamma;
+  p.beta = beta;
+  p.gamma32 = weight_dtype == AWQ_F32;
+  p.rms = rms != 0;
+  p.vec = rows_vec(K, {X, gamma, beta, Y, codes});
+  p.eps = eps;
+  p.T = T;
+  p.K = K;
+  p.Y = Y;
+  p.stats = stats;
+  p.codes = codes;
+  p.steps = steps;
+  AWQ_HIP(timed(AWQ_K_NORM, st, [&] { return launch_norm(p, dt(dtype), st); }), "layer_norm");
+  return AWQ_OK;
+}
+
+extern "C" awq_status awq_layer_norm_backward(const void* dY, const void* X, const float* stats,
+                                              awq_dtype dtype, int64_t T, int64_t K,
+                                              const void* gamma, awq_dtype weight_dtype,
+                                              int32_t rms, void* dX, void* dgamma, void* dbeta,
+                                              void* ws, size_t ws_bytes, void* stream) {
+  awq_status st_ = check_norm_back(dY, X, stats, dtype, T, K, gamma, weight_dtype, dX, dgamma,
+                                   dbeta, ws, ws_bytes);
+  if (st_ != AWQ_OK) return st_;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const NormBackLayout l = norm_back_layout(T, K);
+  NormBack p{};
+  p.dY = dY;
+  p.X = X;
+  p.stats = stats;
+  p.gamma = gamma;
+  p.gamma32 = weight_dtype == AWQ_F32;
+  p.rms = rms != 0;
+  p.vec = rows_vec(K, {dY, X, gamma, dX});
+  p.T = T;
+  p.K = K;
+  p.Kp = l.Kp;
+  p.groups = l.groups;
+  p.partial = static_cast<float*>(ws);
+  p.dX = dX;
+  p.dgamma = dgamma;
+  p.dbeta = dbeta;
+  AWQ_HIP(timed(AWQ_K_NORM, st, [&] { return launch_norm_back(p, dt(dtype), st); }),
+          "layer_norm_backward");
+  return AWQ_OK;
+}
+
+static awq_status w8_product(const char* name, const W8Product& p, void* stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  AWQ_HIP(timed(AWQ_K_W8A8, st, [&] { return launch_w8_few(p, st); }), name);
+  return AWQ_OK;
+}
+
+extern "C" awq_status awq_w8a8_matmul(const int8_t* codes, const float* steps, int64_t T,
+                                      int64_t N, int64_t K, const int8_t* qweight,
+                                      const float* wsteps, const void* bias, awq_dtype dtype,
+                                      void* Y, void* ws, size_t ws_bytes, void* stream) {
+  awq_status st_ = check_w8("w8a8_matmul", codes, steps, T, N, K, 1, qweight, wsteps, nullptr,
+                            nullptr, bias, AWQ_ACT_SILU, dtype, Y, nullptr, nullptr, ws, ws_bytes);
+  if (st_ != AWQ_OK) return st_;
+  W8Product p{};
+  p.x = codes;
+  p.xs = steps;
+  p.w = {qweight, wsteps};
+  p.bias = static_cast<const uint16_t*>(bias);
+  p.T = T;
+  p.N = N;
+  p.K = K;
+  p.f16 = dtype == AWQ_F16;
+  p.Y = static_cast<uint16_t*>(Y);
+  return w8_product("w8a8_matmul", p, stream);
+}
+
+extern "C" awq_status awq_w8a8_gated_matmul(const int8_t* codes, const float* steps, int64_t T,
+                                            int64_t N, int64_t K, const int8_t* gate,
+                                            const float* gsteps, const int8_t* up,
+                                            const float* usteps, int32_t act, awq_dtype dtype,
+                                            void* H, void* G, void* U, void* ws, size_t ws_bytes,
+                                            void* stream) {
+  awq_status st_ = check_w8("w8a8_gated_matmul", codes, steps, T, N, K, 2, gate, gsteps, up,
+                            usteps, nullptr, act, dtype, H, G, U, ws, ws_bytes);
+  if (st_ != AWQ_OK) return st_;
+  W8Product p{};
+  p.x = codes;
+  p.xs = steps;
+  p.w = {gate, gsteps};
+  p.u = {up, usteps};
+  p.T = T;
+  p.N = N;
+  p.K = K;
+  p.act = act;
+  p.f16 = dtype == AWQ_F16;
+  p.Y = static_cast<uint16_t*>(H);
+  p.G = static_cast<uint16_t*>(G);
+  p.U = static_cast<uint16_t*>(U);
+  return w8_product("w8a8_gated_matmul", p, stream);
+}
+
+static awq_status w8_back(const char* name, W8Back p, int32_t layers, void* ws, void* stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const W8BackLayout l = w8_back_layout(p.T, p.N, p.K, layers);
+  p.Np = l.Np;
+  p.A = at<uint16_t>(ws, l.a);
+  p.B = at<uint16_t>(ws, l.b);
+  p.E = at<float>(ws, l.e);
+  AWQ_HIP(timed(AWQ_K_W8A8, st, [&] { return launch_w8_back(p, st); }), name);
+  return AWQ_OK;
+}
+
+extern "C" awq_status awq_w8a8_backward(const void* dY, awq_dtype dtype, int64_t T, int64_t N,
+                                        int64_t K, const int8_t* qweight, const float* wsteps,
+                                        void* dX, void* ws, size_t ws_bytes, void* stream) {
+  awq_status st_ = check_w8_back("w8a8_backward", dY, nullptr, nullptr, dtype, T, N, K, 1,
+                                 qweight, wsteps, nullptr, nullptr, AWQ_ACT_SILU, dX, nullptr,
+                                 nullptr, ws, ws_bytes);
+  if (st_ != AWQ_OK) return st_;
+  W8Back p{};
+  p.dY = static_cast<const uint16_t*>(dY);
+  p.w = {qweight, wsteps};
+  p.T = T;
+  p.N = N;
+  p.K = K;
+  p.f16 = dtype == AWQ_F16;
+  p.dX = static_cast<uint16_t*>(dX);
+  return w8_back("w8a8_backward", p, 1, ws, stream);
+}
+
+extern "C" awq_status awq_w8a8_gated_backward(const void* dH, const void* G, const void* U,
+                                              awq_dtype dtype, int64_t T, int64_t N, int64_t K,
+                                              const int8_t* gate, const float* gsteps,
+                                              const int8_t* up, const float* usteps, int32_t act,
+                                              void* dX, void* dG, void* dU, void* ws,
+                                              size_t ws_bytes, void* stream) {
+  awq_status st_ = check_w8_back("w8a8_gated_backward", dH, G, U, dtype, T, N, K, 2, gate, gsteps,
+                                 up, usteps, act, dX, dG, dU, ws, ws_bytes);
+  if (st_ != AWQ_OK) return st_;
+  W8Back p{};
+  p.dY = static_cast<const uint16_t*>(dH);
+  p.G = static_cast<const uint16_t*>(G);
+  p.U = static_cast<const uint16_t*>(U);
+  p.w = {gate, gsteps};
+  p.u = {up, usteps};
+  p.T = T;
+  p.N = N;
+  p.K = K;
+  p.act = act;
+  p.f16 = dtype == AWQ_F16;
+  p.dX = static_cast<uint16_t*>(dX);
+  p.dG = static_cast<uint16_t*>(dG);
+  p.dU = static_cast<uint16_t*>(dU);
+  return w8_back("w8a8_gated_backward", p, 2, ws, stream);
 }
 
 extern "C" void awq_profile_enable(int on) {

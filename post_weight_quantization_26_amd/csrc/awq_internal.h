@@ -5,6 +5,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <initializer_list>
 
 #include "awq.h"
 
@@ -276,6 +277,46 @@ awq_status check_lora_backward(const void* dY, const void* X, const float* x8_st
                                const void* dB, const void* ws, size_t ws_bytes);
 awq_status check_act8(const char* name, const void* X, awq_dtype d, int64_t T, int64_t K,
                       const void* codes, const float* steps);
+
+// 8-bit rows, norms and products.
+constexpr int64_t kRows8MaxK = 65536;
+constexpr int64_t kNormMaxK = 16384;
+constexpr int64_t kW8MaxK = (int64_t(1) << 17) - 1;   // 128·128·K fits an int32
+constexpr int64_t kW8BackMaxN = int64_t(1) << 21;
+// The gradient's row groups, each with a row of partial sums of Kp columns.
+struct NormBackLayout {
+  int64_t groups, Kp;
+  size_t total;
+};
+NormBackLayout norm_back_layout(int64_t T, int64_t K);
+size_t w8_workspace(int64_t T, int64_t N, int64_t K, int32_t layers);
+struct W8BackLayout {
+  int64_t Np, C;       // N rounded up to 64; the contraction's length
+  size_t a, b, e;      // 16-bit [T, C] and [K, C], f32 [T]
+  size_t total;
+};
+W8BackLayout w8_back_layout(int64_t T, int64_t N, int64_t K, int32_t layers);
+// Whether a row kernel may take 8 elements at a time.
+bool rows_vec(int64_t K, std::initializer_list<const void*> pointers);
+awq_status check_rows8(const char* name, const void* X, awq_dtype d, int64_t T, int64_t K,
+                       const float* s, const void* codes, const float* steps);
+awq_status check_norm(const void* X, awq_dtype d, int64_t T, int64_t K, const void* gamma,
+                      const void* beta, awq_dtype wd, float eps, const void* Y,
+                      const float* stats, const void* codes, const float* steps);
+awq_status check_norm_back(const void* dY, const void* X, const float* stats, awq_dtype d,
+                           int64_t T, int64_t K, const void* gamma, awq_dtype wd, const void* dX,
+                           const void* dgamma, const void* dbeta, const void* ws,
+                           size_t ws_bytes);
+// layers 1 or 2; q1 and s1 are a pair's second layer.
+awq_status check_w8(const char* name, const void* codes, const float* steps, int64_t T, int64_t N,
+                    int64_t K, int32_t layers, const void* q0, const float* s0, const void* q1,
+                    const float* s1, const void* bias, int32_t act, awq_dtype d, const void* Y,
+                    const void* G, const void* U, const void* ws, size_t ws_bytes);
+awq_status check_w8_back(const char* name, const void* dY, const void* G, const void* U,
+                         awq_dtype d, int64_t T, int64_t N, int64_t K, int32_t layers,
+                         const void* q0, const float* s0, const void* q1, const float* s1,
+                         int32_t act, const void* dX, const void* dG, const void* dU,
+                         const void* ws, size_t ws_bytes);
 
 awq_status set_error(awq_status st, const char* fmt, ...);
 

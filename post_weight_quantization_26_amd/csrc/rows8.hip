@@ -1,0 +1,123 @@
+// Rows in 8 bits with one step each, the operands of the 8-bit products: a
+// token's activations, or an output channel's weights times the scales s.
+//
+//   x' = fl32(x·s_k);  m = max(max |x'|, 2^-100);  step = fl32(m / 127)
+//   code = rint(fl32(x'·fl32(127 / m)));  x^ = fl32(code·step)
+//
+// the arithmetic of an 8-bit checkpoint (act8.h) over a whole row: codes in
+// -127..127, a row that holds a NaN or an infinity gets the step NaN.
+#include "row_block.h"
+#include "w8.h"
+
+namespace awq {
+namespace {
+
+// Bound by HBM. A row stays in registers between its maximum and its codes, so
+// X is read once; s comes from the caches.
+template <int DT, int W, int V, bool VEC>
+__global__ __launch_bounds__(kRowThreads<W>) void quantize_rows8_kernel(
+    const void* __restrict__ X, const float* __restrict__ s, int64_t T, int K,
+    int8_t* __restrict__ codes, float* __restrict__ steps) {
+  __shared__ uint32_t red[16];
+  const int64_t row = row_of<W>(blockIdx.x);
+  if (row >= T) return;   // W = 1: no barrier follows; otherwise row < T
+  const int t = row_thread<W>();
+  float x[V][8];
+#pragma unroll
+  for (int c = 0; c < V; ++c) load_piece<DT, W, VEC>(X, row * K, K, c, t, x[c]);
+  if (s) {
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      float f[8];
+      load_piece<0, W, VEC>(s, 0, K, c, t, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[c][e] *= f[e];
+    }
+  }
+  quantize_row<W, V, VEC>(x, row, K, t, red, codes, steps);
+}
+
+// x^ = code·step, 8 codes a thread; a piece lies within one row (VEC) or is
+// taken element by element.
+template <int DT, bool VEC>
+__global__ __launch_bounds__(256) void dequantize_rows8_kernel(const int8_t* __restrict__ codes,
+                                                               const float* __restrict__ steps,
+                                                               int64_t n, uint32_t K,
+                                                               void* __restrict__ X) {
+  const int64_t p = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if constexpr (VEC) {
+    if (p * 8 >= n) return;
+    const uint2 c = *reinterpret_cast<const uint2*>(codes + p * 8);
+    const float s = steps[uint32_t(p) / (K / 8)];   // p < 2^31
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = float(int8_t(c.x >> (8 * e))) * s;
+      v[4 + e] = float(int8_t(c.y >> (8 * e))) * s;
+    }
+    store8<DT>(X, p * 8, v);
+  } else {
+    // elements 256 apart, so that a wave's are consecutive
+    const int64_t i0 = int64_t(blockIdx.x) * 2048 + threadIdx.x;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int64_t i = i0 + 256 * e;
+      if (i < n) store1<DT>(X, i, float(codes[i]) * steps[i / int64_t(K)]);
+    }
+  }
+}
+
+template <int DT, int W, int V>
+hipError_t launch_quantize(const QuantizeRows8& p, hipStream_t st) {
+  const unsigned grid = unsigned(W == 1 ? (p.T + 3) / 4 : p.T);
+  if (p.vec)
+    quantize_rows8_kernel<DT, W, V, true><<<grid, kRowThreads<W>, 0, st>>>(p.X, p.s, p.T, int(p.K),
+                                                                           p.codes, p.steps);
+  else
+    quantize_rows8_kernel<DT, W, V, false><<<grid, kRowThreads<W>, 0, st>>>(
+        p.X, p.s, p.T, int(p.K), p.codes, p.steps);
+  return hipGetLastError();
+}
+
+// K up to 512·W·V
+template <int DT>
+hipError_t launch_quantize_t(const QuantizeRows8& p, hipStream_t st) {
+  if (p.K <= 512) return launch_quantize<DT, 1, 1>(p, st);
+  if (p.K <= 1024) return launch_quantize<DT, 1, 2>(p, st);
+  if (p.K <= 2048) return launch_quantize<DT, 4, 1>(p, st);
+  if (p.K <= 4096) return launch_quantize<DT, 4, 2>(p, st);
+  if (p.K <= 8192) return launch_quantize<DT, 4, 4>(p, st);
+  if (p.K <= 16384) return launch_quantize<DT, 8, 4>(p, st);
+  if (p.K <= 32768) return launch_quantize<DT, 16, 4>(p, st);
+  if (p.K <= 65536) return launch_quantize<DT, 16, 8>(p, st);
+  return hipErrorInvalidValue;
+}
+
+template <int DT>
+hipError_t launch_dequantize_t(const int8_t* codes, const float* steps, int64_t T, int64_t K,
+                               bool vec, void* X, hipStream_t st) {
+  const int64_t n = T * K;
+  const unsigned grid = unsigned((n + 2047) / 2048);
+  if (vec)
+    dequantize_rows8_kernel<DT, true><<<grid, 256, 0, st>>>(codes, steps, n, uint32_t(K), X);
+  else
+    dequantize_rows8_kernel<DT, false><<<grid, 256, 0, st>>>(codes, steps, n, uint32_t(K), X);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quantize_rows8(const QuantizeRows8& p, int dtype, hipStream_t st) {
+  if (dtype == 0) return launch_quantize_t<0>(p, st);
+  if (dtype == 1) return launch_quantize_t<1>(p, st);
+  return launch_quantize_t<2>(p, st);
+}
+
+hipError_t launch_dequantize_rows8(const int8_t* codes, const float* steps, int dtype, int64_t T,
+                                   int64_t K, bool vec, void* X, hipStream_t st) {
+  if (dtype == 0) return launch_dequantize_t<0>(codes, steps, T, K, vec, X, st);
+  if (dtype == 1) return launch_dequantize_t<1>(codes, steps, T, K, vec, X, st);
+  return launch_dequantize_t<2>(codes, steps, T, K, vec, X, st);
+}
+
+}  // namespace awq

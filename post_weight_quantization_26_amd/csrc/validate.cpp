@@ -757,7 +757,218 @@ awq_status check_act8(const char* name, const void* X, awq_dtype d, int64_t T, i
   return AWQ_OK;
 }
 
+// ---------------------------------------------------------------------------
+// 8-bit rows, norms and products
+// ---------------------------------------------------------------------------
+
+bool rows_vec(int64_t K, std::initializer_list<const void*> pointers) {
+  return K % 8 == 0 && std::all_of(pointers.begin(), pointers.end(), aligned16);
+}
+
+// The row kernels take a workgroup of up to 1024 threads per row.
+static awq_status check_rows(const char* name, awq_dtype d, int64_t T, int64_t K, int64_t most) {
+  if (!dtype_ok(d)) return set_error(AWQ_E_INVALID, "%s: unknown dtype %d", name, int(d));
+  if (T < 1 || K < 1 || T > kMaxDim || K > kMaxDim)
+    return set_error(AWQ_E_INVALID, "%s: bad shape T=%lld K=%lld", name, (long long)T,
+                     (long long)K);
+  if (K > most)
+    return set_error(AWQ_E_UNSUPPORTED, "%s: K=%lld (at most %lld)", name, (long long)K,
+                     (long long)most);
+  if (T * K > kMaxMatrixElems)
+    return set_error(AWQ_E_UNSUPPORTED, "%s: T*K=%lld exceeds 2^34", name, (long long)(T * K));
+  const int64_t threads = K <= 1024 ? 64 : K <= 8192 ? 256 : K <= 16384 ? 512 : 1024;
+  if (!grid_fits(T + 3, threads))
+    return set_error(AWQ_E_UNSUPPORTED, "%s: T=%lld exceeds the grid", name, (long long)T);
+  return AWQ_OK;
+}
+
+awq_status check_rows8(const char* name, const void* X, awq_dtype d, int64_t T, int64_t K,
+                       const float* s, const void* codes, const float* steps) {
+  if (!X || !codes || !steps) return set_error(AWQ_E_INVALID, "%s: NULL pointer argument", name);
+  const awq_status st = check_rows(name, d, T, K, kRows8MaxK);
+  if (st != AWQ_OK) return st;
+  if (!aligned_elem(X, d) || !aligned4(s) || !aligned4(steps))
+    return set_error(AWQ_E_INVALID, "%s: X, s and steps must be aligned to their elements", name);
+  return AWQ_OK;
+}
+
+static awq_status check_norm_weight(const char* name, awq_dtype d, awq_dtype wd) {
+  if (!dtype_ok(wd)) return set_error(AWQ_E_INVALID, "%s: unknown weight dtype %d", name, int(wd));
+  if (wd != d && wd != AWQ_F32)
+    return set_error(AWQ_E_UNSUPPORTED, "%s: gamma and beta must be of X's type or float32", name);
+  return AWQ_OK;
+}
+
+awq_status check_norm(const void* X, awq_dtype d, int64_t T, int64_t K, const void* gamma,
+                      const void* beta, awq_dtype wd, float eps, const void* Y,
+                      const float* stats, const void* codes, const float* steps) {
+  const char* name = "layer_norm";
+  if (!X || !gamma) return set_error(AWQ_E_INVALID, "%s: NULL pointer argument", name);
+  if (!codes != !steps)
+    return set_error(AWQ_E_INVALID, "%s: 8-bit rows need both codes and steps", name);
+  if (!Y && !stats && !codes) return set_error(AWQ_E_INVALID, "%s: no output asked for", name);
+  awq_status st = check_rows(name, d, T, K, kNormMaxK);
+  if (st != AWQ_OK) return st;
+  st = check_norm_weight(name, d, wd);
+  if (st != AWQ_OK) return st;
+  if (!(eps >= 0.f) || eps > 3.4e38f)
+    return set_error(AWQ_E_INVALID, "%s: eps must be finite and not negative", name);
+  if (!aligned_elem(X, d) || !aligned_elem(Y, d) || !aligned_elem(gamma, wd) ||
+      !aligned_elem(beta, wd) || !aligned8(stats) || !aligned4(steps))
+    return set_error(AWQ_E_INVALID,
+                     "%s: X, Y, gamma, beta and steps must be aligned to their elements, stats to "
+                     "8 bytes", name);
+  return AWQ_OK;
+}
+
+// Row groups of the gradient: 16 waves a CU (W of them on a row, as the
+// kernel's launcher picks), and no more than rows.
+NormBackLayout norm_back_layout(int64_t T, int64_t K) {
+  NormBackLayout l{};
+  const int64_t waves = K <= 1024 ? 1 : K <= 4096 ? 4 : K <= 8192 ? 8 : 16;
+  l.groups = std::min<int64_t>(T, 4096 / waves);
+  l.Kp = ceil_div(K, 8) * 8;
+  l.total = align_up(size_t(2 * l.groups) * size_t(l.Kp) * 4);
+  return l;
+}
+
+awq_status check_norm_back(const void* dY, const void* X, const float* stats, awq_dtype d,
+                           int64_t T, int64_t K, const void* gamma, awq_dtype wd, const void* dX,
+                           const void* dgamma, const void* dbeta, const void* ws,
+                           size_t ws_bytes) {
+  const char* name = "layer_norm_backward";
+  if (!dY || !X || !stats || !gamma || !dX || !dgamma)
+    return set_error(AWQ_E_INVALID, "%s: NULL pointer argument", name);
+  awq_status st = check_rows(name, d, T, K, kNormMaxK);
+  if (st != AWQ_OK) return st;
+  st = check_norm_weight(name, d, wd);
+  if (st != AWQ_OK) return st;
+  if (!aligned_elem(dY, d) || !aligned_elem(X, d) || !aligned_elem(dX, d) ||
+      !aligned_elem(gamma, wd) || !aligned_elem(dgamma, wd) || !aligned_elem(dbeta, wd) ||
+      !aligned8(stats))
+    return set_error(AWQ_E_INVALID,
+                     "%s: the matrices, gamma and its gradients must be aligned to their "
+                     "elements, stats to 8 bytes", name);
+  const size_t need = norm_back_layout(T, K).total;
+  if (!ws || !aligned16(ws) || ws_bytes < need)
+    return set_error(AWQ_E_WORKSPACE, "%s: workspace needs %zu bytes (16-byte aligned)", name,
+                     need);
+  return AWQ_OK;
+}
+
+static bool w8_sizes_ok(int64_t T, int64_t N, int64_t K, int32_t layers) {
+  return T >= 1 && N >= 1 && K >= 1 && T <= kMaxDim && N <= kMaxDim && K <= kW8MaxK &&
+         K % kTileK == 0 && (layers == 1 || layers == 2);
+}
+
+size_t w8_workspace(int64_t, int64_t, int64_t, int32_t) { return 0; }
+
+W8BackLayout w8_back_layout(int64_t T, int64_t N, int64_t K, int32_t layers) {
+  W8BackLayout l{};
+  l.Np = ceil_div(N, 64) * 64;
+  l.C = layers * l.Np;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += align_up(bytes);
+    return at;
+  };
+  l.a = take(size_t(T) * size_t(l.C) * 2);
+  l.b = take(size_t(K) * size_t(l.C) * 2);
+  l.e = take(size_t(T) * 4);
+  l.total = off;
+  return l;
+}
+
+// What the products and their gradients share: the layers and the sizes. V is
+// the left operand.
+static awq_status check_w8_common(const char* name, const void* V, awq_dtype d, int64_t T,
+                                  int64_t N, int64_t K, int32_t layers, const void* q0,
+                                  const float* s0, const void* q1, const float* s1, int32_t act) {
+  if (!V || !q0 || !s0 || (layers == 2 && (!q1 || !s1)))
+    return set_error(AWQ_E_INVALID, "%s: NULL pointer argument", name);
+  if (!dtype_ok(d)) return set_error(AWQ_E_INVALID, "%s: unknown dtype %d", name, int(d));
+  if (d == AWQ_F32) return set_error(AWQ_E_UNSUPPORTED, "%s: dtype must be bf16 or fp16", name);
+  if (T < 1 || N < 1 || K < 1 || T > kMaxDim || N > kMaxDim || K > kMaxDim)
+    return set_error(AWQ_E_INVALID, "%s: bad shape T=%lld N=%lld K=%lld", name, (long long)T,
+                     (long long)N, (long long)K);
+  if (K % kTileK)
+    return set_error(AWQ_E_INVALID, "%s: K=%lld not a multiple of 128", name, (long long)K);
+  if (K > kW8MaxK || N * K > kMaxMatrixElems)
+    return set_error(AWQ_E_UNSUPPORTED,
+                     "%s: N=%lld x K=%lld (K below 131072, N*K at most 2^34)", name, (long long)N,
+                     (long long)K);
+  if (layers == 2 && act != AWQ_ACT_SILU && act != AWQ_ACT_GELU)
+    return set_error(AWQ_E_INVALID, "%s: unknown activation %d", name, int(act));
+  if (!grid_fits(search_gemm_blocks(T, std::max(2 * N, K), AWQ_BF16), 256) ||
+      !grid_fits(T, 256) || !grid_fits(ceil_div(T, 16) * ceil_div(N, 16), 1024) ||
+      ceil_div(T, 16) > 65535)
+    return set_error(AWQ_E_UNSUPPORTED, "%s: T=%lld x N=%lld exceed the grids", name,
+                     (long long)T, (long long)N);
+  if (!aligned16(V) || !aligned16(q0) || !aligned16(q1) || !aligned4(s0) || !aligned4(s1))
+    return set_error(AWQ_E_INVALID,
+                     "%s: the codes and the left operand must be 16-byte aligned, steps 4", name);
+  return AWQ_OK;
+}
+
+awq_status check_w8(const char* name, const void* codes, const float* steps, int64_t T, int64_t N,
+                    int64_t K, int32_t layers, const void* q0, const float* s0, const void* q1,
+                    const float* s1, const void* bias, int32_t act, awq_dtype d, const void* Y,
+                    const void* G, const void* U, const void* ws, size_t ws_bytes) {
+  if (!steps || !Y) return set_error(AWQ_E_INVALID, "%s: NULL pointer argument", name);
+  const awq_status st = check_w8_common(name, codes, d, T, N, K, layers, q0, s0, q1, s1, act);
+  if (st != AWQ_OK) return st;
+  if (!G != !U) return set_error(AWQ_E_INVALID, "%s: G and U are kept together", name);
+  if (!aligned4(steps) || !aligned16(Y) || !aligned16(G) || !aligned16(U) ||
+      !aligned_elem(bias, d))
+    return set_error(AWQ_E_INVALID,
+                     "%s: the outputs must be 16-byte aligned, steps 4, bias 2", name);
+  const size_t need = w8_workspace(T, N, K, layers);
+  if (need && (!ws || !aligned16(ws) || ws_bytes < need))
+    return set_error(AWQ_E_WORKSPACE, "%s: workspace needs %zu bytes (16-byte aligned)", name,
+                     need);
+  return AWQ_OK;
+}
+
+awq_status check_w8_back(const char* name, const void* dY, const void* G, const void* U,
+                         awq_dtype d, int64_t T, int64_t N, int64_t K, int32_t layers,
+                         const void* q0, const float* s0, const void* q1, const float* s1,
+                         int32_t act, const void* dX, const void* dG, const void* dU,
+                         const void* ws, size_t ws_bytes) {
+  if (!dX || (layers == 2 && (!G || !U || !dG || !dU)))
+    return set_error(AWQ_E_INVALID, "%s: NULL pointer argument", name);
+  const awq_status st = check_w8_common(name, dY, d, T, N, K, layers, q0, s0, q1, s1, act);
+  if (st != AWQ_OK) return st;
+  if (N >= kW8BackMaxN || N > kMaxMatrixElems / K / layers)
+    return set_error(AWQ_E_UNSUPPORTED, "%s: N=%lld exceeds the 32-bit offsets (below 2^21)",
+                     name, (long long)N);
+  if (!aligned16(G) || !aligned16(U) || !aligned16(dX) || !aligned16(dG) || !aligned16(dU))
+    return set_error(AWQ_E_INVALID, "%s: matrices must be 16-byte aligned", name);
+  const size_t need = w8_back_layout(T, N, K, layers).total;
+  if (!ws || !aligned16(ws) || ws_bytes < need)
+    return set_error(AWQ_E_WORKSPACE, "%s: workspace needs %zu bytes (16-byte aligned)", name,
+                     need);
+  return AWQ_OK;
+}
+
 }  // namespace awq
+
+extern "C" size_t awq_layer_norm_backward_workspace_bytes(int64_t T, int64_t K) {
+  using namespace awq;
+  return T >= 1 && K >= 1 && T <= kMaxDim && K <= kNormMaxK ? norm_back_layout(T, K).total : 0;
+}
+
+extern "C" size_t awq_w8a8_workspace_bytes(int64_t T, int64_t N, int64_t K, int32_t layers) {
+  using namespace awq;
+  return w8_sizes_ok(T, N, K, layers) ? w8_workspace(T, N, K, layers) : 0;
+}
+
+extern "C" size_t awq_w8a8_backward_workspace_bytes(int64_t T, int64_t N, int64_t K,
+                                                    int32_t layers) {
+  using namespace awq;
+  return w8_sizes_ok(T, N, K, layers) && N < kW8BackMaxN ? w8_back_layout(T, N, K, layers).total
+                                                         : 0;
+}
 
 extern "C" size_t awq_w4a16_lora_workspace_bytes(int64_t T, int64_t N, int64_t K, int32_t L,
                                                  int32_t r, awq_dtype dtype) {

@@ -1,0 +1,152 @@
+"""GPU: layer norm and root-mean-square norm, forward and backward, against
+float64 references, element by element, within derived errors."""
+import numpy as np
+import pytest
+import torch
+
+import w8a8_reference as R
+from test_gpu_w8a8 import close, f32, npy, randn
+
+pytestmark = pytest.mark.gpu
+TYPES = R.TYPES
+
+
+@pytest.fixture(scope="module")
+def api():
+    if not torch.cuda.is_available():
+        raise RuntimeError("GPU tests need a GPU")
+    from post_weight_quantization_26_amd import api as A
+    return A
+
+
+SHAPES = [(1, 1), (3, 5), (9, 64), (5, 129), (300, 512), (4, 513), (7, 1000), (1100, 1024),
+          (3, 1152), (2, 2048), (5, 2049), (300, 4096), (3, 4104), (513, 5003), (2, 8192), (3, 8193),
+          (2, 11008), (3, 16383), (300, 16384)]
+
+
+def weights(K, dtype, wide, seed=5):
+    wd = "f32" if wide else dtype
+    gamma = (randn(K, seed=seed) * 0.3 + 1).to(TYPES[wd])
+    return gamma, (randn(K, seed=seed + 1) * 0.3).to(TYPES[wd]), wd
+
+
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T,K", SHAPES)
+def test_forward(api, dtype, rms, T, K):
+    X = (randn(T, K, seed=T + K, scale=2.0) + 0.7).to(TYPES[dtype])
+    for wide, with_beta in ((False, True), (True, False)):
+        gamma, beta, wd = weights(K, dtype, wide)
+        beta = beta if with_beta else None
+        stats = torch.empty(T, 2, device="cuda")
+        codes = torch.empty(T, K, dtype=torch.int8, device="cuda")
+        steps = torch.empty(T, device="cuda")
+        Y = api.layer_norm(X, gamma, beta, eps=1e-5, rms=rms, stats=stats, rows8=(codes, steps))
+        y, st, err, em, er = R.norm(npy(X), npy(gamma), None if beta is None else npy(beta),
+                                    float(np.float32(1e-5)), rms)
+        close(Y, y, R.rounded(y, err, dtype), "Y")
+        close(npy(stats)[:, 0], st[0], em + R.U * np.abs(st[0]), "mean")
+        close(npy(stats)[:, 1], st[1], er + R.U * st[1], "r")
+        step = npy(steps)[:, None]
+        top = np.abs(y).max(1)
+        close(npy(steps) * 127, top, err.max(1) + 2 * R.U * top + 2.0 ** -93, "steps")
+        close(npy(codes) * step, y, err + step * (0.5 + 127 * 4 * R.U), "rows")
+        if dtype == "f32":   # the rows are exactly those of the float32 output
+            rc, rs = R.rows8(f32(Y))
+            assert np.array_equal(codes.cpu().numpy(), rc)
+            assert np.array_equal(steps.cpu().numpy(), rs)
+        only = torch.empty_like(codes), torch.empty_like(steps)
+        assert api.layer_norm(X, gamma, beta, rms=rms, rows8=only, want_y=False) is None
+        assert torch.equal(only[0], codes) and torch.equal(only[1], steps)
+
+
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T,K", SHAPES + [(4097, 40), (9000, 96)])
+def test_gradient(api, dtype, rms, T, K):
+    X = (randn(T, K, seed=T + K, scale=2.0) + 0.7).to(TYPES[dtype])
+    dY = randn(T, K, seed=T + K + 1, scale=0.3, dtype=dtype)
+    for wide, want_beta in ((False, True), (True, False)):
+        gamma, _, wd = weights(K, dtype, wide)
+        stats = torch.empty(T, 2, device="cuda")
+        api.layer_norm(X, gamma, rms=rms, stats=stats)
+        dX, dgamma, dbeta = api.layer_norm_backward(dY, X, stats, gamma, rms=rms,
+                                                    want_beta=want_beta)
+        r = R.norm_back(npy(dY), npy(X), npy(stats), npy(gamma), rms)
+        close(dX, r[0], R.rounded(r[0], r[3], dtype), "dX")
+        close(dgamma, r[1], R.rounded(r[1], r[4], wd), "dgamma")
+        if want_beta:
+            close(dbeta, r[2], R.rounded(r[2], r[5], wd), "dbeta")
+        else:
+            assert dbeta is None
+        again = api.layer_norm_backward(dY, X, stats, gamma, rms=rms, want_beta=want_beta)
+        assert torch.equal(again[0], dX) and torch.equal(again[1], dgamma)
+
+
+@pytest.mark.parametrize("rms", [False, True])
+def test_gradient_against_differences(api, rms):
+    """Central differences of the formula in float64 (their error: below 1e-7 of
+    the terms) against the float32 gradient."""
+    T, K, eps = 6, 50, 1e-3
+    X, dY = randn(T, K, seed=1), randn(T, K, seed=2)
+    gamma = randn(K, seed=3)
+    stats = torch.empty(T, 2, device="cuda")
+    api.layer_norm(X, gamma, eps=eps, rms=rms, stats=stats)
+    dX, dgamma, dbeta = (npy(t) for t in api.layer_norm_backward(dY, X, stats, gamma, rms=rms))
+    x, g, d = npy(X), npy(gamma), npy(dY)
+    b = np.zeros(K)
+    rng = np.random.default_rng(4)
+    e = 1e-5
+
+    def loss(x, g, b):
+        return float((d * R.norm(x, g, b, float(np.float32(eps)), rms)[0]).sum())
+
+    for _ in range(4):
+        vx, vg = rng.standard_normal(x.shape), rng.standard_normal(K)
+        for got, v, lo, hi in ((dX, vx, (x - e * vx, g, b), (x + e * vx, g, b)),
+                               (dgamma, vg, (x, g - e * vg, b), (x, g + e * vg, b)),
+                               (dbeta, vg, (x, g, b - e * vg), (x, g, b + e * vg))):
+            slope = (loss(*hi) - loss(*lo)) / (2 * e)
+            # 100 float32 roundings of the gradient's terms bound its own error
+            assert abs((got * v).sum() - slope) <= 1e-5 * np.abs(got * v).sum() + 1e-6 * abs(slope)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [100, 4096])
+def test_special_rows(api, dtype, K):
+    """Constant and zero rows; a broken row stays alone, but for the column sums."""
+    X = randn(9, K, seed=K, dtype=dtype)
+    X[0] = 0
+    X[1] = 3.0
+    X[2, K - 1] = float("nan")
+    X[3, 0] = float("inf")
+    gamma, beta, _ = weights(K, dtype, False)
+    Y = api.layer_norm(X, gamma, beta)
+    assert torch.equal(Y[0], beta) and torch.equal(Y[1], beta)
+    assert torch.isnan(Y[2]).all() and torch.isnan(Y[3]).all()
+    good = X[4:].clone()
+    assert torch.equal(Y[4:], api.layer_norm(good, gamma, beta))
+    x8 = torch.empty(9, K, dtype=torch.int8, device="cuda"), torch.empty(9, device="cuda")
+    api.layer_norm(X, gamma, beta, rows8=x8, want_y=False)
+    assert torch.isnan(x8[1][2:4]).all() and torch.isfinite(x8[1][4:]).all()
+    assert (x8[0][2:4] == 0).all()
+
+
+def test_unaligned_views(api):
+    base = randn(20, 4100, seed=1, dtype="bf16").reshape(-1)
+    K = 4096
+    gamma, beta, _ = weights(K, "bf16", False)
+    want = None
+    for first in (0, 1, 3):
+        X = torch.empty(8 * K + 8, dtype=torch.bfloat16, device="cuda")[first:first + 8 * K].view(8, K)
+        X.copy_(base[:8 * K].view(8, K))
+        stats = torch.empty(8, 2, device="cuda")
+        Y = api.layer_norm(X, gamma, beta, stats=stats)
+        y, _, err, _, _ = R.norm(npy(X), npy(gamma), npy(beta), 1e-5, False)
+        close(Y, y, R.rounded(y, err, "bf16"), "Y")
+        r = R.norm_back(npy(Y), npy(X), npy(stats), npy(gamma), False)
+        dX, dgamma, dbeta = api.layer_norm_backward(Y, X, stats, gamma)
+        close(dX, r[0], R.rounded(r[0], r[3], "bf16"), "dX")
+        close(dgamma, r[1], R.rounded(r[1], r[4], "bf16"), "dgamma")
+        close(dbeta, r[2], R.rounded(r[2], r[5], "bf16"), "dbeta")
+        want = want if want is not None else Y
