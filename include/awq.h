@@ -531,7 +531,7 @@ awq_status awq_layer_norm_backward(const void* dY, const void* X, const float* s
  * by wsteps_n, the bias (NULL: none; in `dtype`) is added, and the result is
  * rounded once to `dtype` (bf16 or f16). A step that is NaN makes its row or
  * column NaN. K a multiple of 128 below 131072 (the sum fits 32 bits with codes
- * down to -128), N and T any, N*K at most 2^34. codes, qweight, Y, G and U
+ * down to -128), N any below 2^23, T any, N*K at most 2^34. codes, qweight, Y, G and U
  * 16-byte aligned, bias 2, steps 4. ws: at least awq_w8a8_workspace_bytes(T, N,
  * K, layers) bytes, 16-byte aligned (NULL where that is 0), layers 1, or 2 for
  * a gated pair. Does not synchronise.
@@ -548,10 +548,11 @@ awq_status awq_layer_norm_backward(const void* dY, const void* X, const float* s
  * and of a pair, from dH and the forward call's G and U:
  *   dg = dh·u·act'(g);  du = dh·act(g);
  *   dx = Σ_n (dg_n·gsteps_n)·gate[n] + Σ_n (du_n·usteps_n)·up[n].
- * dX [T, K], dG and dU [T, N] are overwritten in `dtype`. The products with the
- * steps are rounded to 16 bits before they meet the codes (fp16: with a power
- * of two per row, so that 2^-24 of a row's largest survives); sums are
- * float32. The layers are not trained. N below 2^21; ws: at least
+ * dX [T, K], dG and dU [T, N] are overwritten in `dtype`. Before they meet the
+ * codes, the gradients' products with the steps are divided by a power of two
+ * per row and rounded to fp16, for either type: 2^-12 of a value is lost, or
+ * 2^-38 of its row's largest, whichever is more. Sums are float32, in an order
+ * that the arguments fix. The layers are not trained. N below 2^21; ws: at least
  * awq_w8a8_backward_workspace_bytes(T, N, K, layers) bytes. */
 enum { AWQ_ACT_SILU = 0, AWQ_ACT_GELU = 1 };
 size_t awq_w8a8_workspace_bytes(int64_t T, int64_t N, int64_t K, int32_t layers);

@@ -27,7 +27,8 @@ SOURCES = ["abi.cpp", "validate.cpp", "stats.hip", "scale.hip", "transform.hip",
            "reduce.hip", "pack.hip", "fold.hip", "w4a16.hip",
            "gram.hip", "fused.hip", "lora_few.hip", "lora_few_back.hip",
            "lora_down.hip", "lora_gemm.hip", "lora_prep.hip", "lora_grad.hip", "act8.hip",
-           "rows8.hip", "norm.hip", "w8_few.hip", "w8_back.hip"]
+           "rows8.hip", "norm.hip", "w8_few.hip", "w8_mid.hip", "w8_gemm.hip",
+           "w8_back.hip", "w8_back_few.hip"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950", "-ffp-contract=off",
           "-fhip-fp32-correctly-rounded-divide-sqrt",

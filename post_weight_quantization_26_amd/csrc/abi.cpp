@@ -1059,9 +1059,23 @@ extern "C" awq_status awq_layer_norm_backward(const void* dY, const void* X, con
   return AWQ_OK;
 }
 
-static awq_status w8_product(const char* name, const W8Product& p, void* stream) {
+static awq_status w8_product(const char* name, W8Product p, int32_t layers, void* ws,
+                             void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
-  AWQ_HIP(timed(AWQ_K_W8A8, st, [&] { return launch_w8_few(p, st); }), name);
+  const W8Plan l = w8_plan(p.T, p.N, p.K, layers);
+  p.tile_n = l.tile_n;
+  p.tile_t = l.tile_t;
+  p.runs = int(l.runs);
+  p.ldp = l.ldp;
+  p.partial = static_cast<int*>(ws);
+  p.cut = {int(l.cut.full), int(l.cut.runs), static_cast<float*>(ws)};
+  AWQ_HIP(timed(AWQ_K_W8A8, st,
+                [&] {
+                  return l.form == W8Form::kFew   ? launch_w8_few(p, st)
+                         : l.form == W8Form::kMid ? launch_w8_mid(p, st)
+                                                  : launch_w8_gemm(p, st);
+                }),
+          name);
   return AWQ_OK;
 }
 
@@ -1082,7 +1096,7 @@ extern "C" awq_status awq_w8a8_matmul(const int8_t* codes, const float* steps, i
   p.K = K;
   p.f16 = dtype == AWQ_F16;
   p.Y = static_cast<uint16_t*>(Y);
-  return w8_product("w8a8_matmul", p, stream);
+  return w8_product("w8a8_matmul", p, 1, ws, stream);
 }
 
 extern "C" awq_status awq_w8a8_gated_matmul(const int8_t* codes, const float* steps, int64_t T,
@@ -1107,7 +1121,7 @@ extern "C" awq_status awq_w8a8_gated_matmul(const int8_t* codes, const float* st
   p.Y = static_cast<uint16_t*>(H);
   p.G = static_cast<uint16_t*>(G);
   p.U = static_cast<uint16_t*>(U);
-  return w8_product("w8a8_gated_matmul", p, stream);
+  return w8_product("w8a8_gated_matmul", p, 2, ws, stream);
 }
 
 static awq_status w8_back(const char* name, W8Back p, int32_t layers, void* ws, void* stream) {
@@ -1115,8 +1129,14 @@ static awq_status w8_back(const char* name, W8Back p, int32_t layers, void* ws, 
   const W8BackLayout l = w8_back_layout(p.T, p.N, p.K, layers);
   p.Np = l.Np;
   p.A = at<uint16_t>(ws, l.a);
-  p.B = at<uint16_t>(ws, l.b);
   p.E = at<float>(ws, l.e);
+  p.B = at<uint16_t>(ws, l.b);
+  p.vec = rows_vec(8, {p.w.steps, p.u.steps});
+  p.few = l.few;
+  p.tile_t = l.tile_t;
+  p.runs = int(l.runs);
+  p.partial = at<float>(ws, l.sums);
+  p.cut = {int(l.cut.full), int(l.cut.runs), p.partial};
   AWQ_HIP(timed(AWQ_K_W8A8, st, [&] { return launch_w8_back(p, st); }), name);
   return AWQ_OK;
 }

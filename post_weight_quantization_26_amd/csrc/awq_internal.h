@@ -282,6 +282,7 @@ awq_status check_act8(const char* name, const void* X, awq_dtype d, int64_t T, i
 constexpr int64_t kRows8MaxK = 65536;
 constexpr int64_t kNormMaxK = 16384;
 constexpr int64_t kW8MaxK = (int64_t(1) << 17) - 1;   // 128·128·K fits an int32
+constexpr int64_t kW8MaxN = int64_t(1) << 23;         // 256 rows of outputs: 32-bit offsets
 constexpr int64_t kW8BackMaxN = int64_t(1) << 21;
 // The gradient's row groups, each with a row of partial sums of Kp columns.
 struct NormBackLayout {
@@ -289,10 +290,25 @@ struct NormBackLayout {
   size_t total;
 };
 NormBackLayout norm_back_layout(int64_t T, int64_t K);
-size_t w8_workspace(int64_t T, int64_t N, int64_t K, int32_t layers);
+// Which kernels a product takes (w8_few.hip, w8_mid.hip, w8_gemm.hip).
+enum class W8Form { kFew, kMid, kBig };
+struct W8Plan {
+  W8Form form;
+  int tile_n, tile_t;  // kMid: rows of A and tokens of a tile,
+  int64_t runs;        // runs of the contraction
+  int64_t ldp;         // and N rounded up to 4,
+  LoraCut cut;         // kBig: the last tiles, cut
+  size_t bytes;        // the runs' sums: kMid [runs, layers, T, ldp] int32, kBig tiles
+};
+W8Plan w8_plan(int64_t T, int64_t N, int64_t K, int32_t layers);
 struct W8BackLayout {
   int64_t Np, C;       // N rounded up to 64; the contraction's length
-  size_t a, b, e;      // 16-bit [T, C] and [K, C], f32 [T]
+  bool few;            // no transposed layer: tokens of a tile and runs
+  int tile_t;
+  int64_t runs;
+  size_t a, b, e;      // fp16 [T (few: rounded up to 16), C], [K, C] (not few), f32 [T]
+  LoraCut cut;         // not few: the last 256x256 tiles, cut
+  size_t sums;         // the runs' sums: [runs, T, K] f32, or the cut tiles
   size_t total;
 };
 W8BackLayout w8_back_layout(int64_t T, int64_t N, int64_t K, int32_t layers);

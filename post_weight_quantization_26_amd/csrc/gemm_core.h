@@ -196,6 +196,14 @@ __device__ __forceinline__ void mfma16_first(floatx4& c, const bf16x8_t& a, cons
 __device__ __forceinline__ void mfma16_first(floatx4& c, const f16x8_t& a, const f16x8_t& b) {
   asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, 0" : "=a"(c) : "v"(a), "v"(b));
 }
+// 16 codes an operand; the accumulator's registers hold 4 int32 sums (whose
+// zero is the float's).
+__device__ __forceinline__ void mfma16(floatx4& c, const i8x16_t& a, const i8x16_t& b) {
+  asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
+__device__ __forceinline__ void mfma16_first(floatx4& c, const i8x16_t& a, const i8x16_t& b) {
+  asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, 0" : "=a"(c) : "v"(a), "v"(b));
+}
 template <bool FIRST, class V>
 __device__ __forceinline__ void mfma16_acc(floatx4& c, const V& a, const V& b) {
   if (FIRST) mfma16_first(c, a, b);
@@ -299,9 +307,9 @@ __device__ __forceinline__ void mfma_8x8(floatx4 (&acc)[8][8], const V (&fa)[8],
 // them safe to read (the last MFMAs have drained). INIT: adds to what they
 // hold instead; k-tile 0's copies (dma64<0>(c, 0)) are the caller's then, so
 // that they can be in flight while it makes that starting value.
-template <bool F16, bool INIT = false>
-__device__ __forceinline__ void gemm_mainloop16(const GemmCtx64& c, floatx4 (&acc)[8][8]) {
-  typedef typename Operand<F16>::type V;
+// V: the operands' type; of 8-bit codes the context counts pairs as elements.
+template <class V, bool INIT = false>
+__device__ __forceinline__ void gemm_mainloop16_of(const GemmCtx64& c, floatx4 (&acc)[8][8]) {
   int rdA[2], rdB[2];
   frag_offsets16(c, rdA, rdB);
   if constexpr (!INIT) dma64<0>(c, 0);
@@ -325,6 +333,11 @@ __device__ __forceinline__ void gemm_mainloop16(const GemmCtx64& c, floatx4 (&ac
   for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) asm volatile("" : "+a"(acc[i][j]));
+}
+
+template <bool F16, bool INIT = false>
+__device__ __forceinline__ void gemm_mainloop16(const GemmCtx64& c, floatx4 (&acc)[8][8]) {
+  gemm_mainloop16_of<typename Operand<F16>::type, INIT>(c, acc);
 }
 
 // The k-loop of one tile in a chain of tiles: k-tile 0 is already in stage

@@ -10,6 +10,7 @@ namespace {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef int i8x16_t __attribute__((ext_vector_type(4)));   // 16 8-bit codes
 
 // MFMA operand vector of 8 elements: bf16 or fp16 (F16 = true).
 template <bool F16>

@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cstdarg>
 #include <cstdio>
+#include <cstdlib>
 #include <cstring>
 
 #include "awq_internal.h"
@@ -857,11 +858,113 @@ awq_status check_norm_back(const void* dY, const void* X, const float* stats, aw
 }
 
 static bool w8_sizes_ok(int64_t T, int64_t N, int64_t K, int32_t layers) {
-  return T >= 1 && N >= 1 && K >= 1 && T <= kMaxDim && N <= kMaxDim && K <= kW8MaxK &&
+  return T >= 1 && N >= 1 && K >= 1 && T <= kMaxDim && N < kW8MaxN && K <= kW8MaxK &&
          K % kTileK == 0 && (layers == 1 || layers == 2);
 }
 
-size_t w8_workspace(int64_t, int64_t, int64_t, int32_t) { return 0; }
+static int w8_force(const char* name) {
+  const char* v = getenv(name);
+  return v ? atoi(v) : -1;
+}
+
+// 256x256 tiles: time in us for rounds of 256 tiles and the last ones, whole or cut
+// into the runs that take least. Steps are slower the more CUs work (1.15 us alone,
+// 1.65 on all; the chip's power), a round's ends take 15 us, the runs' sums 0.035 us
+// each and a launch: 4096 tokens of 4096x11008 150 us (this rule 157), 1600 of them
+// 77 cut and 129 whole (80 and 138), 5000 of 28672x8192 1019 (1066).
+static double w8_big_us(int64_t rows, int64_t T, int64_t steps, LoraCut& cut) {
+  const int64_t tiles = ceil_div(T, 256) * ceil_div(rows, 256), rest = tiles % 256;
+  const double s = double(steps);
+  cut = LoraCut{};
+  double tail = rest ? 15 + s * (1.1 + 0.6 * double(rest) / 256) : 0;
+  for (int64_t runs = 2; rest && runs <= std::min<int64_t>(256 / rest, steps / 2); ++runs) {
+    const double units = double(rest * runs);
+    const double t = 12 + 0.035 * units + s / double(runs) * (0.95 + 0.5 * units / 256);
+    if (t < tail) {
+      tail = t;
+      cut.runs = runs;
+    }
+  }
+  if (cut.runs) {
+    cut.full = tiles - rest;
+    cut.bytes = size_t(rest) * size_t(cut.runs) * 256 * 256 * 4;
+  }
+  return double(tiles / 256) * (15 + 1.65 * s) + tail;
+}
+
+// Tile and runs of the contraction for a product of `rows` output channels, T
+// tokens and `steps` steps of 128 bytes, by an estimate in us of each choice.
+struct W8Tiling {
+  bool big;
+  int tile_n, tile_t;
+  int64_t runs;
+  LoraCut cut;
+};
+static W8Tiling w8_tiling(int64_t rows, int64_t T, int64_t steps) {
+  W8Tiling best{};
+  best.big = true;
+  best.tile_n = best.tile_t = 256;
+  best.runs = 1;
+  double least = w8_big_us(rows, T, steps, best.cut);
+  struct Shape {
+    int n, t;
+    double us;    // a step of a tile on a CU
+    bool pairs;   // two workgroups a CU share it: half rounds count
+  };
+  static constexpr Shape shapes[] = {
+      {128, 32, 0.27, true}, {128, 64, 0.35, true}, {128, 128, 0.62, false}, {256, 128, 1.15, false}};
+  for (const Shape& s : shapes) {
+    const int64_t n = ceil_div(rows, s.n) * ceil_div(T, s.t);
+    if (n > 16384) continue;
+    for (int64_t runs = 1; runs <= 8 && runs * 2 <= std::max<int64_t>(steps, 2); ++runs) {
+      if (runs > 1 && n * runs > 768) break;
+      const int64_t units = n * runs;
+      const double rounds = s.pairs ? std::max(1.0, double(units) / 256)
+                                    : double(ceil_div(units, 256));
+      double us = 5 + rounds * s.us * double(steps) / double(runs);
+      if (runs > 1) us += 3 + double(runs) * double(T) * double(rows) * 8 / 6e6;
+      if (us < least) {
+        least = us;
+        best.big = false;
+        best.tile_n = s.n;
+        best.tile_t = s.t;
+        best.runs = runs;
+        best.cut = LoraCut{};
+      }
+    }
+  }
+  return best;
+}
+
+W8Plan w8_plan(int64_t T, int64_t N, int64_t K, int32_t layers) {
+  W8Plan l{};
+  l.runs = 1;
+  const int64_t codes = N * layers * K;
+  const int f = w8_force("W8_FORM");
+  if (f >= 0 ? f == 0 : T <= 4 || (T <= 8 && codes <= (64 << 20)) || (T <= 16 && codes <= (32 << 20))) {
+    l.form = W8Form::kFew;
+    return l;
+  }
+  W8Tiling t = w8_tiling(N * layers, T, K / 128);
+  if (f == 1) {
+    t.big = false; t.cut = LoraCut{};
+    const int tt = w8_force("W8_TILE"), r = w8_force("W8_RUNS");
+    if (tt > 0) { t.tile_t = tt; t.tile_n = 128; if (tt == 256) { t.tile_n = 256; t.tile_t = 128; } }
+    if (r > 0) t.runs = std::min<int64_t>(r, K / 128);
+  }
+  if (f == 2) { t = W8Tiling{}; t.big = true; }
+  if (f == 3) { t = W8Tiling{}; t.big = true; t.cut = lora_cut(T, N * layers, K / 2); 
+    if (w8_force("W8_RUNS") > 0) { const int64_t tl = ceil_div(T, 256) * ceil_div(N, layers == 2 ? 128 : 256); t.cut.runs = std::min<int64_t>(w8_force("W8_RUNS"), K / 128); t.cut.full = tl / 256 * 256; t.cut.bytes = size_t(tl % 256) * t.cut.runs * 262144; if (tl % 256 == 0) t.cut = LoraCut{}; } }
+  l.form = t.big ? W8Form::kBig : W8Form::kMid;
+  l.tile_n = t.tile_n;
+  l.tile_t = t.tile_t;
+  l.runs = t.runs ? t.runs : 1;
+  l.ldp = ceil_div(N, 4) * 4;
+  l.cut = t.cut;
+  l.bytes = t.big ? align_up(l.cut.bytes)
+            : l.runs > 1 ? align_up(size_t(l.runs * layers) * size_t(T) * size_t(l.ldp) * 4) : 0;
+  return l;
+}
 
 W8BackLayout w8_back_layout(int64_t T, int64_t N, int64_t K, int32_t layers) {
   W8BackLayout l{};
@@ -873,9 +976,27 @@ W8BackLayout w8_back_layout(int64_t T, int64_t N, int64_t K, int32_t layers) {
     off += align_up(bytes);
     return at;
   };
-  l.a = take(size_t(T) * size_t(l.C) * 2);
-  l.b = take(size_t(K) * size_t(l.C) * 2);
+  const double us = w8_big_us(K, T, l.C / 64, l.cut) + 5 + double(l.C) * double(K) * 3 / 4e6;
+  l.tile_t = T <= 16 ? 16 : T <= 32 ? 32 : 64;
+  l.runs = 1;
+  const int64_t tiles = (K / 128) * ceil_div(T, l.tile_t), blocks = l.C / 32;
+  l.runs = std::max<int64_t>(1, std::min<int64_t>({512 / tiles, blocks / 16, 16}));
+  const int f = w8_force("W8_FORM");
+  l.few = us > 1e9 || T <= 512;
+  if (f == 1) { l.few = true; if (w8_force("W8_TILE") > 0) l.tile_t = w8_force("W8_TILE"); if (w8_force("W8_RUNS") > 0) l.runs = std::min<int64_t>(w8_force("W8_RUNS"), blocks); }
+  if (f == 2 || f == 3) { l.few = false; l.cut = LoraCut{}; 
+    const int64_t tl = ceil_div(T, 256) * ceil_div(K, 256);
+    if (f == 3 && tl % 256) { l.cut.runs = std::min<int64_t>(w8_force("W8_RUNS"), l.C / 64); l.cut.full = tl / 256 * 256; l.cut.bytes = size_t(tl % 256) * l.cut.runs * 262144; } }
+  l.a = take(size_t(l.few ? ceil_div(T, 16) * 16 : T) * size_t(l.C) * 2);
   l.e = take(size_t(T) * 4);
+  if (l.few) {
+    l.cut = LoraCut{};
+    if (l.runs > 1) l.sums = take(size_t(l.runs) * size_t(T) * size_t(K) * 4);
+  } else {
+    l.runs = 1;
+    l.b = take(size_t(K) * size_t(l.C) * 2);
+    l.sums = take(l.cut.bytes);
+  }
   l.total = off;
   return l;
 }
@@ -894,14 +1015,14 @@ static awq_status check_w8_common(const char* name, const void* V, awq_dtype d, 
                      (long long)N, (long long)K);
   if (K % kTileK)
     return set_error(AWQ_E_INVALID, "%s: K=%lld not a multiple of 128", name, (long long)K);
-  if (K > kW8MaxK || N * K > kMaxMatrixElems)
+  if (K > kW8MaxK || N >= kW8MaxN || N * K > kMaxMatrixElems)
     return set_error(AWQ_E_UNSUPPORTED,
-                     "%s: N=%lld x K=%lld (K below 131072, N*K at most 2^34)", name, (long long)N,
-                     (long long)K);
+                     "%s: N=%lld x K=%lld (K below 131072, N below 2^23, N*K at most 2^34)", name,
+                     (long long)N, (long long)K);
   if (layers == 2 && act != AWQ_ACT_SILU && act != AWQ_ACT_GELU)
     return set_error(AWQ_E_INVALID, "%s: unknown activation %d", name, int(act));
   if (!grid_fits(search_gemm_blocks(T, std::max(2 * N, K), AWQ_BF16), 256) ||
-      !grid_fits(T, 256) || !grid_fits(ceil_div(T, 16) * ceil_div(N, 16), 1024) ||
+      !grid_fits(T, 1024) || !grid_fits(ceil_div(T, 16) * ceil_div(N, 16), 1024) ||
       ceil_div(T, 16) > 65535)
     return set_error(AWQ_E_UNSUPPORTED, "%s: T=%lld x N=%lld exceed the grids", name,
                      (long long)T, (long long)N);
@@ -923,7 +1044,7 @@ awq_status check_w8(const char* name, const void* codes, const float* steps, int
       !aligned_elem(bias, d))
     return set_error(AWQ_E_INVALID,
                      "%s: the outputs must be 16-byte aligned, steps 4, bias 2", name);
-  const size_t need = w8_workspace(T, N, K, layers);
+  const size_t need = w8_plan(T, N, K, layers).bytes;
   if (need && (!ws || !aligned16(ws) || ws_bytes < need))
     return set_error(AWQ_E_WORKSPACE, "%s: workspace needs %zu bytes (16-byte aligned)", name,
                      need);
@@ -960,7 +1081,7 @@ extern "C" size_t awq_layer_norm_backward_workspace_bytes(int64_t T, int64_t K) 
 
 extern "C" size_t awq_w8a8_workspace_bytes(int64_t T, int64_t N, int64_t K, int32_t layers) {
   using namespace awq;
-  return w8_sizes_ok(T, N, K, layers) ? w8_workspace(T, N, K, layers) : 0;
+  return w8_sizes_ok(T, N, K, layers) ? w8_plan(T, N, K, layers).bytes : 0;
 }
 
 extern "C" size_t awq_w8a8_backward_workspace_bytes(int64_t T, int64_t N, int64_t K,

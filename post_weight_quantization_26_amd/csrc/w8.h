@@ -51,6 +51,14 @@ struct NormBack {
 };
 hipError_t launch_norm_back(const NormBack& p, int dtype, hipStream_t st);
 
+// 256x256 tiles: those from `full` (a multiple of 256) on are cut into runs of the
+// contraction, whose accumulators go to part [cut tiles, runs, 256·256]. runs 0:
+// none is.
+struct W8Cut {
+  int full, runs;
+  float* part;
+};
+
 // One 8-bit layer: codes [N, K], steps [N].
 struct W8Layer {
   const int8_t* q;
@@ -70,8 +78,15 @@ struct W8Product {
   uint16_t* Y;
   uint16_t* G;         // [T, N] products before the activation, or NULL
   uint16_t* U;
+  // a few hundred tokens: rows of A (128 or 256) and tokens of a tile, runs of the
+  // contraction, and for more than one run their sums [runs, layers, T, ldp]
+  int tile_n, tile_t, runs;
+  int64_t ldp;
+  int* partial;
+  W8Cut cut;           // many tokens
 };
 hipError_t launch_w8_few(const W8Product& p, hipStream_t st);
+hipError_t launch_w8_mid(const W8Product& p, hipStream_t st);
 hipError_t launch_w8_gemm(const W8Product& p, hipStream_t st);
 
 // dX[t][k] = Σ_n (dY[t][n]·w_n)·q[n][k], or of a gated pair from dH, G and U.
@@ -83,12 +98,17 @@ struct W8Back {
   int64_t T, N, K, Np; // Np: N rounded up to 64
   int act;
   bool f16;
-  uint16_t* A;         // [T, C] operand, C = Np (twice that for a pair)
-  float* E;            // [T] factor of a row of A (fp16)
-  uint16_t* B;         // [K, C] codes
+  uint16_t* A;         // fp16 operand of [T, C], C = Np (twice that for a pair)
+  float* E;            // [T] factor of a row of A
+  uint16_t* B;         // many tokens: [K, C] codes as fp16
   uint16_t* dX;
-  uint16_t* dG;        // or NULL
+  uint16_t* dG;        // a pair's
   uint16_t* dU;
+  bool vec;            // the steps are 16-byte aligned
+  bool few;            // no transposed layer: tokens of a tile, runs of the
+  int tile_t, runs;    // contraction and, for more than one, their sums [runs, T, K]
+  float* partial;
+  W8Cut cut;           // many tokens
 };
 hipError_t launch_w8_back(const W8Back& p, hipStream_t st);
 

@@ -5,85 +5,185 @@
 //   gated   dg = dh·u·act'(g), du = dh·act(g);
 //           dx[t][k] = Σ_n (dg·wg_n)·qg[n][k] + Σ_n (du·wu_n)·qu[n][k]
 //
-// One 16-bit product: the steps join the gradient in the operand A [T, C] (one
-// rounding), the codes are exact operands B [K, C] in either type. A pair's
-// two sums are one contraction of twice the length. Three launches: A, B, and
-// the 256x256 main loop of gemm_core.h.
-#include "gemm_core.h"
-#include "w8_common.h"
+// One fp16 product: the steps join the gradient in the operand A (one rounding),
+// the codes are exact fp16 numbers. A pair's two sums are one contraction of
+// twice the length. fp16 for bf16 gradients too: it keeps 3 bits more, and a
+// power of two per row takes the place of bf16's range. Launch 1 forms A; then
+//  * many tokens: launch 2 writes the codes' transpose as fp16 operand rows [K, C]
+//    and launch 3 is the 256x256 main loop of gemm_core.h;
+//  * fewer: w8_back_few.hip takes the codes as they are.
+#include "w8_cut.h"
+#include "w8_back.h"
 
 namespace awq {
 namespace {
 
-// A row of A. fp16: dy·w may leave the type's range, so the row is divided by
-// the power of two that takes its largest finite value below 2^14, which the
-// last launch multiplies back in (exactly, but for results below 2^-126); a
-// first pass finds it. Columns from N to Np are zero.
-template <bool F16, bool GATED, int ACT>
-__global__ __launch_bounds__(256) void w8_grad_rows_kernel(const W8Back p) {
-  __shared__ uint32_t red[4];
-  const int64_t t = blockIdx.x;
-  const uint16_t* dy = p.dY + t * p.N;
-  const uint16_t* gr = GATED ? p.G + t * p.N : nullptr;
-  const uint16_t* ur = GATED ? p.U + t * p.N : nullptr;
-  uint16_t* out = p.A + t * (GATED ? 2 : 1) * p.Np;
-  auto values = [&](int64_t n, float& a, float& b, float& dg, float& du) {
-    const float d = widen16<F16>(dy[n]);
-    if constexpr (GATED) {
-      const float u = widen16<F16>(ur[n]);
-      float ac;
-      const float slope = act_slope<ACT>(widen16<F16>(gr[n]), ac);
-      dg = (d * u) * slope;
-      du = d * ac;
-      a = dg * p.w.steps[n];
-      b = du * p.u.steps[n];
-    } else {
-      a = d * p.w.steps[n];
-      b = 0.f;
-    }
-  };
-  float scale = 1.f;
-  if constexpr (F16) {
-    uint32_t m = 0;
-    for (int64_t n = threadIdx.x; n < p.N; n += 256) {
-      float a, b, dg, du;
-      values(n, a, b, dg, du);
-      const uint32_t ua = __float_as_uint(a) & 0x7FFFFFFFu, ub = __float_as_uint(b) & 0x7FFFFFFFu;
-      if (ua < 0x7F800000u && ua > m) m = ua;
-      if (ub < 0x7F800000u && ub > m) m = ub;
-    }
-#pragma unroll
-    for (int i = 32; i; i >>= 1) {
-      const uint32_t o = __shfl_xor(m, i);
-      m = m > o ? m : o;
-    }
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = m > red[i] ? m : red[i];
-    // 2^e <= largest < 2^(e+1): divide by 2^(e-13); the factor and its inverse
-    // stay normal numbers
-    int e = int(m >> 23) - 127 - 13;
-    e = e < -126 ? -126 : e > 126 ? 126 : e;
-    scale = m ? __uint_as_float(uint32_t(127 - e) << 23) : 1.f;
-    if (threadIdx.x == 0) p.E[t] = m ? __uint_as_float(uint32_t(127 + e) << 23) : 1.f;
+__device__ __forceinline__ uint32_t finite_abs(float v) {
+  const uint32_t u = __float_as_uint(v) & 0x7FFFFFFFu;
+  return u < 0x7F800000u ? u : 0;
+}
+
+// The power of two of a row whose largest finite |a| has these bits: 2^e takes it
+// to [2^13, 2^14), where |code|·a stays far from the fp16 and float32 limits.
+// Returns e, with 2^e and 2^-e normal numbers; 0 for a row of zeros.
+__device__ __forceinline__ int row_exponent(uint32_t largest) {
+  if (!largest) return 0;
+  const int e = int(largest >> 23) - 127 - 13;
+  return e < -126 ? -126 : e;   // at most 254 - 140
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(127 + e) << 23); }
+
+// dg·wg and du·wu (or dy·w alone) of one output.
+template <bool GATED, int ACT>
+__device__ __forceinline__ void back_values(float d, float g, float u, float w, float wu, float& a,
+                                            float& b, float& dg, float& du) {
+  if constexpr (GATED) {
+    float ac;
+    const float slope = act_slope<ACT>(g, ac);
+    dg = (d * u) * slope;
+    du = d * ac;
+    a = dg * w;
+    b = du * wu;
+  } else {
+    a = d * w;
+    b = 0.f;
   }
+}
+
+__device__ __forceinline__ uint32_t block_max(uint32_t m) {
+  __shared__ uint32_t red[16];
+  m = wave_max(m);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+  __syncthreads();
+  uint32_t r = 0;
+  for (int i = 0; i < int(blockDim.x >> 6); ++i) r = r > red[i] ? r : red[i];
+  return r;
+}
+
+// A's element (t, c), c over the layers' Np each: rows [T, C], or, for few tokens,
+// in the order of that kernel's operand: blocks of 32 c x 16 tokens, a lane's 8
+// consecutive c together.
+__device__ __forceinline__ int64_t operand_at(const W8Back& p, int64_t t, int64_t c, int64_t C) {
+  if (!p.few) return t * C + c;
+  const int64_t tb = (p.T + 15) >> 4;
+  return (((c >> 5) * tb + (t >> 4)) * 64 + ((c >> 3) & 3) * 16 + (t & 15)) * 8 + (c & 7);
+}
+
+// A row of A, its values held in registers between the maximum and the rounding:
+// dY, G and U are read once. N a multiple of 8, at most 8·V·blockDim. Bound by HBM.
+template <bool F16, bool GATED, int ACT, int V>
+__global__ __launch_bounds__(1024) void w8_grad_rows_kernel(const W8Back p) {
+  const int64_t t = blockIdx.x, C = (GATED ? 2 : 1) * p.Np;
+  const int n8 = int(p.N >> 3);
+  const int64_t row = t * p.N;
+  uint4 rd[V], rg[V], ru[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int j = threadIdx.x + i * blockDim.x;
+    if (j >= n8) continue;
+    rd[i] = *reinterpret_cast<const uint4*>(p.dY + row + j * 8);
+    if constexpr (GATED) {
+      rg[i] = *reinterpret_cast<const uint4*>(p.G + row + j * 8);
+      ru[i] = *reinterpret_cast<const uint4*>(p.U + row + j * 8);
+    }
+  }
+  auto half = [](const uint4& v, int e) {
+    const uint32_t w = e < 2 ? v.x : e < 4 ? v.y : e < 6 ? v.z : v.w;
+    return widen16<F16>(uint16_t(e & 1 ? w >> 16 : w));
+  };
+  float a[V][8], b[GATED ? V : 1][8];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int j = threadIdx.x + i * blockDim.x;
+    if (j >= n8) continue;
+    float w[8], wu[8];
+    load8<0>(p.w.steps, j * 8, w);
+    if constexpr (GATED) load8<0>(p.u.steps, j * 8, wu);
+    uint32_t hg[4], hu[4];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float dg, du, bb;
+      back_values<GATED, ACT>(half(rd[i], e), GATED ? half(rg[i], e) : 0.f,
+                              GATED ? half(ru[i], e) : 0.f, w[e], GATED ? wu[e] : 0.f, a[i][e], bb,
+                              dg, du);
+      const uint32_t ma = finite_abs(a[i][e]);
+      m = m > ma ? m : ma;
+      if constexpr (GATED) {
+        b[i][e] = bb;
+        const uint32_t mb = finite_abs(bb);
+        m = m > mb ? m : mb;
+        const uint32_t g16 = round16<F16>(dg), u16 = round16<F16>(du);
+        hg[e >> 1] = e & 1 ? hg[e >> 1] | g16 << 16 : g16;
+        hu[e >> 1] = e & 1 ? hu[e >> 1] | u16 << 16 : u16;
+      }
+    }
+    if constexpr (GATED) {
+      *reinterpret_cast<uint4*>(p.dG + row + j * 8) = make_uint4(hg[0], hg[1], hg[2], hg[3]);
+      *reinterpret_cast<uint4*>(p.dU + row + j * 8) = make_uint4(hu[0], hu[1], hu[2], hu[3]);
+    }
+  }
+  const int e = row_exponent(block_max(m));
+  const float down = pow2(-e);
+  if (threadIdx.x == 0) p.E[t] = pow2(e);
+  auto store = [&](const float (&v)[8], int64_t c) {
+    float s[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s[k] = v[k] * down;
+    store8<2>(p.A, operand_at(p, t, c, C), s);
+  };
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int j = threadIdx.x + i * blockDim.x;
+    if (j >= n8) continue;
+    store(a[i], j * 8);
+    if constexpr (GATED) store(b[i], p.Np + j * 8);
+  }
+  // from N to Np: zeros
+  const int pad = int((p.Np - p.N) >> 3);
+  const float zero[8] = {};
+  if (int(threadIdx.x) < pad) {
+    store8<2>(p.A, operand_at(p, t, p.N + threadIdx.x * 8, C), zero);
+    if constexpr (GATED) store8<2>(p.A, operand_at(p, t, p.Np + p.N + threadIdx.x * 8, C), zero);
+  }
+}
+
+// The same for any N, element by element in two passes.
+template <bool F16, bool GATED, int ACT>
+__global__ __launch_bounds__(256) void w8_grad_rows_any_kernel(const W8Back p) {
+  const int64_t t = blockIdx.x, C = (GATED ? 2 : 1) * p.Np;
+  const int64_t row = t * p.N;
+  auto values = [&](int64_t n, float& a, float& b, float& dg, float& du) {
+    back_values<GATED, ACT>(widen16<F16>(p.dY[row + n]), GATED ? widen16<F16>(p.G[row + n]) : 0.f,
+                            GATED ? widen16<F16>(p.U[row + n]) : 0.f, p.w.steps[n],
+                            GATED ? p.u.steps[n] : 0.f, a, b, dg, du);
+  };
+  uint32_t m = 0;
+  for (int64_t n = threadIdx.x; n < p.N; n += 256) {
+    float a, b, dg, du;
+    values(n, a, b, dg, du);
+    const uint32_t ma = finite_abs(a), mb = finite_abs(b);
+    m = m > ma ? m : ma;
+    m = m > mb ? m : mb;
+  }
+  const int e = row_exponent(block_max(m));
+  const float down = pow2(-e);
+  if (threadIdx.x == 0) p.E[t] = pow2(e);
   for (int64_t n = threadIdx.x; n < p.Np; n += 256) {
     float a = 0.f, b = 0.f, dg, du;
     if (n < p.N) {
       values(n, a, b, dg, du);
       if constexpr (GATED) {
-        p.dG[t * p.N + n] = round16<F16>(dg);
-        p.dU[t * p.N + n] = round16<F16>(du);
+        p.dG[row + n] = round16<F16>(dg);
+        p.dU[row + n] = round16<F16>(du);
       }
     }
-    out[n] = round16<F16>(a * scale);
-    if constexpr (GATED) out[p.Np + n] = round16<F16>(b * scale);
+    p.A[operand_at(p, t, n, C)] = round16<true>(a * down);
+    if constexpr (GATED) p.A[operand_at(p, t, p.Np + n, C)] = round16<true>(b * down);
   }
 }
 
-// B: 64 x 64 codes through LDS, as 16-bit numbers. grid (Np / 64, K / 64, layers).
-template <bool F16>
+// B: 64 x 64 codes through LDS, as fp16 numbers. grid (Np / 64, K / 64, layers).
 __global__ __launch_bounds__(256) void w8_transpose_kernel(const W8Back p, int64_t C) {
   __shared__ uint32_t tile[64][17];   // [n][k / 4]
   const int64_t n0 = int64_t(blockIdx.x) * 64, k0 = int64_t(blockIdx.y) * 64;
@@ -100,67 +200,111 @@ __global__ __launch_bounds__(256) void w8_transpose_kernel(const W8Back p, int64
   const int k = threadIdx.x >> 2, nn = (threadIdx.x & 3) * 16;
   uint32_t h[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int8_t lo = int8_t(tile[nn + 2 * i][k >> 2] >> (8 * (k & 3)));
-    const int8_t hi = int8_t(tile[nn + 2 * i + 1][k >> 2] >> (8 * (k & 3)));
-    h[i] = uint32_t(round16<F16>(float(lo))) | uint32_t(round16<F16>(float(hi))) << 16;
-  }
+  for (int i = 0; i < 8; ++i)
+    h[i] = codes_to_f16(tile[nn + 2 * i][k >> 2], tile[nn + 2 * i + 1][k >> 2],
+                        byte_pair(0) + 0x00010001u * (k & 3));
   uint4* o = reinterpret_cast<uint4*>(p.B + (k0 + k) * C + int64_t(blockIdx.z) * p.Np + n0 + nn);
   o[0] = make_uint4(h[0], h[1], h[2], h[3]);
   o[1] = make_uint4(h[4], h[5], h[6], h[7]);
 }
 
-// dX = E·(A·Bᵀ): the main loop's A rows are the channels k, so a lane holds 4
-// consecutive ones of a token.
+// Channels k .. k + 3 of a token.
 template <bool F16>
+__device__ __forceinline__ void store_dx(const W8Back& p, int64_t t, int64_t k, float e,
+                                         floatx4 s) {
+  const float y[4] = {s[0] * e, s[1] * e, s[2] * e, s[3] * e};
+  store4<F16>(p.dX + t * p.K + k, true, 4, y);
+}
+
+// dX = E·(A·Bᵀ): the main loop's A rows are the channels k, so a lane holds 4
+// consecutive ones of a token. Bound by the matrix cores.
+template <bool F16, bool CUT>
 __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void w8_back_gemm_kernel(const W8Back p, int64_t C, int tiles_t, int tiles_k) {
-  int tt, tk;
-  if (!tile_of(blockIdx.x, tiles_t, tiles_k, tt, tk)) return;
-  const int64_t t0 = int64_t(tt) * BN, k0 = int64_t(tk) * BM;
-  const int64_t rows_k = p.K - k0 < BM ? p.K - k0 : BM;
+  W8Unit unit;
+  if (!w8_unit<CUT>(p.cut, tiles_t, tiles_k, unit)) return;
+  const int64_t t0 = int64_t(unit.tt) * BN, o0 = int64_t(unit.tn) * BM;
+  const int64_t rows_o = p.K - o0 < BM ? p.K - o0 : BM;
   const int64_t rows_t = p.T - t0 < BN ? p.T - t0 : BN;
+  int64_t c0 = 0, c1 = C;
+  if constexpr (CUT) w8_run(p.cut, unit, int(C / BK64), c0, c1);
   GemmCtx64 c;
-  gemm_setup64(c, p.B + k0 * C, rows_k, p.A + t0 * C, rows_t, C);
+  w8_setup(c, p.B + o0 * C + c0, rows_o, p.A + t0 * C + c0, rows_t, C, c1 - c0);
   floatx4 acc[8][8];
-  gemm_mainloop16<F16>(c, acc);
+  gemm_mainloop16<true>(c, acc);
+  if (CUT && unit.slot >= 0) {
+    w8_store_run(p.cut, unit, c.wave, acc);
+    return;
+  }
   const int lane = threadIdx.x & 63;
   const int wm = c.wave >> 1, wn = c.wave & 1;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int64_t t = t0 + wn * 128 + j * 16 + (lane & 15);
     if (t >= p.T) continue;
-    const float e = F16 ? p.E[t] : 1.f;
+    const float e = p.E[t];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int64_t k = k0 + wm * 128 + i * 16 + 4 * (lane >> 4);
-      if (k >= p.K) continue;   // K is a multiple of 128
-      uint16_t h[4];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) h[v] = round16<F16>(acc[i][j][v] * e);
-      *reinterpret_cast<uint2*>(p.dX + t * p.K + k) =
-          make_uint2(uint32_t(h[0]) | uint32_t(h[1]) << 16, uint32_t(h[2]) | uint32_t(h[3]) << 16);
+      const int64_t k = o0 + wm * 128 + i * 16 + 4 * (lane >> 4);
+      if (k < p.K) store_dx<F16>(p, t, k, e, from_agpr(acc[i][j]));   // K is a multiple of 128
     }
   }
+}
+
+// Workgroup (cut tile, wave, block row i) adds the runs of 16 channels x 128 tokens.
+template <bool F16>
+__global__ __launch_bounds__(256) void w8_back_gemm_sum_kernel(const W8Back p, int tiles_t) {
+  const int cut = int(blockIdx.x), wave = int(blockIdx.y), i = int(blockIdx.z);
+  const int lane = threadIdx.x & 63, tile = p.cut.full + cut;
+  const int64_t t0 = int64_t(tile % tiles_t) * BN + (wave & 1) * 128 + (lane & 15);
+  const int64_t k = int64_t(tile / tiles_t) * BM + (wave >> 1) * 128 + i * 16 + 4 * (lane >> 4);
+  if (k >= p.K) return;
+#pragma unroll
+  for (int j = threadIdx.x >> 6; j < 8; j += 4) {
+    const int64_t t = t0 + j * 16;
+    if (t < p.T)
+      store_dx<F16>(p, t, k, p.E[t], w8_sum_runs<floatx4>(p.cut, cut, wave, i, j));
+  }
+}
+
+template <bool F16, bool GATED, int ACT>
+hipError_t launch_rows(const W8Back& p, hipStream_t st) {
+  const unsigned rows = unsigned(p.T);
+  // steps are 16-byte aligned where a row of 8 values takes them at once
+  const bool vec = p.N % 8 == 0 && p.N <= 32768 && p.vec;
+  if (!vec) w8_grad_rows_any_kernel<F16, GATED, ACT><<<rows, 256, 0, st>>>(p);
+  else if (p.N <= 2048) w8_grad_rows_kernel<F16, GATED, ACT, 1><<<rows, 256, 0, st>>>(p);
+  else if (p.N <= 8192) w8_grad_rows_kernel<F16, GATED, ACT, 2><<<rows, 512, 0, st>>>(p);
+  else if (p.N <= 16384) w8_grad_rows_kernel<F16, GATED, ACT, 2><<<rows, 1024, 0, st>>>(p);
+  else w8_grad_rows_kernel<F16, GATED, ACT, 4><<<rows, 1024, 0, st>>>(p);
+  return hipGetLastError();
 }
 
 template <bool F16>
 hipError_t launch_back(const W8Back& p, hipStream_t st) {
   const bool gated = p.G != nullptr;
   const int64_t C = (gated ? 2 : 1) * p.Np;
-  const unsigned rows = unsigned(p.T);
-  if (!gated) w8_grad_rows_kernel<F16, false, kSilu><<<rows, 256, 0, st>>>(p);
-  else if (p.act == kSilu) w8_grad_rows_kernel<F16, true, kSilu><<<rows, 256, 0, st>>>(p);
-  else w8_grad_rows_kernel<F16, true, kGelu><<<rows, 256, 0, st>>>(p);
-  hipError_t e = hipGetLastError();
+  hipError_t e = !gated             ? launch_rows<F16, false, kSilu>(p, st)
+                 : p.act == kSilu ? launch_rows<F16, true, kSilu>(p, st)
+                                  : launch_rows<F16, true, kGelu>(p, st);
   if (e != hipSuccess) return e;
+  if (p.few) return launch_w8_back_few(p, st);
   const dim3 grid(unsigned(p.Np / 64), unsigned(p.K / 64), gated ? 2 : 1);
-  w8_transpose_kernel<F16><<<grid, 256, 0, st>>>(p, C);
+  w8_transpose_kernel<<<grid, 256, 0, st>>>(p, C);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int tiles_t = int((p.T + BN - 1) / BN), tiles_k = int((p.K + BM - 1) / BM);
-  w8_back_gemm_kernel<F16><<<unsigned(gemm_blocks(tiles_t, tiles_k)), NT, 0, st>>>(p, C, tiles_t,
-                                                                                 tiles_k);
+  if (!p.cut.runs) {
+    w8_back_gemm_kernel<F16, false>
+        <<<unsigned(gemm_blocks(tiles_t, tiles_k)), NT, 0, st>>>(p, C, tiles_t, tiles_k);
+    return hipGetLastError();
+  }
+  const int cut = tiles_t * tiles_k - p.cut.full;
+  w8_back_gemm_kernel<F16, true>
+      <<<unsigned(p.cut.full + cut * p.cut.runs), NT, 0, st>>>(p, C, tiles_t, tiles_k);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  w8_back_gemm_sum_kernel<F16><<<dim3(unsigned(cut), 4, 8), 256, 0, st>>>(p, tiles_t);
   return hipGetLastError();
 }
 

@@ -51,10 +51,77 @@ __device__ __forceinline__ float widen16(uint16_t h) {
   return F16 ? f16_to_f32(h) : bf16_to_f32(h);
 }
 
+// Four consecutive 16-bit outputs from o; vec: whole and 8-byte aligned.
+template <bool F16>
+__device__ __forceinline__ void store4(uint16_t* p, bool vec, int64_t left, const float (&y)[4]) {
+  uint16_t h[4];
+#pragma unroll
+  for (int v = 0; v < 4; ++v) h[v] = round16<F16>(y[v]);
+  if (vec) {
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(uint32_t(h[0]) | uint32_t(h[1]) << 16, uint32_t(h[2]) | uint32_t(h[3]) << 16);
+    return;
+  }
+#pragma unroll
+  for (int v = 0; v < 4; ++v)
+    if (v < left) p[v] = h[v];
+}
+
 // A product from its exact sum: one rounding of the sum to float32 (2^-24),
 // then two float32 products.
 __device__ __forceinline__ float scaled(int sum, float xs, float w) {
   return (float(sum) * xs) * w;
+}
+
+// The channels' side of the outputs n .. n + 3 (of N): steps and bias.
+template <bool GATED>
+struct Channels {
+  float w[4], u[4], bias[4];
+};
+template <bool F16, bool GATED>
+__device__ __forceinline__ Channels<GATED> channels(const W8Product& p, int64_t n) {
+  Channels<GATED> c;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const int64_t i = n + v < p.N ? n + v : p.N - 1;
+    c.w[v] = p.w.steps[i];
+    c.u[v] = GATED ? p.u.steps[i] : 0.f;
+    c.bias[v] = !GATED && p.bias ? widen16<F16>(p.bias[i]) : 0.f;
+  }
+  return c;
+}
+
+// A tile's outputs: pointers at its first one, so that offsets within 256 rows of
+// N (below 2^23) fit 32 bits.
+struct Outputs {
+  uint16_t *Y, *G, *U;
+};
+__device__ __forceinline__ Outputs outputs_at(const W8Product& p, int64_t t, int64_t n) {
+  const int64_t o = t * p.N + n;
+  return {p.Y + o, p.G ? p.G + o : nullptr, p.G ? p.U + o : nullptr};
+}
+
+// Outputs o .. o + 3 from their sums (and the second layer's), `left` of them valid.
+template <bool F16, bool GATED, int ACT>
+__device__ __forceinline__ void finish4(const Outputs& out, const Channels<GATED>& c, float xs,
+                                        bool bias, uint32_t o, bool vec, int64_t left, intx4 s,
+                                        intx4 su) {
+  float y[4], u[4];
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    y[v] = scaled(s[v], xs, c.w[v]);
+    if constexpr (GATED) u[v] = scaled(su[v], xs, c.u[v]);
+    else if (bias) y[v] += c.bias[v];
+  }
+  if constexpr (GATED) {
+    if (out.G) {
+      store4<F16>(out.G + o, vec, left, y);
+      store4<F16>(out.U + o, vec, left, u);
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) y[v] = act_of<ACT>(y[v]) * u[v];
+  }
+  store4<F16>(out.Y + o, vec, left, y);
 }
 
 }  // namespace

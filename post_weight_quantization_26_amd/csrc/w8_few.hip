@@ -9,8 +9,6 @@
 // 128-byte block (the contraction's order is free as long as both operands
 // share it), so a wave's loads cover whole lines. Integer sums are exact, in
 // any order.
-#include <type_traits>
-
 #include "w8_common.h"
 
 namespace awq {
@@ -18,15 +16,20 @@ namespace {
 
 // Waves of a workgroup at most: their sums fit 64 KiB of LDS.
 constexpr int few_waves(int rb, int tb) { return 64 / (rb * tb) < 16 ? 64 / (rb * tb) : 16; }
-// 128-byte blocks of K loaded at once: 64 registers.
-constexpr int few_units(int rb, int tb) { return 8 / (rb + tb) < 1 ? 1 : 8 / (rb + tb); }
+#ifndef FEW_U
+#define FEW_U 4
+#endif
+constexpr int few_units(int rb, int tb) { return FEW_U / (rb + tb) < 1 ? 1 : FEW_U / (rb + tb); }
 
 template <bool F16, int RB, int TB, bool GATED, int ACT>
 __global__ __launch_bounds__(few_waves(RB, TB) * 64) void w8_few_kernel(const W8Product p) {
   static_assert(!GATED || RB % 2 == 0, "a pair takes blocks of both layers");
   constexpr int NB = GATED ? RB / 2 : RB;   // blocks of 16 output channels
   extern __shared__ int few_sums[];         // [waves][RB·TB][256]
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  // (a scalar: the matrix instructions ignore the execution mask, so what skips
+  // them has to be a branch)
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
   const int r = lane & 15, q = lane >> 4;
   const int64_t n0 = int64_t(blockIdx.x) * (16 * NB), t0 = int64_t(blockIdx.y) * (16 * TB);
   const int64_t K = p.K;
@@ -45,34 +48,47 @@ __global__ __launch_bounds__(few_waves(RB, TB) * 64) void w8_few_kernel(const W8
   }
   intx4 acc[RB][TB] = {};
   const int units = int(K >> 7);
-  const int u1 = int(int64_t(units) * (wave + 1) / waves);
-  int u = int(int64_t(units) * wave / waves);
-  auto step = [&](auto n) {
-    constexpr int U = decltype(n)::value;
+  const int u1 = units * (wave + 1) / waves;   // units < 1024
+  int u = units * wave / waves;
+  // U blocks of 128 bytes at a time, the next ones loaded before these are used
+  constexpr int U = few_units(RB, TB);
+  struct Batch {
     intx4 a[U][RB][2], b[U][TB][2];
+  };
+  auto load = [&](Batch& d, int at_unit) {
 #pragma unroll
-    for (int i = 0; i < U; ++i)
+    for (int i = 0; i < U; ++i) {
+      if (at_unit + i >= u1) break;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int64_t at = int64_t(u + i) * 128 + h * 16;
+        const int64_t at = int64_t(at_unit + i) * 128 + h * 16;
 #pragma unroll
-        for (int j = 0; j < RB; ++j) a[i][j][h] = *reinterpret_cast<const intx4*>(w[j] + at);
+        for (int j = 0; j < RB; ++j) d.a[i][j][h] = *reinterpret_cast<const intx4*>(w[j] + at);
 #pragma unroll
-        for (int j = 0; j < TB; ++j) b[i][j][h] = *reinterpret_cast<const intx4*>(x[j] + at);
+        for (int j = 0; j < TB; ++j) d.b[i][j][h] = *reinterpret_cast<const intx4*>(x[j] + at);
       }
+    }
+  };
+  auto use = [&](const Batch& d, int at_unit) {
 #pragma unroll
-    for (int i = 0; i < U; ++i)
+    for (int i = 0; i < U; ++i) {
+      if (at_unit + i >= u1) break;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int j = 0; j < RB; ++j)
 #pragma unroll
-          for (int k = 0; k < TB; ++k) acc[j][k] = mfma_16x16x64(a[i][j][h], b[i][k][h], acc[j][k]);
-    u += U;
+          for (int k = 0; k < TB; ++k) acc[j][k] = mfma_16x16x64(d.a[i][j][h], d.b[i][k][h], acc[j][k]);
+    }
   };
-  constexpr int U = few_units(RB, TB);
-  while (u + U <= u1) step(std::integral_constant<int, U>{});
-  while (u < u1) step(std::integral_constant<int, 1>{});
+  Batch d0, d1;
+  load(d0, u);
+  for (; u < u1; u += 2 * U) {
+    load(d1, u + U);
+    use(d0, u);
+    load(d0, u + 2 * U);
+    use(d1, u + U);
+  }
 
   // element (row 4q + v, token r) of a block at 16·r + 4q + v: a token's 16
   // channels are consecutive
@@ -116,7 +132,8 @@ hipError_t launch_few(const W8Product& p, hipStream_t st) {
   const int64_t units = p.K / 128;
   // 8 waves per CU or more where K has a block of 128 for each; the waves'
   // sums fit 64 KiB
-  int64_t waves = (2048 + blocks * tiles - 1) / (blocks * tiles);
+  static int tgt = getenv("FEW_W") ? atoi(getenv("FEW_W")) : 2048;
+  int64_t waves = (tgt + blocks * tiles - 1) / (blocks * tiles);
   if (waves < 4) waves = 4;
   if (waves > few_waves(RB, TB)) waves = few_waves(RB, TB);
   if (waves > units) waves = units;
@@ -128,6 +145,8 @@ hipError_t launch_few(const W8Product& p, hipStream_t st) {
 
 template <bool F16, bool GATED, int ACT>
 hipError_t launch_few_t(const W8Product& p, hipStream_t st) {
+  static int rb = getenv("FEW_RB") ? atoi(getenv("FEW_RB")) : 1;
+  if constexpr (!GATED) if (p.T <= 16 && rb == 1) return launch_few<F16, 1, 1, GATED, ACT>(p, st);
   if (p.T <= 16) return launch_few<F16, 2, 1, GATED, ACT>(p, st);
   if (p.T <= 32) return launch_few<F16, 2, 2, GATED, ACT>(p, st);
   return launch_few<F16, 4, 4, GATED, ACT>(p, st);

@@ -267,5 +267,5 @@ def test_reference_products():
             want = sum(int(i) * int(j) for i, j in zip(x[t], q[n])) * xs[t] * w[n] + b[n]
             assert abs(y[t, n] - want) <= 1e-12 * abs(want) and err[t, n] > 0
     d = rng.standard_normal((3, 5))
-    dx, _ = R.back_product([(d, np.zeros_like(d), q, w)], "bf16")
+    dx, _ = R.back_product([(d, np.zeros_like(d), q, w)])
     assert np.allclose(dx, (d * w) @ q)

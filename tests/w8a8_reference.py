@@ -121,23 +121,20 @@ def gated(g, eg, u, eu, kind):
     return h, np.abs(u) * ea + np.abs(a) * eu + 3 * U * np.abs(h) + ea * eu
 
 
-def back_product(pairs, dtype):
+def back_product(pairs):
     """Σ over (d, ed, q, w) of (d·w)·q and its error: d known within ed, d·w
-    rounded to float32 and to dtype (fp16: of a row whose largest lies in 2^13
-    to 2^14, a subnormal's half step is 2^-38 of it), float32 sums of C terms
-    whose tree is no deeper than C."""
-    h = half(dtype) + 2 * U
+    rounded to float32 and, scaled by a power of two per row that takes the
+    largest to 2^13 .. 2^14, to fp16 (2^-12 relative; a subnormal's half step,
+    2^-25, is 2^-38 of the largest), float32 sums of C terms whose tree is no
+    deeper than C."""
+    h = 2.0 ** -12 + 2 * U
     total, err, mag = 0.0, 0.0, 0.0
     C = sum(p[0].shape[1] for p in pairs) + 256
     top = np.max([np.abs(d * w).max(1) for d, _, _, w in pairs], axis=0)[:, None]
     for d, ed, q, w in pairs:
         q, w = np.asarray(q, np.float64), np.asarray(w, np.float64)
         total = total + (d * w) @ q
-        each = np.abs(d * w) * h + ed * np.abs(w)
-        if dtype == "f16":
-            each = each + 2.0 ** -38 * top
-        else:
-            each = each + floor(dtype)
+        each = np.abs(d * w) * h + ed * np.abs(w) + 2.0 ** -38 * top
         err = err + each @ np.abs(q)
         mag = mag + np.abs(d * w) @ np.abs(q)
     return total, err + C * U * (mag + err)
