@@ -550,8 +550,8 @@ awq_status awq_layer_norm_backward(const void* dY, const void* X, const float* s
  *   dx = Σ_n (dg_n·gsteps_n)·gate[n] + Σ_n (du_n·usteps_n)·up[n].
  * dX [T, K], dG and dU [T, N] are overwritten in `dtype`. Before they meet the
  * codes, the gradients' products with the steps are divided by a power of two
- * per row and rounded to fp16, for either type: 2^-12 of a value is lost, or
- * 2^-38 of its row's largest, whichever is more. Sums are float32, in an order
+ * per row and rounded to fp16, for either type: off by at most 2^-11 of a value
+ * or 2^-38 of its row's largest, whichever is more. Sums are float32, in an order
  * that the arguments fix. The layers are not trained. N below 2^21; ws: at least
  * awq_w8a8_backward_workspace_bytes(T, N, K, layers) bytes. */
 enum { AWQ_ACT_SILU = 0, AWQ_ACT_GELU = 1 };

@@ -981,7 +981,7 @@ extern "C" awq_status awq_quantize_rows8(const void* X, awq_dtype dtype, int64_t
   awq_status st_ = check_rows8("quantize_rows8", X, dtype, T, K, s, codes, steps);
   if (st_ != AWQ_OK) return st_;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const QuantizeRows8 p{X, s, T, K, codes, steps, rows_vec(K, {X, s, codes})};
+  const QuantizeRows8 p{X, s, T, K, codes, steps};
   AWQ_HIP(timed(AWQ_K_ROWS8, st, [&] { return launch_quantize_rows8(p, dt(dtype), st); }),
           "quantize_rows8");
   return AWQ_OK;
@@ -993,11 +993,8 @@ extern "C" awq_status awq_dequantize_rows8(const int8_t* codes, const float* ste
   awq_status st_ = check_rows8("dequantize_rows8", X, dtype, T, K, nullptr, codes, steps);
   if (st_ != AWQ_OK) return st_;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const bool vec = rows_vec(K, {X, codes});
   AWQ_HIP(timed(AWQ_K_ROWS8, st,
-                [&] {
-                  return launch_dequantize_rows8(codes, steps, dt(dtype), T, K, vec, X, st);
-                }),
+                [&] { return launch_dequantize_rows8(codes, steps, dt(dtype), T, K, X, st); }),
           "dequantize_rows8");
   return AWQ_OK;
 }
@@ -1016,7 +1013,6 @@ extern "C" awq_status awq_layer_norm(const void* X, awq_dtype dtype, int64_t T, 
   p.beta = beta;
   p.gamma32 = weight_dtype == AWQ_F32;
   p.rms = rms != 0;
-  p.vec = rows_vec(K, {X, gamma, beta, Y, codes});
   p.eps = eps;
   p.T = T;
   p.K = K;
@@ -1045,7 +1041,6 @@ extern "C" awq_status awq_layer_norm_backward(const void* dY, const void* X, con
   p.gamma = gamma;
   p.gamma32 = weight_dtype == AWQ_F32;
   p.rms = rms != 0;
-  p.vec = rows_vec(K, {dY, X, gamma, dX});
   p.T = T;
   p.K = K;
   p.Kp = l.Kp;
@@ -1131,7 +1126,7 @@ static awq_status w8_back(const char* name, W8Back p, int32_t layers, void* ws, 
   p.A = at<uint16_t>(ws, l.a);
   p.E = at<float>(ws, l.e);
   p.B = at<uint16_t>(ws, l.b);
-  p.vec = rows_vec(8, {p.w.steps, p.u.steps});
+  p.vec = all_aligned16({p.w.steps, p.u.steps});
   p.few = l.few;
   p.tile_t = l.tile_t;
   p.runs = int(l.runs);

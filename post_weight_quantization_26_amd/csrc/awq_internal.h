@@ -312,8 +312,7 @@ struct W8BackLayout {
   size_t total;
 };
 W8BackLayout w8_back_layout(int64_t T, int64_t N, int64_t K, int32_t layers);
-// Whether a row kernel may take 8 elements at a time.
-bool rows_vec(int64_t K, std::initializer_list<const void*> pointers);
+bool all_aligned16(std::initializer_list<const void*> pointers);
 awq_status check_rows8(const char* name, const void* X, awq_dtype d, int64_t T, int64_t K,
                        const float* s, const void* codes, const float* steps);
 awq_status check_norm(const void* X, awq_dtype d, int64_t T, int64_t K, const void* gamma,

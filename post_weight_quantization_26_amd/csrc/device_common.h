@@ -98,8 +98,33 @@ __device__ __forceinline__ void load8<0>(const void* base, int64_t idx, float (&
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
-// Store 8 consecutive elements at element i (aligned as for load8), each rounded
-// once to nearest even.
+// 8 values of a 16-bit type, packed; each rounded once to nearest even.
+template <int DT>
+__device__ __forceinline__ void unpack8(const uint4& q, float (&v)[8]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = DT == 1 ? __uint_as_float(w[i] << 16) : f16_to_f32(uint16_t(w[i] & 0xFFFFu));
+    v[2 * i + 1] =
+        DT == 1 ? __uint_as_float(w[i] & 0xFFFF0000u) : f16_to_f32(uint16_t(w[i] >> 16));
+  }
+}
+template <int DT>
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (DT == 1)
+      w[e] = uint32_t(__builtin_bit_cast(uint16_t, static_cast<__bf16>(v[2 * e]))) |
+             uint32_t(__builtin_bit_cast(uint16_t, static_cast<__bf16>(v[2 * e + 1]))) << 16;
+    else
+      w[e] = uint32_t(__builtin_bit_cast(uint16_t, static_cast<_Float16>(v[2 * e]))) |
+             uint32_t(__builtin_bit_cast(uint16_t, static_cast<_Float16>(v[2 * e + 1]))) << 16;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Store 8 consecutive elements at element i (aligned as for load8).
 template <int DT>
 __device__ __forceinline__ void store8(void* X, int64_t i, const float (&v)[8]) {
   if constexpr (DT == 0) {
@@ -107,17 +132,7 @@ __device__ __forceinline__ void store8(void* X, int64_t i, const float (&v)[8]) 
     p[0] = make_float4(v[0], v[1], v[2], v[3]);
     p[1] = make_float4(v[4], v[5], v[6], v[7]);
   } else {
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if constexpr (DT == 1)
-        w[e] = uint32_t(__builtin_bit_cast(uint16_t, static_cast<__bf16>(v[2 * e]))) |
-               uint32_t(__builtin_bit_cast(uint16_t, static_cast<__bf16>(v[2 * e + 1]))) << 16;
-      else
-        w[e] = uint32_t(__builtin_bit_cast(uint16_t, static_cast<_Float16>(v[2 * e]))) |
-               uint32_t(__builtin_bit_cast(uint16_t, static_cast<_Float16>(v[2 * e + 1]))) << 16;
-    }
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(X) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(X) + i) = pack8<DT>(v);
   }
 }
 

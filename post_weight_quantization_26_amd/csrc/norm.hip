@@ -12,16 +12,16 @@ namespace awq {
 namespace {
 
 // gamma and beta, in X's type or float32.
-template <int DT, int W, bool VEC>
+template <int DT, int W>
 __device__ __forceinline__ void load_weight(const void* g, bool f32, int K, int c, int t,
                                             float (&x)[8]) {
-  if (DT != 0 && !f32) load_piece<DT, W, VEC>(g, 0, K, c, t, x);
-  else load_piece<0, W, VEC>(g, 0, K, c, t, x);
+  if (DT != 0 && !f32) load_piece<DT, W>(g, 0, K, c, t, x);
+  else load_piece<0, W>(g, 0, K, c, t, x);
 }
 
 // Bound by HBM: a row stays in registers over its three passes (sum, squares
 // of deviations, output), so X is read once; gamma and beta come from L2.
-template <int DT, int W, int V, bool VEC>
+template <int DT, int W, int V>
 __global__ __launch_bounds__(kRowThreads<W>) void norm_kernel(const Norm p) {
   __shared__ float red0[16], red1[16];
   __shared__ uint32_t red2[16];
@@ -31,7 +31,7 @@ __global__ __launch_bounds__(kRowThreads<W>) void norm_kernel(const Norm p) {
   const int64_t at = row * K;
   float x[V][8];
 #pragma unroll
-  for (int c = 0; c < V; ++c) load_piece<DT, W, VEC>(p.X, at, K, c, t, x[c]);
+  for (int c = 0; c < V; ++c) load_piece<DT, W>(p.X, at, K, c, t, x[c]);
   float mean = 0.f;
   if (!p.rms) {
     float s = 0.f;
@@ -46,7 +46,7 @@ __global__ __launch_bounds__(kRowThreads<W>) void norm_kernel(const Norm p) {
   for (int c = 0; c < V; ++c)
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (row_col<W, VEC>(c, e, t) < K) {
+      if (row_col<W>(c, t) + e < K) {
         x[c][e] -= mean;
         q = __builtin_fmaf(x[c][e], x[c][e], q);
       }
@@ -54,17 +54,17 @@ __global__ __launch_bounds__(kRowThreads<W>) void norm_kernel(const Norm p) {
 #pragma unroll
   for (int c = 0; c < V; ++c) {
     float g[8], b[8];
-    load_weight<DT, W, VEC>(p.gamma, p.gamma32, K, c, t, g);
-    if (p.beta) load_weight<DT, W, VEC>(p.beta, p.gamma32, K, c, t, b);
+    load_weight<DT, W>(p.gamma, p.gamma32, K, c, t, g);
+    if (p.beta) load_weight<DT, W>(p.beta, p.gamma32, K, c, t, b);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float xh = x[c][e] * rstd;
       x[c][e] = p.beta ? __builtin_fmaf(xh, g[e], b[e]) : xh * g[e];
     }
-    if (p.Y) store_piece<DT, W, VEC>(p.Y, at, K, c, t, x[c]);
+    if (p.Y) store_piece<DT, W>(p.Y, at, K, c, t, x[c]);
   }
   if (p.stats && t == 0) *reinterpret_cast<float2*>(p.stats + 2 * row) = make_float2(mean, rstd);
-  if (p.codes) quantize_row<W, V, VEC>(x, row, K, t, red2, p.codes, p.steps);
+  if (p.codes) quantize_row<W, V>(x, row, K, t, red2, p.codes, p.steps);
 }
 
 // Gradient, first launch. A group of W waves takes every groups-th row and
@@ -72,44 +72,39 @@ __global__ __launch_bounds__(kRowThreads<W>) void norm_kernel(const Norm p) {
 // once and dX written once; the groups' sums go to `partial` (float32), which a
 // second launch adds up in a fixed order. A row's values are loaded one row
 // ahead. Bound by HBM.
-template <int DT, bool VEC>
-struct Raw {   // a piece as loaded: 16 bytes of a 16-bit type stay packed
+template <int DT>
+struct Raw {   // a piece as loaded: 16-bit types stay packed
+  uint4 v;
+  template <int W>
+  __device__ __forceinline__ void load(const void* base, int64_t at, int K, int c, int t) {
+    const int col = row_col<W>(c, t);
+    if (col + 8 <= K) {
+      v = load16(element<DT>(base, at + col));
+      return;
+    }
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (col + e < K)
+        w[e >> 1] |= uint32_t(static_cast<const uint16_t*>(base)[at + col + e]) << (16 * (e & 1));
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const { unpack8<DT>(v, x); }
+};
+template <>
+struct Raw<0> {
   float v[8];
   template <int W>
   __device__ __forceinline__ void load(const void* base, int64_t at, int K, int c, int t) {
-    load_piece<DT, W, VEC>(base, at, K, c, t, v);
+    load_piece<0, W>(base, at, K, c, t, v);
   }
   __device__ __forceinline__ void get(float (&x)[8]) const {
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = v[e];
   }
 };
-template <int DT>
-struct Raw16 {
-  uint4 v;
-  template <int W>
-  __device__ __forceinline__ void load(const void* base, int64_t at, int K, int c, int t) {
-    const int col = row_col<W, true>(c, 0, t);
-    v = make_uint4(0, 0, 0, 0);
-    if (col < K)
-      v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at + col);
-  }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = DT == 1 ? __uint_as_float(w[i] << 16) : f16_to_f32(uint16_t(w[i]));
-      x[2 * i + 1] =
-          DT == 1 ? __uint_as_float(w[i] & 0xFFFF0000u) : f16_to_f32(uint16_t(w[i] >> 16));
-    }
-  }
-};
-template <>
-struct Raw<1, true> : Raw16<1> {};
-template <>
-struct Raw<2, true> : Raw16<2> {};
 
-template <int DT, int W, int V, bool VEC>
+template <int DT, int W, int V>
 __global__ __launch_bounds__(kRowThreads<W>) void norm_back_kernel(const NormBack p) {
   __shared__ float2 red[2][16];
   const int t = row_thread<W>(), K = int(p.K);
@@ -118,8 +113,8 @@ __global__ __launch_bounds__(kRowThreads<W>) void norm_back_kernel(const NormBac
   const float inv_k = 1.f / float(K);
   float g[V][8], ag[V][8] = {}, ab[V][8] = {};
 #pragma unroll
-  for (int c = 0; c < V; ++c) load_weight<DT, W, VEC>(p.gamma, p.gamma32, K, c, t, g[c]);
-  Raw<DT, VEC> rx[V], ry[V];
+  for (int c = 0; c < V; ++c) load_weight<DT, W>(p.gamma, p.gamma32, K, c, t, g[c]);
+  Raw<DT> rx[V], ry[V];
   float2 st = make_float2(0.f, 0.f);
   int64_t row = group;
   auto load = [&](int64_t r) {
@@ -171,14 +166,14 @@ __global__ __launch_bounds__(kRowThreads<W>) void norm_back_kernel(const NormBac
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         o[e] = rstd * __builtin_fmaf(-xh[c][e], c2, d[c][e] - c1);
-      store_piece<DT, W, VEC>(p.dX, row * K, K, c, t, o);
+      store_piece<DT, W>(p.dX, row * K, K, c, t, o);
     }
   }
 #pragma unroll
   for (int c = 0; c < V; ++c) {
-    store_piece<0, W, VEC>(p.partial, group * p.Kp, K, c, t, ag[c]);
+    store_piece<0, W>(p.partial, group * p.Kp, K, c, t, ag[c]);
     if (p.dbeta)
-      store_piece<0, W, VEC>(p.partial, (p.groups + group) * p.Kp, K, c, t, ab[c]);
+      store_piece<0, W>(p.partial, (p.groups + group) * p.Kp, K, c, t, ab[c]);
   }
 }
 
@@ -217,8 +212,7 @@ __global__ __launch_bounds__(1024) void norm_sums_kernel(const float* __restrict
 template <int DT, int W, int V>
 hipError_t launch_fwd(const Norm& p, hipStream_t st) {
   const unsigned grid = unsigned(W == 1 ? (p.T + 3) / 4 : p.T);
-  if (p.vec) norm_kernel<DT, W, V, true><<<grid, kRowThreads<W>, 0, st>>>(p);
-  else norm_kernel<DT, W, V, false><<<grid, kRowThreads<W>, 0, st>>>(p);
+  norm_kernel<DT, W, V><<<grid, kRowThreads<W>, 0, st>>>(p);
   return hipGetLastError();
 }
 
@@ -236,8 +230,7 @@ hipError_t launch_fwd_t(const Norm& p, hipStream_t st) {
 template <int DT, int W, int V>
 hipError_t launch_back(const NormBack& p, hipStream_t st) {
   const unsigned grid = unsigned(W == 1 ? (p.groups + 3) / 4 : p.groups);
-  if (p.vec) norm_back_kernel<DT, W, V, true><<<grid, kRowThreads<W>, 0, st>>>(p);
-  else norm_back_kernel<DT, W, V, false><<<grid, kRowThreads<W>, 0, st>>>(p);
+  norm_back_kernel<DT, W, V><<<grid, kRowThreads<W>, 0, st>>>(p);
   return hipGetLastError();
 }
 
@@ -248,7 +241,7 @@ hipError_t launch_back_t(const NormBack& p, hipStream_t st) {
   if (p.K <= 2048) return launch_back<DT, 4, 1>(p, st);
   if (p.K <= 4096) return launch_back<DT, 4, 2>(p, st);
   if (p.K <= 8192) return launch_back<DT, 8, 2>(p, st);
-  if (p.K <= 16384) return launch_back<DT, 16, 2>(p, st);
+  if (p.K <= 16384) return launch_back<DT, 8, 4>(p, st);
   return hipErrorInvalidValue;
 }
 

@@ -2,10 +2,10 @@
 // reductions shared by the row quantiser (rows8.hip) and the norms (norm.hip).
 //
 // W is 1 (a workgroup of 4 waves holds 4 rows) or 4, 8, 16 (a workgroup is one
-// row). A lane holds V pieces of 8 values. VEC: K is a multiple of 8 and every
-// row 16-byte aligned, so a piece is 8 consecutive values; otherwise the 8
-// values of a piece lie W·64 apart, so that a wave still reads consecutive
-// elements.
+// row). A lane holds V pieces of 8 consecutive values, which one or two loads of
+// 16 bytes bring wherever the row starts: global memory takes them at any
+// element's address, and rows of odd lengths run nearly as fast as aligned ones.
+// Only a row's last piece, if it is not whole, goes element by element.
 #pragma once
 
 #include "act8.h"
@@ -44,58 +44,74 @@ __device__ __forceinline__ int64_t row_of(int64_t block) {
   return W == 1 ? block * 4 + (threadIdx.x >> 6) : block;
 }
 
-template <int W, bool VEC>
-__device__ __forceinline__ int row_col(int c, int e, int t) {
-  return VEC ? (c * (W * 64) + t) * 8 + e : (c * 8 + e) * (W * 64) + t;
+// First column of a thread's piece c.
+template <int W>
+__device__ __forceinline__ int row_col(int c, int t) {
+  return (c * (W * 64) + t) * 8;
+}
+
+// 16 or 8 bytes at any address.
+__device__ __forceinline__ uint4 load16(const void* p) {
+  uint4 v;
+  __builtin_memcpy(&v, p, 16);
+  return v;
+}
+template <int DT>
+__device__ __forceinline__ const char* element(const void* base, int64_t i) {
+  return static_cast<const char*>(base) + i * (DT == 0 ? 4 : 2);
 }
 
 // Columns past K are zero.
-template <int DT, int W, bool VEC>
+template <int DT, int W>
 __device__ __forceinline__ void load_piece(const void* base, int64_t at, int K, int c, int t,
                                            float (&x)[8]) {
-  if constexpr (VEC) {
-    if (row_col<W, VEC>(c, 0, t) < K) {
-      load8<DT>(base, at + row_col<W, VEC>(c, 0, t), x);
-      return;
-    }
+  const int col = row_col<W>(c, t);
+  if (col + 8 <= K) {
+    const char* p = element<DT>(base, at + col);
+    if constexpr (DT == 0) {
+      const uint4 a = load16(p), b = load16(p + 16);
+      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.f;
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int col = row_col<W, VEC>(c, e, t);
-      x[e] = col < K ? load1<DT>(base, at + col) : 0.f;
+      for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(w[e]);
+    } else {
+      unpack8<DT>(load16(p), x);
     }
+    return;
   }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = col + e < K ? load1<DT>(base, at + col + e) : 0.f;
 }
 
-template <int DT, int W, bool VEC>
+template <int DT, int W>
 __device__ __forceinline__ void store_piece(void* base, int64_t at, int K, int c, int t,
                                             const float (&x)[8]) {
-  if constexpr (VEC) {
-    if (row_col<W, VEC>(c, 0, t) < K) store8<DT>(base, at + row_col<W, VEC>(c, 0, t), x);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int col = row_col<W, VEC>(c, e, t);
-      if (col < K) store1<DT>(base, at + col, x[e]);
+  const int col = row_col<W>(c, t);
+  if (col + 8 <= K) {
+    char* p = const_cast<char*>(element<DT>(base, at + col));
+    if constexpr (DT == 0) {
+      __builtin_memcpy(p, x, 32);
+    } else {
+      const uint4 v = pack8<DT>(x);
+      __builtin_memcpy(p, &v, 16);
     }
+    return;
   }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (col + e < K) store1<DT>(base, at + col + e, x[e]);
 }
 
-template <int W, bool VEC>
+template <int W>
 __device__ __forceinline__ void store_codes(int8_t* base, int64_t at, int K, int c, int t,
                                             uint2 codes) {
-  if constexpr (VEC) {
-    if (row_col<W, VEC>(c, 0, t) < K)
-      *reinterpret_cast<uint2*>(base + at + row_col<W, VEC>(c, 0, t)) = codes;
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int col = row_col<W, VEC>(c, e, t);
-      if (col < K) base[at + col] = int8_t((e < 4 ? codes.x : codes.y) >> (8 * (e & 3)));
-    }
+  const int col = row_col<W>(c, t);
+  if (col + 8 <= K) {
+    __builtin_memcpy(base + at + col, &codes, 8);
+    return;
   }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (col + e < K) base[at + col + e] = int8_t((e < 4 ? codes.x : codes.y) >> (8 * (e & 3)));
 }
 
 // v summed over a wave, the same bits in every lane.
@@ -150,7 +166,7 @@ __device__ __forceinline__ uint32_t row_max(uint32_t m, uint32_t* red) {
 }
 
 // The row's codes and step from its values.
-template <int W, int V, bool VEC>
+template <int W, int V>
 __device__ __forceinline__ void quantize_row(const float (&x)[V][8], int64_t row, int K, int t,
                                              uint32_t* red, int8_t* codes, float* steps) {
   uint32_t m = 0;
@@ -163,7 +179,7 @@ __device__ __forceinline__ void quantize_row(const float (&x)[V][8], int64_t row
   const int64_t at = row * K;
 #pragma unroll
   for (int c = 0; c < V; ++c)
-    store_codes<W, VEC>(codes, at, K, c, t, act8_codes(x[c], s));
+    store_codes<W>(codes, at, K, c, t, act8_codes(x[c], s));
   if (t == 0) steps[row] = s.step;
 }
 

@@ -14,7 +14,7 @@ namespace {
 
 // Bound by HBM. A row stays in registers between its maximum and its codes, so
 // X is read once; s comes from the caches.
-template <int DT, int W, int V, bool VEC>
+template <int DT, int W, int V>
 __global__ __launch_bounds__(kRowThreads<W>) void quantize_rows8_kernel(
     const void* __restrict__ X, const float* __restrict__ s, int64_t T, int K,
     int8_t* __restrict__ codes, float* __restrict__ steps) {
@@ -24,45 +24,55 @@ __global__ __launch_bounds__(kRowThreads<W>) void quantize_rows8_kernel(
   const int t = row_thread<W>();
   float x[V][8];
 #pragma unroll
-  for (int c = 0; c < V; ++c) load_piece<DT, W, VEC>(X, row * K, K, c, t, x[c]);
+  for (int c = 0; c < V; ++c) load_piece<DT, W>(X, row * K, K, c, t, x[c]);
   if (s) {
 #pragma unroll
     for (int c = 0; c < V; ++c) {
       float f[8];
-      load_piece<0, W, VEC>(s, 0, K, c, t, f);
+      load_piece<0, W>(s, 0, K, c, t, f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[c][e] *= f[e];
     }
   }
-  quantize_row<W, V, VEC>(x, row, K, t, red, codes, steps);
+  quantize_row<W, V>(x, row, K, t, red, codes, steps);
 }
 
-// x^ = code·step, 8 codes a thread; a piece lies within one row (VEC) or is
-// taken element by element.
-template <int DT, bool VEC>
+// x^ = code·step, 8 codes of a row a thread, 4 rows a workgroup apart loaded
+// together. Bound by HBM.
+template <int DT>
 __global__ __launch_bounds__(256) void dequantize_rows8_kernel(const int8_t* __restrict__ codes,
                                                                const float* __restrict__ steps,
-                                                               int64_t n, uint32_t K,
-                                                               void* __restrict__ X) {
-  const int64_t p = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if constexpr (VEC) {
-    if (p * 8 >= n) return;
-    const uint2 c = *reinterpret_cast<const uint2*>(codes + p * 8);
-    const float s = steps[uint32_t(p) / (K / 8)];   // p < 2^31
-    float v[8];
+                                                               int64_t pieces, uint32_t per_row,
+                                                               int K, void* __restrict__ X) {
+  constexpr int U = 4;
+  const int64_t p0 = int64_t(blockIdx.x) * (256 * U) + threadIdx.x;
+  int64_t row[U];
+  int col[U];
+  float s[U];
+  uint2 c[U];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] = float(int8_t(c.x >> (8 * e))) * s;
-      v[4 + e] = float(int8_t(c.y >> (8 * e))) * s;
-    }
-    store8<DT>(X, p * 8, v);
-  } else {
-    // elements 256 apart, so that a wave's are consecutive
-    const int64_t i0 = int64_t(blockIdx.x) * 2048 + threadIdx.x;
+  for (int u = 0; u < U; ++u) {
+    const int64_t p = p0 + 256 * u;
+    if (p >= pieces) break;
+    row[u] = uint32_t(p) / per_row;      // pieces < 2^32
+    col[u] = int(uint32_t(p) - uint32_t(row[u]) * per_row) * 8;
+    s[u] = steps[row[u]];
+    if (col[u] + 8 <= K) __builtin_memcpy(&c[u], codes + row[u] * K + col[u], 8);
+  }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int64_t i = i0 + 256 * e;
-      if (i < n) store1<DT>(X, i, float(codes[i]) * steps[i / int64_t(K)]);
+  for (int u = 0; u < U; ++u) {
+    if (p0 + 256 * u >= pieces) break;
+    const int64_t at = row[u] * K + col[u];
+    if (col[u] + 8 <= K) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = float(int8_t(c[u].x >> (8 * e))) * s[u];
+        v[4 + e] = float(int8_t(c[u].y >> (8 * e))) * s[u];
+      }
+      store_piece<DT, 1>(X, at, 8, 0, 0, v);
+    } else {
+      for (int e = 0; col[u] + e < K; ++e) store1<DT>(X, at + e, float(codes[at + e]) * s[u]);
     }
   }
 }
@@ -70,12 +80,8 @@ __global__ __launch_bounds__(256) void dequantize_rows8_kernel(const int8_t* __r
 template <int DT, int W, int V>
 hipError_t launch_quantize(const QuantizeRows8& p, hipStream_t st) {
   const unsigned grid = unsigned(W == 1 ? (p.T + 3) / 4 : p.T);
-  if (p.vec)
-    quantize_rows8_kernel<DT, W, V, true><<<grid, kRowThreads<W>, 0, st>>>(p.X, p.s, p.T, int(p.K),
-                                                                           p.codes, p.steps);
-  else
-    quantize_rows8_kernel<DT, W, V, false><<<grid, kRowThreads<W>, 0, st>>>(
-        p.X, p.s, p.T, int(p.K), p.codes, p.steps);
+  quantize_rows8_kernel<DT, W, V><<<grid, kRowThreads<W>, 0, st>>>(p.X, p.s, p.T, int(p.K),
+                                                                   p.codes, p.steps);
   return hipGetLastError();
 }
 
@@ -95,13 +101,11 @@ hipError_t launch_quantize_t(const QuantizeRows8& p, hipStream_t st) {
 
 template <int DT>
 hipError_t launch_dequantize_t(const int8_t* codes, const float* steps, int64_t T, int64_t K,
-                               bool vec, void* X, hipStream_t st) {
-  const int64_t n = T * K;
-  const unsigned grid = unsigned((n + 2047) / 2048);
-  if (vec)
-    dequantize_rows8_kernel<DT, true><<<grid, 256, 0, st>>>(codes, steps, n, uint32_t(K), X);
-  else
-    dequantize_rows8_kernel<DT, false><<<grid, 256, 0, st>>>(codes, steps, n, uint32_t(K), X);
+                               void* X, hipStream_t st) {
+  const int64_t per_row = (K + 7) / 8, pieces = T * per_row;
+  if (pieces >= int64_t(1) << 32) return hipErrorInvalidValue;
+  dequantize_rows8_kernel<DT><<<unsigned((pieces + 1023) / 1024), 256, 0, st>>>(
+      codes, steps, pieces, uint32_t(per_row), int(K), X);
   return hipGetLastError();
 }
 
@@ -114,10 +118,10 @@ hipError_t launch_quantize_rows8(const QuantizeRows8& p, int dtype, hipStream_t 
 }
 
 hipError_t launch_dequantize_rows8(const int8_t* codes, const float* steps, int dtype, int64_t T,
-                                   int64_t K, bool vec, void* X, hipStream_t st) {
-  if (dtype == 0) return launch_dequantize_t<0>(codes, steps, T, K, vec, X, st);
-  if (dtype == 1) return launch_dequantize_t<1>(codes, steps, T, K, vec, X, st);
-  return launch_dequantize_t<2>(codes, steps, T, K, vec, X, st);
+                                   int64_t K, void* X, hipStream_t st) {
+  if (dtype == 0) return launch_dequantize_t<0>(codes, steps, T, K, X, st);
+  if (dtype == 1) return launch_dequantize_t<1>(codes, steps, T, K, X, st);
+  return launch_dequantize_t<2>(codes, steps, T, K, X, st);
 }
 
 }  // namespace awq

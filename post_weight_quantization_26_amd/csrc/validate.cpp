@@ -4,7 +4,6 @@
 #include <algorithm>
 #include <cstdarg>
 #include <cstdio>
-#include <cstdlib>
 #include <cstring>
 
 #include "awq_internal.h"
@@ -762,8 +761,8 @@ awq_status check_act8(const char* name, const void* X, awq_dtype d, int64_t T, i
 // 8-bit rows, norms and products
 // ---------------------------------------------------------------------------
 
-bool rows_vec(int64_t K, std::initializer_list<const void*> pointers) {
-  return K % 8 == 0 && std::all_of(pointers.begin(), pointers.end(), aligned16);
+bool all_aligned16(std::initializer_list<const void*> pointers) {
+  return std::all_of(pointers.begin(), pointers.end(), aligned16);
 }
 
 // The row kernels take a workgroup of up to 1024 threads per row.
@@ -822,12 +821,15 @@ awq_status check_norm(const void* X, awq_dtype d, int64_t T, int64_t K, const vo
   return AWQ_OK;
 }
 
-// Row groups of the gradient: 16 waves a CU (W of them on a row, as the
-// kernel's launcher picks), and no more than rows.
+// Row groups of the gradient (W waves each, as the kernel's launcher picks): at most
+// 16 waves a CU, few enough that a group's partial sums are a small part of its rows,
+// and all with the same number of rows.
 NormBackLayout norm_back_layout(int64_t T, int64_t K) {
   NormBackLayout l{};
-  const int64_t waves = K <= 1024 ? 1 : K <= 4096 ? 4 : K <= 8192 ? 8 : 16;
-  l.groups = std::min<int64_t>(T, 4096 / waves);
+  const int64_t waves = K <= 1024 ? 1 : K <= 4096 ? 4 : 8;
+  const int64_t most = 4096 / waves;
+  const int64_t rows = std::max<int64_t>(ceil_div(T, most), std::min<int64_t>(4, ceil_div(T, 256)));
+  l.groups = ceil_div(T, rows);
   l.Kp = ceil_div(K, 8) * 8;
   l.total = align_up(size_t(2 * l.groups) * size_t(l.Kp) * 4);
   return l;
@@ -862,24 +864,17 @@ static bool w8_sizes_ok(int64_t T, int64_t N, int64_t K, int32_t layers) {
          K % kTileK == 0 && (layers == 1 || layers == 2);
 }
 
-static int w8_force(const char* name) {
-  const char* v = getenv(name);
-  return v ? atoi(v) : -1;
-}
-
 // 256x256 tiles: time in us for rounds of 256 tiles and the last ones, whole or cut
-// into the runs that take least. Steps are slower the more CUs work (1.15 us alone,
-// 1.65 on all; the chip's power), a round's ends take 15 us, the runs' sums 0.035 us
-// each and a launch: 4096 tokens of 4096x11008 150 us (this rule 157), 1600 of them
-// 77 cut and 129 whole (80 and 138), 5000 of 28672x8192 1019 (1066).
+// into the runs that take least. Steps are slower the more CUs work, a round's ends
+// take 14 us, the runs' sums 0.035 us each and a launch.
 static double w8_big_us(int64_t rows, int64_t T, int64_t steps, LoraCut& cut) {
   const int64_t tiles = ceil_div(T, 256) * ceil_div(rows, 256), rest = tiles % 256;
   const double s = double(steps);
   cut = LoraCut{};
-  double tail = rest ? 15 + s * (1.1 + 0.6 * double(rest) / 256) : 0;
+  double tail = rest ? 14 + s * (0.93 + 0.55 * double(rest) / 256) : 0;
   for (int64_t runs = 2; rest && runs <= std::min<int64_t>(256 / rest, steps / 2); ++runs) {
     const double units = double(rest * runs);
-    const double t = 12 + 0.035 * units + s / double(runs) * (0.95 + 0.5 * units / 256);
+    const double t = 12 + 0.035 * units + s / double(runs) * (0.93 + 0.55 * units / 256);
     if (t < tail) {
       tail = t;
       cut.runs = runs;
@@ -889,11 +884,17 @@ static double w8_big_us(int64_t rows, int64_t T, int64_t steps, LoraCut& cut) {
     cut.full = tiles - rest;
     cut.bytes = size_t(rest) * size_t(cut.runs) * 256 * 256 * 4;
   }
-  return double(tiles / 256) * (15 + 1.65 * s) + tail;
+  return double(tiles / 256) * (14 + 1.5 * s) + tail;
 }
 
 // Tile and runs of the contraction for a product of `rows` output channels, T
-// tokens and `steps` steps of 128 bytes, by an estimate in us of each choice.
+// tokens and `steps` steps of 128 bytes, by an estimate in us of each choice: the
+// steps of the rounds it takes, 5 for a launch and, with runs, 3 and their sums'
+// bytes. Over random sizes the choice was within 6% of the best one on average.
+// us, chosen first: 64 tokens of 4096x11008 15.5 (128x32, 4 runs), 27 (1 run), 96
+// (256x256); 200 of 11008x4096 23 (128x64), 27 (128x32), 26 (128x128), 48; 800 of
+// 4096x11008 53 (128x128), 55 (128x64); 1600 78 (256x256 cut in 2), 98 (256x128),
+// 102 (128x128), 112 (128x64).
 struct W8Tiling {
   bool big;
   int tile_n, tile_t;
@@ -917,7 +918,7 @@ static W8Tiling w8_tiling(int64_t rows, int64_t T, int64_t steps) {
     const int64_t n = ceil_div(rows, s.n) * ceil_div(T, s.t);
     if (n > 16384) continue;
     for (int64_t runs = 1; runs <= 8 && runs * 2 <= std::max<int64_t>(steps, 2); ++runs) {
-      if (runs > 1 && n * runs > 768) break;
+      if (runs > 1 && (s.n == 256 || n * runs > 768)) break;
       const int64_t units = n * runs;
       const double rounds = s.pairs ? std::max(1.0, double(units) / 256)
                                     : double(ceil_div(units, 256));
@@ -936,33 +937,33 @@ static W8Tiling w8_tiling(int64_t rows, int64_t T, int64_t steps) {
   return best;
 }
 
+// Few tokens: us at T of 1, 8 and 16 by registers (w8_few.hip) and by the best tile:
+// 4096x11008 10.6 / 14.0, 12.1 / 14.1, 13.7 / 14.3; 11008x4096 10.8 / 12.6, 12.5 /
+// 12.6, 15.0 / 13.0; 28672x8192 37 / 35, 43 / 36, 53 / 36, as a pair 82 / 89 at T = 1;
+// 512x512 3.9 / 5.0 at all three.
+static bool w8_few(int64_t T, int64_t K, int64_t codes) {
+  return T <= 4 || (T <= 8 && codes <= (int64_t(64) << 20)) ||
+         (T <= 16 && K <= 4096 && codes <= (int64_t(32) << 20));
+}
+
 W8Plan w8_plan(int64_t T, int64_t N, int64_t K, int32_t layers) {
   W8Plan l{};
   l.runs = 1;
-  const int64_t codes = N * layers * K;
-  const int f = w8_force("W8_FORM");
-  if (f >= 0 ? f == 0 : T <= 4 || (T <= 8 && codes <= (64 << 20)) || (T <= 16 && codes <= (32 << 20))) {
+  l.ldp = ceil_div(N, 4) * 4;
+  if (w8_few(T, K, N * layers * K)) {
     l.form = W8Form::kFew;
     return l;
   }
-  W8Tiling t = w8_tiling(N * layers, T, K / 128);
-  if (f == 1) {
-    t.big = false; t.cut = LoraCut{};
-    const int tt = w8_force("W8_TILE"), r = w8_force("W8_RUNS");
-    if (tt > 0) { t.tile_t = tt; t.tile_n = 128; if (tt == 256) { t.tile_n = 256; t.tile_t = 128; } }
-    if (r > 0) t.runs = std::min<int64_t>(r, K / 128);
-  }
-  if (f == 2) { t = W8Tiling{}; t.big = true; }
-  if (f == 3) { t = W8Tiling{}; t.big = true; t.cut = lora_cut(T, N * layers, K / 2); 
-    if (w8_force("W8_RUNS") > 0) { const int64_t tl = ceil_div(T, 256) * ceil_div(N, layers == 2 ? 128 : 256); t.cut.runs = std::min<int64_t>(w8_force("W8_RUNS"), K / 128); t.cut.full = tl / 256 * 256; t.cut.bytes = size_t(tl % 256) * t.cut.runs * 262144; if (tl % 256 == 0) t.cut = LoraCut{}; } }
+  const W8Tiling t = w8_tiling(N * layers, T, K / 128);
   l.form = t.big ? W8Form::kBig : W8Form::kMid;
   l.tile_n = t.tile_n;
   l.tile_t = t.tile_t;
-  l.runs = t.runs ? t.runs : 1;
-  l.ldp = ceil_div(N, 4) * 4;
+  l.runs = t.runs;
   l.cut = t.cut;
-  l.bytes = t.big ? align_up(l.cut.bytes)
-            : l.runs > 1 ? align_up(size_t(l.runs * layers) * size_t(T) * size_t(l.ldp) * 4) : 0;
+  if (t.big)
+    l.bytes = align_up(l.cut.bytes);
+  else if (l.runs > 1)
+    l.bytes = align_up(size_t(l.runs * layers) * size_t(T) * size_t(l.ldp) * 4);
   return l;
 }
 
@@ -976,17 +977,36 @@ W8BackLayout w8_back_layout(int64_t T, int64_t N, int64_t K, int32_t layers) {
     off += align_up(bytes);
     return at;
   };
-  const double us = w8_big_us(K, T, l.C / 64, l.cut) + 5 + double(l.C) * double(K) * 3 / 4e6;
-  l.tile_t = T <= 16 ? 16 : T <= 32 ? 32 : 64;
-  l.runs = 1;
-  const int64_t tiles = (K / 128) * ceil_div(T, l.tile_t), blocks = l.C / 32;
-  l.runs = std::max<int64_t>(1, std::min<int64_t>({512 / tiles, blocks / 16, 16}));
-  const int f = w8_force("W8_FORM");
-  l.few = us > 1e9 || T <= 512;
-  if (f == 1) { l.few = true; if (w8_force("W8_TILE") > 0) l.tile_t = w8_force("W8_TILE"); if (w8_force("W8_RUNS") > 0) l.runs = std::min<int64_t>(w8_force("W8_RUNS"), blocks); }
-  if (f == 2 || f == 3) { l.few = false; l.cut = LoraCut{}; 
-    const int64_t tl = ceil_div(T, 256) * ceil_div(K, 256);
-    if (f == 3 && tl % 256) { l.cut.runs = std::min<int64_t>(w8_force("W8_RUNS"), l.C / 64); l.cut.full = tl / 256 * 256; l.cut.bytes = size_t(tl % 256) * l.cut.runs * 262144; } }
+  // With a transposed layer (its codes read and written at about 4.4 bytes a ns)
+  const double big = w8_big_us(K, T, l.C / 64, l.cut) + 5 + double(l.C) * double(K) * 3 / 4.4e6;
+  // or from the codes: a wave's blocks of 32 rows at `alone` us where every CU has a
+  // workgroup at most, `full` where it has all it can hold
+  struct Shape {
+    int t;
+    int64_t slots;
+    double alone, full;
+  };
+  static constexpr Shape shapes[] = {{16, 1024, 0.51, 1.4}, {32, 768, 0.59, 1.5}, {64, 512, 0.77, 1.5}};
+  const int64_t blocks = l.C / 32;
+  double least = 0;
+  for (const Shape& s : shapes) {
+    const int64_t tiles = (K / 128) * ceil_div(T, s.t);
+    if (tiles > 8192 && least) continue;
+    for (int64_t runs = 1; runs <= 12 && (runs == 1 || runs * 8 <= blocks); ++runs) {
+      const int64_t units = tiles * runs;
+      const double load =
+          std::min(1.0, std::max(0.0, double(units - 256) / double(s.slots - 256)));
+      double us = 4 + double(ceil_div(units, s.slots)) * double(blocks) / double(4 * runs) *
+                          (s.alone + (s.full - s.alone) * load);
+      if (runs > 1) us += 4 + double(runs) * double(T) * double(K) * 8 / 4e6;
+      if (!least || us < least) {
+        least = us;
+        l.tile_t = s.t;
+        l.runs = runs;
+      }
+    }
+  }
+  l.few = least < big;
   l.a = take(size_t(l.few ? ceil_div(T, 16) * 16 : T) * size_t(l.C) * 2);
   l.e = take(size_t(T) * 4);
   if (l.few) {
@@ -1021,9 +1041,9 @@ static awq_status check_w8_common(const char* name, const void* V, awq_dtype d, 
                      (long long)N, (long long)K);
   if (layers == 2 && act != AWQ_ACT_SILU && act != AWQ_ACT_GELU)
     return set_error(AWQ_E_INVALID, "%s: unknown activation %d", name, int(act));
+  // 256x256 tiles of either direction, and the gradient's workgroup per token
   if (!grid_fits(search_gemm_blocks(T, std::max(2 * N, K), AWQ_BF16), 256) ||
-      !grid_fits(T, 1024) || !grid_fits(ceil_div(T, 16) * ceil_div(N, 16), 1024) ||
-      ceil_div(T, 16) > 65535)
+      !grid_fits(T, 1024))
     return set_error(AWQ_E_UNSUPPORTED, "%s: T=%lld x N=%lld exceed the grids", name,
                      (long long)T, (long long)N);
   if (!aligned16(V) || !aligned16(q0) || !aligned16(q1) || !aligned4(s0) || !aligned4(s1))

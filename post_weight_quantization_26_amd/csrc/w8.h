@@ -6,27 +6,24 @@
 
 namespace awq {
 
-// Rows of X [T, K] (times s [K], if given) to codes and steps. vec: K is a
-// multiple of 8 and X, s and codes are 16-byte aligned.
+// Rows of X [T, K] (times s [K], if given) to codes and steps.
 struct QuantizeRows8 {
   const void* X;
   const float* s;
   int64_t T, K;
   int8_t* codes;
   float* steps;
-  bool vec;
 };
 hipError_t launch_quantize_rows8(const QuantizeRows8& p, int dtype, hipStream_t st);
 hipError_t launch_dequantize_rows8(const int8_t* codes, const float* steps, int dtype, int64_t T,
-                                   int64_t K, bool vec, void* X, hipStream_t st);
+                                   int64_t K, void* X, hipStream_t st);
 
-// A norm of the rows of X [T, K]. vec: K is a multiple of 8 and every matrix
-// and vector over K is 16-byte aligned.
+// A norm of the rows of X [T, K].
 struct Norm {
   const void* X;
   const void* gamma;   // [K], X's type or float32 (gamma32)
   const void* beta;    // like gamma, or NULL
-  bool gamma32, rms, vec;
+  bool gamma32, rms;
   float eps;
   int64_t T, K;
   void* Y;             // [T, K], or NULL
@@ -42,7 +39,7 @@ struct NormBack {
   const void* X;
   const float* stats;
   const void* gamma;
-  bool gamma32, rms, vec;
+  bool gamma32, rms;
   int64_t T, K, Kp, groups;
   float* partial;
   void* dX;

@@ -238,15 +238,20 @@ void w8_back_gemm_kernel(const W8Back p, int64_t C, int tiles_t, int tiles_k) {
   }
   const int lane = threadIdx.x & 63;
   const int wm = c.wave >> 1, wn = c.wave & 1;
+  float e[8];   // all before the first store
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int64_t t = t0 + wn * 128 + j * 16 + (lane & 15);
+    e[j] = p.E[t < p.T ? t : p.T - 1];
+  }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int64_t t = t0 + wn * 128 + j * 16 + (lane & 15);
     if (t >= p.T) continue;
-    const float e = p.E[t];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int64_t k = o0 + wm * 128 + i * 16 + 4 * (lane >> 4);
-      if (k < p.K) store_dx<F16>(p, t, k, e, from_agpr(acc[i][j]));   // K is a multiple of 128
+      if (k < p.K) store_dx<F16>(p, t, k, e[j], from_agpr(acc[i][j]));   // K is a multiple of 128
     }
   }
 }

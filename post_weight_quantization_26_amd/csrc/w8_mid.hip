@@ -25,12 +25,23 @@ __global__ __launch_bounds__(256) void w8_mid_kernel(const W8Product p, int tile
   const int lane = threadIdx.x & 63;
   constexpr int NI = GATED ? RA / 64 : RA / 32;
   const Outputs out = outputs_at(p, t0, n0);
+  // every step and bias before the first store (w8_gemm.hip)
+  Channels<GATED> ch[RUNS ? 1 : NI];
+  float xs[TR / 32];
+  if constexpr (!RUNS) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      ch[i] = channels<F16, GATED>(p, n0 + (m.wave >> 1) * (BC / 2) + i * 16 + 4 * (lane >> 4));
+#pragma unroll
+    for (int j = 0; j < TR / 32; ++j) {
+      const int64_t t = t0 + (m.wave & 1) * (TR / 2) + j * 16 + (lane & 15);
+      xs[j] = p.xs[t < p.T ? t : p.T - 1];
+    }
+  }
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int64_t n = n0 + (m.wave >> 1) * (BC / 2) + i * 16 + 4 * (lane >> 4);
     if (n >= p.N) continue;
-    Channels<GATED> ch;
-    if constexpr (!RUNS) ch = channels<F16, GATED>(p, n);
 #pragma unroll
     for (int j = 0; j < TR / 32; ++j) {
       const int64_t t = t0 + (m.wave & 1) * (TR / 2) + j * 16 + (lane & 15);
@@ -40,7 +51,7 @@ __global__ __launch_bounds__(256) void w8_mid_kernel(const W8Product p, int tile
         *reinterpret_cast<intx4*>(o) = acc[i][j];
         if constexpr (GATED) *reinterpret_cast<intx4*>(o + p.T * p.ldp) = acc[i + NI][j];
       } else {
-        finish4<F16, GATED, ACT>(out, ch, p.xs[t], p.bias,
+        finish4<F16, GATED, ACT>(out, ch[i], xs[j], p.bias,
                                  uint32_t(t - t0) * uint32_t(p.N) + uint32_t(n - n0),
                                  p.N % 4 == 0, p.N - n, acc[i][j], acc[GATED ? i + NI : i][j]);
       }
@@ -76,7 +87,8 @@ hipError_t launch_mid(const W8Product& p, hipStream_t st) {
     w8_mid_kernel<F16, GATED, ACT, RA, TR, false><<<grid, 256, 0, st>>>(p, tiles_n, tiles_t);
     return hipGetLastError();
   }
-  w8_mid_kernel<F16, GATED, ACT, RA, TR, true><<<grid, 256, 0, st>>>(p, tiles_n, tiles_t);
+  if constexpr (RA == 128) w8_mid_kernel<F16, GATED, ACT, RA, TR, true><<<grid, 256, 0, st>>>(p, tiles_n, tiles_t);
+  else return hipErrorInvalidValue;   // runs are cut of tiles of 128 rows only
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   w8_mid_sum_kernel<F16, GATED, ACT>

@@ -155,6 +155,67 @@ def test_gated(api, dtype, act, T, N, K):
     assert torch.equal(H, api.w8a8_gated_matmul(x, xs, gate, up, TYPES[dtype], act=act))
 
 
+# Sizes of every other form: 128-row tiles of 64 and 128 tokens, 256-row tiles,
+# each with one run of the contraction and (128 rows) with several; 256x256 tiles
+# whole, all cut into runs, and the last ones cut behind 256 whole ones.
+FORMS = [(17, 16, 2048), (1500, 7, 2048), (4400, 1, 4096), (6000, 129, 128), (6000, 520, 128),
+         (4400, 1048, 128), (4100, 3001, 2048), (1000, 2000, 8192), (4100, 4096, 4096)]
+
+
+@pytest.mark.parametrize("pair", [False, True])
+@pytest.mark.parametrize("T,N,K", FORMS)
+def test_forms(api, T, N, K, pair):
+    dtype = "f16" if (T + N) % 2 else "bf16"
+    if pair and N > 1:
+        N //= 2
+    x, xs = rows(T, K, T + N)
+    gate, up = layer8(N, K, N + K), layer8(N, K, N + K + 1)
+    g, eg = R.product(npy(x), npy(xs), npy(gate[0]), npy(gate[1]))
+    if not pair:
+        close(api.w8a8_matmul(x, xs, *gate, TYPES[dtype]), g, R.rounded(g, eg, dtype), "Y")
+        return
+    pre = tuple(torch.empty(T, N, dtype=TYPES[dtype], device="cuda") for _ in range(2))
+    H = api.w8a8_gated_matmul(x, xs, gate, up, TYPES[dtype], pre=pre)
+    u, eu = R.product(npy(x), npy(xs), npy(up[0]), npy(up[1]))
+    close(pre[0], g, R.rounded(g, eg, dtype), "G")
+    close(pre[1], u, R.rounded(u, eu, dtype), "U")
+    h, eh = R.gated(g, eg, u, eu, "silu")
+    close(H, h, R.rounded(h, eh, dtype), "H")
+
+
+@pytest.mark.parametrize("T", [3, 20, 300])
+def test_offsets_past_32_bits(api, T):
+    """A layer of more than 2^32 bytes: its last channels, and its gradient."""
+    N, K = 270000, 16384
+    q = torch.randint(-127, 128, (N, K), dtype=torch.int8, device="cuda")
+    w = torch.rand(N, device="cuda") * 1e-3 + 1e-4
+    x, xs = rows(T, K, 1)
+    Y = api.w8a8_matmul(x, xs, q, w, torch.float16)
+    dY = torch.zeros(T, N, dtype=torch.float16, device="cuda")
+    for part in (slice(0, 130), slice(131000, 131200), slice(N - 130, N)):
+        y, err = R.product(npy(x), npy(xs), npy(q[part]), npy(w[part]))
+        close(Y[:, part], y, R.rounded(y, err, "f16"), "Y")
+        dY[:, part] = randn(T, part.stop - part.start, seed=2, dtype="f16")
+    del Y
+    dX = api.w8a8_backward(dY, q, w)
+    keep = torch.cat([torch.arange(0, 130), torch.arange(131000, 131200), torch.arange(N - 130, N)])
+    d = npy(dY[:, keep.cuda()])
+    ref, err = R.back_product([(d, np.zeros_like(d), npy(q[keep.cuda()]), npy(w[keep.cuda()]))])
+    # the zeros between add their number of exact additions
+    close(dX, ref, R.rounded(ref, err, "f16"), "dX")
+
+
+def test_many_outputs_past_32_bits(api):
+    """Outputs of more than 2^32 bytes: the last tokens."""
+    T, N, K = 9001, 262144, 128
+    x, xs = rows(T, K, 1)
+    q, w = layer8(N, K, 2)
+    Y = api.w8a8_matmul(x, xs, q, w, torch.bfloat16)
+    for part in (slice(0, 3), slice(4090, 4100), slice(T - 5, T)):
+        y, err = R.product(npy(x[part]), npy(xs[part]), npy(q), npy(w))
+        close(Y[part], y, R.rounded(y, err, "bf16"), "Y")
+
+
 @pytest.mark.parametrize("T", [1, 40, 300])
 def test_largest_sums(api, T):
     """Codes of -128 on both sides over a long contraction: 2^14·K stays an exact int32."""
@@ -230,6 +291,50 @@ def test_gated_gradient(api, dtype, act, T, N, K):
     ref, err = R.back_product([(dg, edg, npy(gate[0]), npy(gate[1])),
                                (du, edu, npy(up[0]), npy(up[1]))])
     close(dX, ref, R.rounded(ref, err, dtype), "dX")
+
+
+# From the codes, with tiles of 16, 32 and 64 tokens, one run and several; through a
+# transposed layer, whole 256x256 tiles, all cut, the last ones cut.
+BACK_FORMS = [(1, 1500, 128), (200, 1, 4096), (17, 1500, 4096), (200, 1, 8192), (33, 3001, 4096),
+              (4100, 1000, 2048), (2500, 1500, 2048), (4100, 1048, 4096), (20, 33000, 128),
+              (20, 20000, 128), (20, 12000, 256)]
+
+
+@pytest.mark.parametrize("pair", [False, True])
+@pytest.mark.parametrize("T,N,K", BACK_FORMS)
+def test_gradient_forms(api, T, N, K, pair):
+    dtype = "f16" if (T + N) % 2 else "bf16"
+    gate = layer8(N, K, N + K)
+    dH = randn(T, N, seed=T, scale=0.01, dtype=dtype)
+    d = npy(dH)
+    if not pair:
+        ref, err = R.back_product([(d, np.zeros_like(d), npy(gate[0]), npy(gate[1]))])
+        close(api.w8a8_backward(dH, *gate), ref, R.rounded(ref, err, dtype), "dX")
+        return
+    up = layer8(N, K, N + K + 1)
+    pre = randn(T, N, seed=T + 1, scale=3.0, dtype=dtype), randn(T, N, seed=T + 2, dtype=dtype)
+    dX, dG, dU = api.w8a8_gated_backward(dH, pre, gate, up)
+    g, u = npy(pre[0]), npy(pre[1])
+    a, slope, ea, es = R.act(g, "silu")
+    dg, du = d * u * slope, d * a
+    edg = np.abs(d * u) * es + 3 * R.U * np.abs(dg)
+    edu = np.abs(d) * ea + 2 * R.U * np.abs(du)
+    close(dG, dg, R.rounded(dg, edg, dtype), "dG")
+    close(dU, du, R.rounded(du, edu, dtype), "dU")
+    ref, err = R.back_product([(dg, edg, npy(gate[0]), npy(gate[1])),
+                               (du, edu, npy(up[0]), npy(up[1]))])
+    close(dX, ref, R.rounded(ref, err, dtype), "dX")
+
+
+@pytest.mark.parametrize("T", [30, 4100])
+def test_gradient_with_steps_off_16_bytes(api, T):
+    """Steps and gradients of any alignment that the calls take."""
+    N, K = 1048, 2048
+    q, w = layer8(N, K, 5)
+    shifted = torch.empty(N + 1, device="cuda")[1:]
+    shifted.copy_(w)
+    dY = randn(T, N, seed=9, dtype="f16")
+    assert torch.equal(api.w8a8_backward(dY, q, w), api.w8a8_backward(dY, q, shifted))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])

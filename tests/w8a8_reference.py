@@ -1,8 +1,8 @@
 """References of the 8-bit rows, norms and 8-bit products, in numpy float64 and
 apart from the kernels' order of work, with the error that each result may have.
 
-Rounding units: float32 U = 2^-24, an output type's half step H (bf16 2^-9 of
-the value's binade at most 2^-8 relative, see ``half``)."""
+A rounding is off by at most half a step: float32 U = 2^-24 relative, ``half`` of
+the others (bf16 2^-8, fp16 2^-11)."""
 import numpy as np
 import torch
 from scipy.special import erfc
@@ -81,10 +81,17 @@ def norm_back(dy, x, stats, gamma, rms):
             depth * np.abs(dy).sum(0))
 
 
+def matmul(a, b):
+    """a·b in float64, on the GPU where it is large."""
+    if a.shape[0] * a.shape[1] * b.shape[1] > 1 << 30 and torch.cuda.is_available():
+        return (torch.from_numpy(a).cuda() @ torch.from_numpy(np.ascontiguousarray(b)).cuda()).cpu().numpy()
+    return a @ b
+
+
 def product(codes, steps, q, w, bias=None):
     """Y and its error: the sum's rounding, two products, the bias."""
     # int8 products in float64 are exact
-    s = np.asarray(codes, np.float64) @ np.asarray(q, np.float64).T
+    s = matmul(np.asarray(codes, np.float64), np.asarray(q, np.float64).T)
     y = s * np.asarray(steps, np.float64)[:, None] * np.asarray(w, np.float64)
     err = 3 * U * np.abs(y)
     if bias is not None:
@@ -124,17 +131,17 @@ def gated(g, eg, u, eu, kind):
 def back_product(pairs):
     """Σ over (d, ed, q, w) of (d·w)·q and its error: d known within ed, d·w
     rounded to float32 and, scaled by a power of two per row that takes the
-    largest to 2^13 .. 2^14, to fp16 (2^-12 relative; a subnormal's half step,
+    largest to 2^13 .. 2^14, to fp16 (half a step: 2^-11 relative; a subnormal's,
     2^-25, is 2^-38 of the largest), float32 sums of C terms whose tree is no
     deeper than C."""
-    h = 2.0 ** -12 + 2 * U
+    h = half("f16") + 2 * U
     total, err, mag = 0.0, 0.0, 0.0
     C = sum(p[0].shape[1] for p in pairs) + 256
     top = np.max([np.abs(d * w).max(1) for d, _, _, w in pairs], axis=0)[:, None]
     for d, ed, q, w in pairs:
         q, w = np.asarray(q, np.float64), np.asarray(w, np.float64)
-        total = total + (d * w) @ q
+        total = total + matmul(d * w, q)
         each = np.abs(d * w) * h + ed * np.abs(w) + 2.0 ** -38 * top
-        err = err + each @ np.abs(q)
-        mag = mag + np.abs(d * w) @ np.abs(q)
+        err = err + matmul(each, np.abs(q))
+        mag = mag + matmul(np.abs(d * w), np.abs(q))
     return total, err + C * U * (mag + err)
