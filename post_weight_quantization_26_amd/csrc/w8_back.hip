@@ -9,7 +9,7 @@
 // the codes are exact fp16 numbers. A pair's two sums are one contraction of
 // twice the length. fp16 for bf16 gradients too: it keeps 3 bits more, and a
 // power of two per row takes the place of bf16's range. Launch 1 forms A; then
-//  * many tokens: launch 2 writes the codes' transpose as fp16 operand rows [K, C]
+//  * many tokens: launch 2 writes the codes' transpose as the fp16 operand of [K, C]
 //    and launch 3 is the 256x256 main loop of gemm_core.h;
 //  * fewer: w8_back_few.hip takes the codes as they are.
 #include "w8_cut.h"
@@ -60,11 +60,11 @@ __device__ __forceinline__ uint32_t block_max(uint32_t m) {
   return r;
 }
 
-// A's element (t, c), c over the layers' Np each: rows [T, C], or, for few tokens,
-// in the order of that kernel's operand: blocks of 32 c x 16 tokens, a lane's 8
-// consecutive c together.
-__device__ __forceinline__ int64_t operand_at(const W8Back& p, int64_t t, int64_t c, int64_t C) {
-  if (!p.few) return t * C + c;
+// A's element (t, c), c over the layers' Np each: panels of 64 c (w8_cut.h), or, for
+// few tokens, the order of that kernel's operand: blocks of 32 c x 16 tokens, a
+// lane's 8 consecutive c together.
+__device__ __forceinline__ int64_t operand_at(const W8Back& p, int64_t t, int64_t c) {
+  if (!p.few) return ((c >> 6) * p.T + t) * 64 + (c & 63);
   const int64_t tb = (p.T + 15) >> 4;
   return (((c >> 5) * tb + (t >> 4)) * 64 + ((c >> 3) & 3) * 16 + (t & 15)) * 8 + (c & 7);
 }
@@ -73,7 +73,7 @@ __device__ __forceinline__ int64_t operand_at(const W8Back& p, int64_t t, int64_
 // dY, G and U are read once. N a multiple of 8, at most 8·V·blockDim. Bound by HBM.
 template <bool F16, bool GATED, int ACT, int V>
 __global__ __launch_bounds__(1024) void w8_grad_rows_kernel(const W8Back p) {
-  const int64_t t = blockIdx.x, C = (GATED ? 2 : 1) * p.Np;
+  const int64_t t = blockIdx.x;
   const int n8 = int(p.N >> 3);
   const int64_t row = t * p.N;
   uint4 rd[V], rg[V], ru[V];
@@ -130,7 +130,7 @@ __global__ __launch_bounds__(1024) void w8_grad_rows_kernel(const W8Back p) {
     float s[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) s[k] = v[k] * down;
-    store8<2>(p.A, operand_at(p, t, c, C), s);
+    store8<2>(p.A, operand_at(p, t, c), s);
   };
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -143,15 +143,15 @@ __global__ __launch_bounds__(1024) void w8_grad_rows_kernel(const W8Back p) {
   const int pad = int((p.Np - p.N) >> 3);
   const float zero[8] = {};
   if (int(threadIdx.x) < pad) {
-    store8<2>(p.A, operand_at(p, t, p.N + threadIdx.x * 8, C), zero);
-    if constexpr (GATED) store8<2>(p.A, operand_at(p, t, p.Np + p.N + threadIdx.x * 8, C), zero);
+    store8<2>(p.A, operand_at(p, t, p.N + threadIdx.x * 8), zero);
+    if constexpr (GATED) store8<2>(p.A, operand_at(p, t, p.Np + p.N + threadIdx.x * 8), zero);
   }
 }
 
 // The same for any N, element by element in two passes.
 template <bool F16, bool GATED, int ACT>
 __global__ __launch_bounds__(256) void w8_grad_rows_any_kernel(const W8Back p) {
-  const int64_t t = blockIdx.x, C = (GATED ? 2 : 1) * p.Np;
+  const int64_t t = blockIdx.x;
   const int64_t row = t * p.N;
   auto values = [&](int64_t n, float& a, float& b, float& dg, float& du) {
     back_values<GATED, ACT>(widen16<F16>(p.dY[row + n]), GATED ? widen16<F16>(p.G[row + n]) : 0.f,
@@ -178,13 +178,14 @@ __global__ __launch_bounds__(256) void w8_grad_rows_any_kernel(const W8Back p) {
         p.dU[row + n] = round16<F16>(du);
       }
     }
-    p.A[operand_at(p, t, n, C)] = round16<true>(a * down);
-    if constexpr (GATED) p.A[operand_at(p, t, p.Np + n, C)] = round16<true>(b * down);
+    p.A[operand_at(p, t, n)] = round16<true>(a * down);
+    if constexpr (GATED) p.A[operand_at(p, t, p.Np + n)] = round16<true>(b * down);
   }
 }
 
-// B: 64 x 64 codes through LDS, as fp16 numbers. grid (Np / 64, K / 64, layers).
-__global__ __launch_bounds__(256) void w8_transpose_kernel(const W8Back p, int64_t C) {
+// B in panels: 64 x 64 codes through LDS, as fp16 numbers, 8 KiB in one piece. grid
+// (Np / 64, K / 64, layers).
+__global__ __launch_bounds__(256) void w8_transpose_kernel(const W8Back p) {
   __shared__ uint32_t tile[64][17];   // [n][k / 4]
   const int64_t n0 = int64_t(blockIdx.x) * 64, k0 = int64_t(blockIdx.y) * 64;
   const int8_t* q = blockIdx.z ? p.u.q : p.w.q;
@@ -203,7 +204,8 @@ __global__ __launch_bounds__(256) void w8_transpose_kernel(const W8Back p, int64
   for (int i = 0; i < 8; ++i)
     h[i] = codes_to_f16(tile[nn + 2 * i][k >> 2], tile[nn + 2 * i + 1][k >> 2],
                         byte_pair(0) + 0x00010001u * (k & 3));
-  uint4* o = reinterpret_cast<uint4*>(p.B + (k0 + k) * C + int64_t(blockIdx.z) * p.Np + n0 + nn);
+  const int64_t panel = int64_t(blockIdx.z) * (p.Np >> 6) + blockIdx.x;
+  uint4* o = reinterpret_cast<uint4*>(p.B + (panel * p.K + k0 + k) * 64 + nn);
   o[0] = make_uint4(h[0], h[1], h[2], h[3]);
   o[1] = make_uint4(h[4], h[5], h[6], h[7]);
 }
@@ -220,49 +222,53 @@ __device__ __forceinline__ void store_dx(const W8Back& p, int64_t t, int64_t k, 
 // consecutive ones of a token. Bound by the matrix cores.
 template <bool F16, bool CUT>
 __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1)))
-void w8_back_gemm_kernel(const W8Back p, int64_t C, int tiles_t, int tiles_k) {
-  W8Unit unit;
-  if (!w8_unit<CUT>(p.cut, tiles_t, tiles_k, unit)) return;
+void w8_back_gemm_kernel(const W8Back p, int steps, int tiles_t, int tiles_k) {
+  const W8Unit unit = w8_unit<CUT>(p.cut, tiles_t, tiles_k);
   const int64_t t0 = int64_t(unit.tt) * BN, o0 = int64_t(unit.tn) * BM;
   const int64_t rows_o = p.K - o0 < BM ? p.K - o0 : BM;
   const int64_t rows_t = p.T - t0 < BN ? p.T - t0 : BN;
-  int64_t c0 = 0, c1 = C;
-  if constexpr (CUT) w8_run(p.cut, unit, int(C / BK64), c0, c1);
-  GemmCtx64 c;
-  w8_setup(c, p.B + o0 * C + c0, rows_o, p.A + t0 * C + c0, rows_t, C, c1 - c0);
+  int k0 = 0, k1 = steps;
+  if constexpr (CUT) w8_run(p.cut, unit, steps, k0, k1);
+  const int64_t step_a = p.K * 64, step_b = p.T * 64;
+  PanelCtx c;
+  panel_setup(c, p.B + k0 * step_a + o0 * 64, rows_o, step_a, p.A + k0 * step_b + t0 * 64, rows_t,
+              step_b, k1 - k0);
   floatx4 acc[8][8];
-  gemm_mainloop16<true>(c, acc);
+  gemm_mainloop16_of<f16x8_t>(c, acc);
   if (CUT && unit.slot >= 0) {
     w8_store_run(p.cut, unit, c.wave, acc);
     return;
   }
   const int lane = threadIdx.x & 63;
   const int wm = c.wave >> 1, wn = c.wave & 1;
-  float e[8];   // all before the first store
+  const int64_t tw = t0 + wn * 128, ow = o0 + wm * 128;
+  const int left_t = int(rows_t) - wn * 128;
+  if (left_t <= 0 || ow >= p.K) return;   // K is a multiple of 128
+  const WaveTile<128> tile(c.wave);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const int64_t t = t0 + wn * 128 + j * 16 + (lane & 15);
-    e[j] = p.E[t < p.T ? t : p.T - 1];
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int64_t t = t0 + wn * 128 + j * 16 + (lane & 15);
-    if (t >= p.T) continue;
+    const int t = j * 16 + (lane & 15);
+    const float e = p.E[tw + (t < left_t ? t : left_t - 1)];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int64_t k = o0 + wm * 128 + i * 16 + 4 * (lane >> 4);
-      if (k < p.K) store_dx<F16>(p, t, k, e[j], from_agpr(acc[i][j]));   // K is a multiple of 128
+      const floatx4 s = from_agpr(acc[i][j]);
+      const float y[4] = {s[0] * e, s[1] * e, s[2] * e, s[3] * e};
+      tile.template put<F16>(t, i * 16 + 4 * (lane >> 4), y);
     }
   }
+  tile.store(p.dX + tw * p.K + ow, uint32_t(p.K), left_t, 128);
 }
 
 // Workgroup (cut tile, wave, block row i) adds the runs of 16 channels x 128 tokens.
 template <bool F16>
-__global__ __launch_bounds__(256) void w8_back_gemm_sum_kernel(const W8Back p, int tiles_t) {
+__global__ __launch_bounds__(256) void w8_back_gemm_sum_kernel(const W8Back p, int tiles_t,
+                                                               int tiles_k) {
   const int cut = int(blockIdx.x), wave = int(blockIdx.y), i = int(blockIdx.z);
   const int lane = threadIdx.x & 63, tile = p.cut.full + cut;
-  const int64_t t0 = int64_t(tile % tiles_t) * BN + (wave & 1) * 128 + (lane & 15);
-  const int64_t k = int64_t(tile / tiles_t) * BM + (wave >> 1) * 128 + i * 16 + 4 * (lane >> 4);
+  int tt, tk;
+  w8_tile(tile, tiles_t, tiles_k, tt, tk);
+  const int64_t t0 = int64_t(tt) * BN + (wave & 1) * 128 + (lane & 15);
+  const int64_t k = int64_t(tk) * BM + (wave >> 1) * 128 + i * 16 + 4 * (lane >> 4);
   if (k >= p.K) return;
 #pragma unroll
   for (int j = threadIdx.x >> 6; j < 8; j += 4) {
@@ -288,28 +294,28 @@ hipError_t launch_rows(const W8Back& p, hipStream_t st) {
 template <bool F16>
 hipError_t launch_back(const W8Back& p, hipStream_t st) {
   const bool gated = p.G != nullptr;
-  const int64_t C = (gated ? 2 : 1) * p.Np;
+  const int steps = int((gated ? 2 : 1) * p.Np / 64);
   hipError_t e = !gated             ? launch_rows<F16, false, kSilu>(p, st)
                  : p.act == kSilu ? launch_rows<F16, true, kSilu>(p, st)
                                   : launch_rows<F16, true, kGelu>(p, st);
   if (e != hipSuccess) return e;
   if (p.few) return launch_w8_back_few(p, st);
   const dim3 grid(unsigned(p.Np / 64), unsigned(p.K / 64), gated ? 2 : 1);
-  w8_transpose_kernel<<<grid, 256, 0, st>>>(p, C);
+  w8_transpose_kernel<<<grid, 256, 0, st>>>(p);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int tiles_t = int((p.T + BN - 1) / BN), tiles_k = int((p.K + BM - 1) / BM);
   if (!p.cut.runs) {
     w8_back_gemm_kernel<F16, false>
-        <<<unsigned(gemm_blocks(tiles_t, tiles_k)), NT, 0, st>>>(p, C, tiles_t, tiles_k);
+        <<<unsigned(tiles_t * tiles_k), NT, 0, st>>>(p, steps, tiles_t, tiles_k);
     return hipGetLastError();
   }
   const int cut = tiles_t * tiles_k - p.cut.full;
   w8_back_gemm_kernel<F16, true>
-      <<<unsigned(p.cut.full + cut * p.cut.runs), NT, 0, st>>>(p, C, tiles_t, tiles_k);
+      <<<unsigned(p.cut.full + cut * p.cut.runs), NT, 0, st>>>(p, steps, tiles_t, tiles_k);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  w8_back_gemm_sum_kernel<F16><<<dim3(unsigned(cut), 4, 8), 256, 0, st>>>(p, tiles_t);
+  w8_back_gemm_sum_kernel<F16><<<dim3(unsigned(cut), 4, 8), 256, 0, st>>>(p, tiles_t, tiles_k);
   return hipGetLastError();
 }
 

@@ -10,6 +10,29 @@
 namespace awq {
 namespace {
 
+// Operands in panels: 64 consecutive elements of every row (one k-tile), then the
+// next 64. A tile's k-tile is 32 KiB in one piece, where long rows take a page or
+// two for each: 4096 tokens of a pair of 11008 (rows of 44 KB) 634 -> 576 us, one of
+// 11008 (22 KB) 274 -> 277.
+struct PanelCtx {
+  const uint16_t *A, *B;        // the tile's first rows in the first panel
+  int64_t step_a, step_b;       // elements of a panel
+  int bytes_a, bytes_b;         // of the tile's valid rows in a panel
+  int v[2];                     // the lane's byte offset in copy 0, for even and odd copies
+  int wave, KT;
+  template <int S>
+  __device__ __forceinline__ void copy(int kt, int q) const {
+    // copy q of the 16 a wave issues per k-tile: rows 8·(q % 8) on of A for q < 8, then B
+    const int j = q & 7, k = kt < KT ? kt : 0, past = kt < KT ? 0 : BM * 128;
+    const uint16_t* base = q < 8 ? A + k * step_a : B + k * step_b;
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint16_t*>(base), 0, q < 8 ? bytes_a : bytes_b, 0x00020000);
+    uint4* to = (q < 8 ? stage64_a<S>() : stage64_b<S>()) + (wave * 8 + j) * 64;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, AWQ_LDS(to), 16, v[j & 1] + past + j * 1024, 0, 0,
+                                             0);
+  }
+};
+
 // The main loop's context with everything that the compiler has to know to be
 // uniform said so: else every copy is a loop over the lanes' resources (4096
 // tokens of 4096x11008: 165 instead of 150 us).
@@ -27,43 +50,75 @@ __device__ __forceinline__ void w8_setup(GemmCtx64& c, const uint16_t* A, int64_
                __builtin_amdgcn_readfirstlane(int(rows_b)), ld, k, false);
   c.KT = __builtin_amdgcn_readfirstlane(c.KT);
 }
+__device__ __forceinline__ void panel_setup(PanelCtx& c, const uint16_t* A, int64_t rows_a,
+                                            int64_t step_a, const uint16_t* B, int64_t rows_b,
+                                            int64_t step_b, int steps) {
+  c.A = uniform(A);
+  c.B = uniform(B);
+  c.step_a = step_a;
+  c.step_b = step_b;
+  c.bytes_a = __builtin_amdgcn_readfirstlane(int(rows_a)) * 128;
+  c.bytes_b = __builtin_amdgcn_readfirstlane(int(rows_b)) * 128;
+  c.wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+  c.KT = __builtin_amdgcn_readfirstlane(steps);
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int row = c.wave * 64 + 8 * j + (lane >> 3);
+    c.v[j] = (row - 8 * j) * 128 + ((lane & 7) ^ ((row >> 1) & 7)) * 16;
+  }
+}
 
 // A workgroup's tile and, of a cut one, its run (slot >= 0).
 struct W8Unit {
   int tt, tn, run, slot;
 };
 
-// Token tile fastest; XCD i takes a contiguous run of the whole tiles, and of the
-// (tile, run) units behind them. False for padding.
+// Tile number -> (token tile, channel tile): groups of at most 6 token tiles, in each
+// the channel tiles one after the other with the group's token tiles fastest.
+__device__ __forceinline__ void w8_tile(int tile, int tiles_t, int tiles_n, int& tt, int& tn) {
+  const int groups = (tiles_t + 5) / 6, size = (tiles_t + groups - 1) / groups;
+  const int g = tile / (size * tiles_n), rest = tile - g * size * tiles_n;
+  const int mine = tiles_t - g * size < size ? tiles_t - g * size : size;
+  tn = rest / mine;
+  tt = g * size + rest - tn * mine;
+}
+
+// Number i of n in the order that gives each XCD (consecutive workgroups go round
+// them) a contiguous run of numbers: its 32 CUs work on about 5 x 6 neighbouring
+// tiles, so their L2 holds what they share.
+__device__ __forceinline__ int w8_of_xcd(int i, int n) {
+  const int q = n / 8, rem = n % 8, x = i % 8;
+  return x * q + (x < rem ? x : rem) + i / 8;
+}
+
 template <bool CUT>
-__device__ __forceinline__ bool w8_unit(const W8Cut& cut, int tiles_t, int tiles_n, W8Unit& u) {
+__device__ __forceinline__ W8Unit w8_unit(const W8Cut& cut, int tiles_t, int tiles_n) {
+  W8Unit u;
   u.run = 0;
   u.slot = -1;
+  int tile;
   if constexpr (CUT) {
-    int tile;
     const int id = int(blockIdx.x);
     if (id < cut.full) {
-      tile = (id % 8) * (cut.full / 8) + id / 8;
+      tile = w8_of_xcd(id, cut.full);
     } else {
-      const int v = id - cut.full, units = int(gridDim.x) - cut.full, q = units / 8,
-                rem = units % 8, x = v % 8;
-      u.slot = x * q + (x < rem ? x : rem) + v / 8;
+      u.slot = w8_of_xcd(id - cut.full, int(gridDim.x) - cut.full);
       tile = cut.full + u.slot / cut.runs;
       u.run = u.slot % cut.runs;
     }
-    u.tt = tile % tiles_t;
-    u.tn = tile / tiles_t;
   } else {
-    if (!tile_of(blockIdx.x, tiles_t, tiles_n, u.tt, u.tn)) return false;
+    tile = w8_of_xcd(int(blockIdx.x), int(gridDim.x));
   }
-  return true;
+  w8_tile(tile, tiles_t, tiles_n, u.tt, u.tn);
+  return u;
 }
 
-// First and last + 1 of a run's elements among `steps` 64-wide k-tiles.
-__device__ __forceinline__ void w8_run(const W8Cut& cut, const W8Unit& u, int steps, int64_t& k0,
-                                       int64_t& k1) {
-  k0 = u.slot < 0 ? 0 : int64_t(steps) * u.run / cut.runs * BK64;
-  k1 = u.slot < 0 ? int64_t(steps) * BK64 : int64_t(steps) * (u.run + 1) / cut.runs * BK64;
+// First and last + 1 of a run's k-tiles, of `steps`.
+__device__ __forceinline__ void w8_run(const W8Cut& cut, const W8Unit& u, int steps, int& k0,
+                                       int& k1) {
+  k0 = u.slot < 0 ? 0 : steps * u.run / cut.runs;   // both below 2^15
+  k1 = u.slot < 0 ? steps : steps * (u.run + 1) / cut.runs;
 }
 
 // Keeps an accumulator in its AGPRs up to this use: with two ways out of a kernel
@@ -95,6 +150,50 @@ __device__ __forceinline__ V w8_sum_runs(const W8Cut& cut, int tile, int wave, i
   for (int r = 1; r < cut.runs; ++r) s += src[int64_t(r) * 4 * 4096];
   return s;
 }
+
+// A wave's outputs, 128 tokens x COLS channels of 16 bits, through its quarter of
+// the main loop's LDS: lanes hold 4 channels of a token, rows of 16 tokens; the
+// stores take 16 bytes a lane and whole lines. (With 8-byte stores of 16 tokens each a
+// round of 256 tiles of K = 2048 took 42 us, with these 33.) 16-byte chunks are XORed
+// with the row, so that 16 lanes write or read distinct banks.
+template <int COLS>
+struct WaveTile {
+  static constexpr int kChunks = COLS / 8;
+  uint4* lds;
+  __device__ __forceinline__ WaveTile(int wave)
+      : lds(wave == 0 ? s64A0 : wave == 1 ? s64A1 : wave == 2 ? s64B0 : s64B1) {}
+  __device__ __forceinline__ uint4* at(int t, int chunk) const {
+    return lds + t * kChunks + (chunk ^ (COLS == 64 ? (t >> 1) & 7 : t & 15));
+  }
+  // channels n .. n + 3 (a multiple of 4) of token t
+  template <bool F16>
+  __device__ __forceinline__ void put(int t, int n, const float (&y)[4]) const {
+    uint32_t h[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) h[v] = round16<F16>(y[v]);
+    reinterpret_cast<uint2*>(at(t, n >> 3))[(n >> 2) & 1] =
+        make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+  }
+  // To out, rows of ld elements: the first left_t tokens and left_n channels.
+  __device__ __forceinline__ void store(uint16_t* out, uint32_t ld, int left_t, int left_n) const {
+    const int lane = threadIdx.x & 63, n = lane % kChunks * 8;
+#pragma unroll
+    for (int i = 0; i < 128 * kChunks / 64; ++i) {
+      const int t = i * (64 / kChunks) + lane / kChunks;
+      const uint4 v = *at(t, lane % kChunks);
+      if (t >= left_t || n >= left_n) continue;
+      uint16_t* o = out + (uint32_t(t) * ld + uint32_t(n));
+      if (n + 8 <= left_n) {
+        __builtin_memcpy(o, &v, 16);   // rows of any length: at any element's address
+        continue;
+      }
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 7; ++e)
+        if (n + e < left_n) o[e] = uint16_t(e & 1 ? w[e >> 1] >> 16 : w[e >> 1]);
+    }
+  }
+};
 
 }  // namespace
 }  // namespace awq

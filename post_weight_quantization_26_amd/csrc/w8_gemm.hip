@@ -16,12 +16,12 @@ template <bool F16, bool GATED, int ACT, bool CUT>
 __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void w8_gemm_kernel(const W8Product p, int tiles_t, int tiles_n) {
   constexpr int BC = GATED ? BM / 2 : BM;   // output channels of a tile
-  W8Unit unit;
-  if (!w8_unit<CUT>(p.cut, tiles_t, tiles_n, unit)) return;
+  const W8Unit unit = w8_unit<CUT>(p.cut, tiles_t, tiles_n);
   const int64_t t0 = int64_t(unit.tt) * BN, n0 = int64_t(unit.tn) * BC;
   const int64_t ld = p.K / 2;               // codes in pairs
-  int64_t k0 = 0, k1 = ld;
-  if constexpr (CUT) w8_run(p.cut, unit, int(ld / BK64), k0, k1);
+  int kt0 = 0, kt1 = int(ld / BK64);
+  if constexpr (CUT) w8_run(p.cut, unit, kt1, kt0, kt1);
+  const int64_t k0 = int64_t(kt0) * BK64, k1 = int64_t(kt1) * BK64;
   const uint16_t* x = reinterpret_cast<const uint16_t*>(p.x) + t0 * ld + k0;
   const int64_t rows_t = p.T - t0 < BN ? p.T - t0 : BN;
   GemmCtx64 c;
@@ -45,52 +45,69 @@ void w8_gemm_kernel(const W8Product p, int tiles_t, int tiles_n) {
   floatx4 acc[8][8];
   gemm_mainloop16_of<i8x16_t>(c, acc);
 
-  if (CUT && unit.slot >= 0) {
-    w8_store_run(p.cut, unit, c.wave, acc);
-    return;
-  }
   const int lane = threadIdx.x & 63;
   const int wm = c.wave >> 1, wn = c.wave & 1;
-  constexpr int NI = GATED ? 4 : 8;
-  const bool whole = p.N % 4 == 0;          // every row of Y is 8-byte aligned
-  const Outputs out = outputs_at(p, t0, n0);
-  const int left_t = int(rows_t), left_n = int(p.N - n0 < BC ? p.N - n0 : BC);
-  const uint32_t N = uint32_t(p.N);
+  constexpr int NI = GATED ? 4 : 8, COLS = BC / 2;
+  const int64_t tw = t0 + wn * 128, nw = n0 + wm * COLS;   // the wave's first
+  const int left_t = int(rows_t) - wn * 128, left_n = int(p.N - nw < COLS ? p.N - nw : COLS);
   // every step and bias first: the compiler does not move a load over a store, and
   // one load's latency for each of the 64 blocks took 20 us
   Channels<GATED> ch[NI];
   float xs[8];
 #pragma unroll
-  for (int i = 0; i < NI; ++i)
-    ch[i] = channels<F16, GATED>(p, n0 + wm * (BC / 2) + i * 16 + 4 * (lane >> 4));
+  for (int i = 0; i < NI; ++i) ch[i] = channels<F16, GATED>(p, nw + i * 16 + 4 * (lane >> 4));
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const int t = wn * 128 + j * 16 + (lane & 15);
-    xs[j] = p.xs[t0 + (t < left_t ? t : left_t - 1)];
+    const int64_t t = tw + j * 16 + (lane & 15);
+    xs[j] = p.xs[t < p.T ? t : p.T - 1];
   }
+  const WaveTile<COLS> tile(c.wave);
+  const int64_t first = tw * p.N + nw;
+  const bool bias = p.bias;
+  // a pair's passes: G and U, if they are kept, then H; none for a run of a cut tile
+  // (one way out: with a branch around the passes the compiler spilled)
+#pragma unroll 1
+  for (int pass = CUT && unit.slot >= 0 ? 3 : GATED && p.G ? 0 : 2; pass < 3; ++pass) {
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int n = wm * (BC / 2) + i * 16 + 4 * (lane >> 4);
-    if (n >= left_n) continue;
+    for (int i = 0; i < NI; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int t = wn * 128 + j * 16 + (lane & 15);
-      if (t < left_t)
-        finish4<F16, GATED, ACT>(out, ch[i], xs[j], p.bias, uint32_t(t) * N + uint32_t(n), whole,
-                                 left_n - n, __builtin_bit_cast(intx4, from_agpr(acc[i][j])),
-                                 __builtin_bit_cast(intx4, from_agpr(acc[GATED ? i + 4 : i][j])));
-    }
+      for (int j = 0; j < 8; ++j) {
+        const intx4 s = __builtin_bit_cast(intx4, from_agpr(acc[i][j]));
+        float y[4];
+        if constexpr (GATED) {
+          const intx4 su = __builtin_bit_cast(intx4, from_agpr(acc[i + 4][j]));
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            if (pass != 1) y[v] = scaled(s[v], xs[j], ch[i].w[v]);
+            if (pass == 2) y[v] = act_of<ACT>(y[v]) * scaled(su[v], xs[j], ch[i].u[v]);
+            if (pass == 1) y[v] = scaled(su[v], xs[j], ch[i].u[v]);
+          }
+        } else {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            y[v] = scaled(s[v], xs[j], ch[i].w[v]);
+            if (bias) y[v] += ch[i].bias[v];
+          }
+        }
+        tile.template put<F16>(j * 16 + (lane & 15), i * 16 + 4 * (lane >> 4), y);
+      }
+    uint16_t* out = GATED && pass == 0 ? p.G : GATED && pass == 1 ? p.U : p.Y;
+    tile.store(out + first, uint32_t(p.N), left_t, left_n);
   }
+  if (CUT && unit.slot >= 0) w8_store_run(p.cut, unit, c.wave, acc);
 }
 
 // Workgroup (cut tile, wave, block row i) adds the runs of 16 channels x 128 tokens.
 template <bool F16, bool GATED, int ACT>
-__global__ __launch_bounds__(256) void w8_gemm_sum_kernel(const W8Product p, int tiles_t) {
+__global__ __launch_bounds__(256) void w8_gemm_sum_kernel(const W8Product p, int tiles_t,
+                                                          int tiles_n) {
   constexpr int BC = GATED ? BM / 2 : BM;
   const int cut = int(blockIdx.x), wave = int(blockIdx.y), i = int(blockIdx.z);
   const int lane = threadIdx.x & 63, tile = p.cut.full + cut;
-  const int64_t t0 = int64_t(tile % tiles_t) * BN + (wave & 1) * 128 + (lane & 15);
-  const int64_t n = int64_t(tile / tiles_t) * BC + (wave >> 1) * (BC / 2) + i * 16 +
+  int tt, tn;
+  w8_tile(tile, tiles_t, tiles_n, tt, tn);
+  const int64_t t0 = int64_t(tt) * BN + (wave & 1) * 128 + (lane & 15);
+  const int64_t n = int64_t(tn) * BC + (wave >> 1) * (BC / 2) + i * 16 +
                     4 * (lane >> 4);
   if (n >= p.N) return;
   const Channels<GATED> ch = channels<F16, GATED>(p, n);
@@ -112,7 +129,7 @@ hipError_t launch_gemm(const W8Product& p, hipStream_t st) {
   const int tiles_t = int((p.T + BN - 1) / BN), tiles_n = int((p.N + BC - 1) / BC);
   if (!p.cut.runs) {
     w8_gemm_kernel<F16, GATED, ACT, false>
-        <<<unsigned(gemm_blocks(tiles_t, tiles_n)), NT, 0, st>>>(p, tiles_t, tiles_n);
+        <<<unsigned(tiles_t * tiles_n), NT, 0, st>>>(p, tiles_t, tiles_n);
     return hipGetLastError();
   }
   const int cut = tiles_t * tiles_n - p.cut.full;
@@ -121,7 +138,7 @@ hipError_t launch_gemm(const W8Product& p, hipStream_t st) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   w8_gemm_sum_kernel<F16, GATED, ACT>
-      <<<dim3(unsigned(cut), 4, GATED ? 4 : 8), 256, 0, st>>>(p, tiles_t);
+      <<<dim3(unsigned(cut), 4, GATED ? 4 : 8), 256, 0, st>>>(p, tiles_t, tiles_n);
   return hipGetLastError();
 }
 
