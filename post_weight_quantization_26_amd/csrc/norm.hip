@@ -67,45 +67,18 @@ __global__ __launch_bounds__(kRowThreads<W>) void norm_kernel(const Norm p) {
   if (p.codes) quantize_row<W, V>(x, row, K, t, red2, p.codes, p.steps);
 }
 
-// Gradient, first launch. A group of W waves takes every groups-th row and
-// keeps its columns' sums of dy·xh and dy in registers, so dY and X are read
-// once and dX written once; the groups' sums go to `partial` (float32), which a
-// second launch adds up in a fixed order. A row's values are loaded one row
-// ahead. Bound by HBM.
-template <int DT>
-struct Raw {   // a piece as loaded: 16-bit types stay packed
-  uint4 v;
-  template <int W>
-  __device__ __forceinline__ void load(const void* base, int64_t at, int K, int c, int t) {
-    const int col = row_col<W>(c, t);
-    if (col + 8 <= K) {
-      v = load16(element<DT>(base, at + col));
-      return;
-    }
-    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (col + e < K)
-        w[e >> 1] |= uint32_t(static_cast<const uint16_t*>(base)[at + col + e]) << (16 * (e & 1));
-    v = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-  __device__ __forceinline__ void get(float (&x)[8]) const { unpack8<DT>(v, x); }
-};
-template <>
-struct Raw<0> {
-  float v[8];
-  template <int W>
-  __device__ __forceinline__ void load(const void* base, int64_t at, int K, int c, int t) {
-    load_piece<0, W>(base, at, K, c, t, v);
-  }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = v[e];
-  }
-};
-
-template <int DT, int W, int V>
-__global__ __launch_bounds__(kRowThreads<W>) void norm_back_kernel(const NormBack p) {
+// Gradient, first launch. A group of waves takes every groups-th row and keeps
+// its columns' sums of dy·xh and dy in registers, so dY and X are read once and
+// dX written once; the groups' sums go to `partial` (float32), which a second
+// launch adds up in a fixed order. A row's values are loaded one row ahead.
+// Bound by HBM for long batches (8192 rows of 8192: 84 us, 4.8 TB/s), by the chain
+// of a row's loads, sums and barrier for short ones.
+//
+// Up to 8192 columns a lane holds 8 of them and a group has as many waves as that
+// takes, up to 16 (W): 8 waves of 16 columns a lane ran 1111 rows of 5000 in 30 us,
+// 10 waves of 8 in 18, both launches. WHOLE: K is a multiple of 8.
+template <int DT, int W, int V, bool WHOLE>
+__global__ __launch_bounds__(V == 4 ? 512 : kRowThreads<W>) void norm_back_kernel(const NormBack p) {
   __shared__ float2 red[2][16];
   const int t = row_thread<W>(), K = int(p.K);
   const int64_t group = row_of<W>(blockIdx.x);
@@ -114,7 +87,7 @@ __global__ __launch_bounds__(kRowThreads<W>) void norm_back_kernel(const NormBac
   float g[V][8], ag[V][8] = {}, ab[V][8] = {};
 #pragma unroll
   for (int c = 0; c < V; ++c) load_weight<DT, W>(p.gamma, p.gamma32, K, c, t, g[c]);
-  Raw<DT> rx[V], ry[V];
+  Piece<DT> rx[V], ry[V];
   float2 st = make_float2(0.f, 0.f);
   int64_t row = group;
   auto load = [&](int64_t r) {
@@ -122,8 +95,8 @@ __global__ __launch_bounds__(kRowThreads<W>) void norm_back_kernel(const NormBac
     st = *reinterpret_cast<const float2*>(p.stats + 2 * r);
 #pragma unroll
     for (int c = 0; c < V; ++c) {
-      rx[c].template load<W>(p.X, r * K, K, c, t);
-      ry[c].template load<W>(p.dY, r * K, K, c, t);
+      rx[c].template load<W, WHOLE>(p.X, r * K, K, c, t);
+      ry[c].template load<W, WHOLE>(p.dY, r * K, K, c, t);
     }
   };
   load(row);
@@ -133,8 +106,8 @@ __global__ __launch_bounds__(kRowThreads<W>) void norm_back_kernel(const NormBac
 #pragma unroll
     for (int c = 0; c < V; ++c) {
       float x[8], dy[8];
-      rx[c].get(x);
-      ry[c].get(dy);
+      rx[c].template get<W, WHOLE>(K, c, t, x);
+      ry[c].template get<W, WHOLE>(K, c, t, dy);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         xh[c][e] = (x[e] - mean) * rstd;
@@ -152,12 +125,10 @@ __global__ __launch_bounds__(kRowThreads<W>) void norm_back_kernel(const NormBac
       // a wave is back at this buffer two rows on, past the other's barrier
       if ((threadIdx.x & 63) == 0) red[par][threadIdx.x >> 6] = make_float2(s1, s2);
       __syncthreads();
-      s1 = s2 = 0.f;
-#pragma unroll
-      for (int i = 0; i < W; ++i) {
-        s1 += red[par][i].x;
-        s2 += red[par][i].y;
-      }
+      const unsigned i = threadIdx.x & 15;
+      const float2 part = i < blockDim.x / 64 ? red[par][i] : make_float2(0.f, 0.f);
+      s1 = row16_sum(part.x);
+      s2 = row16_sum(part.y);
     }
     const float c1 = p.rms ? 0.f : s1 * inv_k, c2 = s2 * inv_k;
 #pragma unroll
@@ -211,8 +182,7 @@ __global__ __launch_bounds__(1024) void norm_sums_kernel(const float* __restrict
 
 template <int DT, int W, int V>
 hipError_t launch_fwd(const Norm& p, hipStream_t st) {
-  const unsigned grid = unsigned(W == 1 ? (p.T + 3) / 4 : p.T);
-  norm_kernel<DT, W, V><<<grid, kRowThreads<W>, 0, st>>>(p);
+  norm_kernel<DT, W, V><<<row_grid<W, V>(p.T), row_block<W, V>(p.K), 0, st>>>(p);
   return hipGetLastError();
 }
 
@@ -220,17 +190,21 @@ template <int DT>
 hipError_t launch_fwd_t(const Norm& p, hipStream_t st) {
   if (p.K <= 512) return launch_fwd<DT, 1, 1>(p, st);
   if (p.K <= 1024) return launch_fwd<DT, 1, 2>(p, st);
-  if (p.K <= 2048) return launch_fwd<DT, 4, 1>(p, st);
-  if (p.K <= 4096) return launch_fwd<DT, 4, 2>(p, st);
-  if (p.K <= 8192) return launch_fwd<DT, 4, 4>(p, st);
-  if (p.K <= 16384) return launch_fwd<DT, 8, 4>(p, st);
+  // Up to a row a CU latency counts, and more waves of 8 columns a lane save some (33
+  // rows of 4096: 4.0 instead of 4.5 us); else 16 a lane (28672 rows of 8192: 182
+  // instead of 233, with 32 a lane 201).
+  if (p.T <= 256 && p.K <= 8192) return launch_fwd<DT, 16, 1>(p, st);
+  if (p.K <= 16384) return launch_fwd<DT, 16, 2>(p, st);
   return hipErrorInvalidValue;
 }
 
 template <int DT, int W, int V>
 hipError_t launch_back(const NormBack& p, hipStream_t st) {
-  const unsigned grid = unsigned(W == 1 ? (p.groups + 3) / 4 : p.groups);
-  norm_back_kernel<DT, W, V><<<grid, kRowThreads<W>, 0, st>>>(p);
+  const unsigned grid = row_grid<W, V>(p.groups), threads = row_block<W, V>(p.K);
+  if (p.K % 8 == 0)
+    norm_back_kernel<DT, W, V, true><<<grid, threads, 0, st>>>(p);
+  else
+    norm_back_kernel<DT, W, V, false><<<grid, threads, 0, st>>>(p);
   return hipGetLastError();
 }
 
@@ -238,10 +212,8 @@ template <int DT>
 hipError_t launch_back_t(const NormBack& p, hipStream_t st) {
   if (p.K <= 512) return launch_back<DT, 1, 1>(p, st);
   if (p.K <= 1024) return launch_back<DT, 1, 2>(p, st);
-  if (p.K <= 2048) return launch_back<DT, 4, 1>(p, st);
-  if (p.K <= 4096) return launch_back<DT, 4, 2>(p, st);
-  if (p.K <= 8192) return launch_back<DT, 8, 2>(p, st);
-  if (p.K <= 16384) return launch_back<DT, 8, 4>(p, st);
+  if (p.K <= 8192) return launch_back<DT, 16, 1>(p, st);
+  if (p.K <= 16384) return launch_back<DT, 16, 4>(p, st);
   return hipErrorInvalidValue;
 }
 

@@ -79,21 +79,18 @@ __global__ __launch_bounds__(256) void dequantize_rows8_kernel(const int8_t* __r
 
 template <int DT, int W, int V>
 hipError_t launch_quantize(const QuantizeRows8& p, hipStream_t st) {
-  const unsigned grid = unsigned(W == 1 ? (p.T + 3) / 4 : p.T);
-  quantize_rows8_kernel<DT, W, V><<<grid, kRowThreads<W>, 0, st>>>(p.X, p.s, p.T, int(p.K),
-                                                                   p.codes, p.steps);
+  quantize_rows8_kernel<DT, W, V><<<row_grid<W, V>(p.T), row_block<W, V>(p.K), 0, st>>>(
+      p.X, p.s, p.T, int(p.K), p.codes, p.steps);
   return hipGetLastError();
 }
 
-// K up to 512·W·V
+// K up to 512·W·V. 16 columns a lane where a row fits 16 waves so: 28672 rows of 8192
+// take 118 us, with 8 a lane 142, with 32 124.
 template <int DT>
 hipError_t launch_quantize_t(const QuantizeRows8& p, hipStream_t st) {
   if (p.K <= 512) return launch_quantize<DT, 1, 1>(p, st);
   if (p.K <= 1024) return launch_quantize<DT, 1, 2>(p, st);
-  if (p.K <= 2048) return launch_quantize<DT, 4, 1>(p, st);
-  if (p.K <= 4096) return launch_quantize<DT, 4, 2>(p, st);
-  if (p.K <= 8192) return launch_quantize<DT, 4, 4>(p, st);
-  if (p.K <= 16384) return launch_quantize<DT, 8, 4>(p, st);
+  if (p.K <= 16384) return launch_quantize<DT, 16, 2>(p, st);
   if (p.K <= 32768) return launch_quantize<DT, 16, 4>(p, st);
   if (p.K <= 65536) return launch_quantize<DT, 16, 8>(p, st);
   return hipErrorInvalidValue;
