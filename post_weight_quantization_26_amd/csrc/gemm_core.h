@@ -196,14 +196,6 @@ __device__ __forceinline__ void mfma16_first(floatx4& c, const bf16x8_t& a, cons
 __device__ __forceinline__ void mfma16_first(floatx4& c, const f16x8_t& a, const f16x8_t& b) {
   asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, 0" : "=a"(c) : "v"(a), "v"(b));
 }
-// 16 codes an operand; the accumulator's registers hold 4 int32 sums (whose
-// zero is the float's).
-__device__ __forceinline__ void mfma16(floatx4& c, const i8x16_t& a, const i8x16_t& b) {
-  asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
-}
-__device__ __forceinline__ void mfma16_first(floatx4& c, const i8x16_t& a, const i8x16_t& b) {
-  asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, 0" : "=a"(c) : "v"(a), "v"(b));
-}
 template <bool FIRST, class V>
 __device__ __forceinline__ void mfma16_acc(floatx4& c, const V& a, const V& b) {
   if (FIRST) mfma16_first(c, a, b);
@@ -212,8 +204,7 @@ __device__ __forceinline__ void mfma16_acc(floatx4& c, const V& a, const V& b) {
 // lane l supplies row l % 16 of a block and k 8·(l / 16) .. +7 of the
 // 32-wide k-step ks (chunk 4·ks + l / 16); block i is 16 rows further on,
 // which leaves the (row / 2) % 8 swizzle unchanged
-template <class Ctx>
-__device__ __forceinline__ void frag_offsets16(const Ctx& c, int (&rdA)[2], int (&rdB)[2]) {
+__device__ __forceinline__ void frag_offsets16(const GemmCtx64& c, int (&rdA)[2], int (&rdB)[2]) {
   const int lane = threadIdx.x & 63;
   const int wm = c.wave >> 1, wn = c.wave & 1;
 #pragma unroll
@@ -247,16 +238,6 @@ __device__ __forceinline__ void copy64(const GemmCtx64& c, int kt, int q) {
                                              16, c.vbaseB[j & 1] + kofsB, j * c.stepB, 0, 0);
   }
 }
-// The same for a context of another layout, which brings its own copy.
-template <int S, class Ctx>
-__device__ __forceinline__ void copy64(const Ctx& c, int kt, int q) {
-  c.template copy<S>(kt, q);
-}
-template <int S, class Ctx>
-__device__ __forceinline__ void dma64(const Ctx& c, int kt) {
-#pragma unroll
-  for (int q = 0; q < 16; ++q) copy64<S>(c, kt, q);
-}
 // Only A's copies of k-tile kt (for loops whose B operand is formed in
 // registers).
 template <int S>
@@ -270,11 +251,11 @@ __device__ __forceinline__ void dma64_a(const GemmCtx64& c, int kt) {
 // NEXT: the copies fetch k-tile 0 of another tile (context cn) instead of
 // k-tile kt + 1 of this one.
 // INIT: without PREV, the accumulators hold a starting value.
-template <int S, bool PREV, bool NEXT = false, bool INIT = false, class V, class Ctx>
-__device__ __forceinline__ void region16(const Ctx& c, const int (&rdA)[2], const int (&rdB)[2],
+template <int S, bool PREV, bool NEXT = false, bool INIT = false, class V>
+__device__ __forceinline__ void region16(const GemmCtx64& c, const int (&rdA)[2], const int (&rdB)[2],
                                          int kt, floatx4 (&acc)[8][8], V (&f0a)[8], V (&f0b)[8],
-                                         V (&f1a)[8], V (&f1b)[8], const Ctx* cn = nullptr) {
-  const Ctx& cc = NEXT ? *cn : c;
+                                         V (&f1a)[8], V (&f1b)[8], const GemmCtx64* cn = nullptr) {
+  const GemmCtx64& cc = NEXT ? *cn : c;
   const int ktc = NEXT ? 0 : kt + 1;
   if (PREV) {
 #pragma unroll
@@ -318,9 +299,9 @@ __device__ __forceinline__ void mfma_8x8(floatx4 (&acc)[8][8], const V (&fa)[8],
 // them safe to read (the last MFMAs have drained). INIT: adds to what they
 // hold instead; k-tile 0's copies (dma64<0>(c, 0)) are the caller's then, so
 // that they can be in flight while it makes that starting value.
-// V: the operands' type; of 8-bit codes the context counts pairs as elements.
-template <class V, bool INIT = false, class Ctx>
-__device__ __forceinline__ void gemm_mainloop16_of(const Ctx& c, floatx4 (&acc)[8][8]) {
+template <bool F16, bool INIT = false>
+__device__ __forceinline__ void gemm_mainloop16(const GemmCtx64& c, floatx4 (&acc)[8][8]) {
+  typedef typename Operand<F16>::type V;
   int rdA[2], rdB[2];
   frag_offsets16(c, rdA, rdB);
   if constexpr (!INIT) dma64<0>(c, 0);
@@ -344,11 +325,6 @@ __device__ __forceinline__ void gemm_mainloop16_of(const Ctx& c, floatx4 (&acc)[
   for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) asm volatile("" : "+a"(acc[i][j]));
-}
-
-template <bool F16, bool INIT = false>
-__device__ __forceinline__ void gemm_mainloop16(const GemmCtx64& c, floatx4 (&acc)[8][8]) {
-  gemm_mainloop16_of<typename Operand<F16>::type, INIT>(c, acc);
 }
 
 // The k-loop of one tile in a chain of tiles: k-tile 0 is already in stage

@@ -10,7 +10,7 @@
 // twice the length. fp16 for bf16 gradients too: it keeps 3 bits more, and a
 // power of two per row takes the place of bf16's range. Launch 1 forms A; then
 //  * many tokens: launch 2 writes the codes' transpose as the fp16 operand of [K, C]
-//    and launch 3 is the 256x256 main loop of gemm_core.h;
+//    and launch 3 is the 256x256 main loop of w8_ring.h;
 //  * fewer: w8_back_few.hip takes the codes as they are.
 #include "w8_cut.h"
 #include "w8_back.h"
@@ -60,7 +60,9 @@ __device__ __forceinline__ uint32_t block_max(uint32_t m) {
   return r;
 }
 
-// A's element (t, c), c over the layers' Np each: panels of 64 c (w8_cut.h), or, for
+// A's element (t, c), c over the layers' Np each: panels of 64 c of every token (a
+// tile's k-tile is 32 KiB in one piece, where rows of 44 KB take a page for two:
+// gradient of 4096 tokens of a pair of 11008, its product 634 -> 576 us), or, for
 // few tokens, the order of that kernel's operand: blocks of 32 c x 16 tokens, a
 // lane's 8 consecutive c together.
 __device__ __forceinline__ int64_t operand_at(const W8Back& p, int64_t t, int64_t c) {
@@ -229,12 +231,13 @@ void w8_back_gemm_kernel(const W8Back p, int steps, int tiles_t, int tiles_k) {
   const int64_t rows_t = p.T - t0 < BN ? p.T - t0 : BN;
   int k0 = 0, k1 = steps;
   if constexpr (CUT) w8_run(p.cut, unit, steps, k0, k1);
-  const int64_t step_a = p.K * 64, step_b = p.T * 64;
-  PanelCtx c;
-  panel_setup(c, p.B + k0 * step_a + o0 * 64, rows_o, step_a, p.A + k0 * step_b + t0 * 64, rows_t,
-              step_b, k1 - k0);
+  const int64_t panel_a = p.K * 64, panel_b = p.T * 64;
+  RingCtx c;
+  c.wave = uniform(int(threadIdx.x >> 6));
+  c.a.set(p.B + k0 * panel_a + o0 * 64, int(rows_o), 128, c.wave * 64, panel_a * 2, k1 - k0);
+  c.b.set(p.A + k0 * panel_b + t0 * 64, int(rows_t), 128, c.wave * 64, panel_b * 2, k1 - k0);
   floatx4 acc[8][8];
-  gemm_mainloop16_of<f16x8_t>(c, acc);
+  ring_mainloop<f16x8_t>(c, acc);
   if (CUT && unit.slot >= 0) {
     w8_store_run(p.cut, unit, c.wave, acc);
     return;

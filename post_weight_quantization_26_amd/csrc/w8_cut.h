@@ -4,70 +4,11 @@
 // register order (1 KiB per store) and a second launch adds them.
 #pragma once
 
-#include "gemm_core.h"
 #include "w8_common.h"
+#include "w8_ring.h"
 
 namespace awq {
 namespace {
-
-// Operands in panels: 64 consecutive elements of every row (one k-tile), then the
-// next 64. A tile's k-tile is 32 KiB in one piece, where long rows take a page or
-// two for each: 4096 tokens of a pair of 11008 (rows of 44 KB) 634 -> 576 us, one of
-// 11008 (22 KB) 274 -> 277.
-struct PanelCtx {
-  const uint16_t *A, *B;        // the tile's first rows in the first panel
-  int64_t step_a, step_b;       // elements of a panel
-  int bytes_a, bytes_b;         // of the tile's valid rows in a panel
-  int v[2];                     // the lane's byte offset in copy 0, for even and odd copies
-  int wave, KT;
-  template <int S>
-  __device__ __forceinline__ void copy(int kt, int q) const {
-    // copy q of the 16 a wave issues per k-tile: rows 8·(q % 8) on of A for q < 8, then B
-    const int j = q & 7, k = kt < KT ? kt : 0, past = kt < KT ? 0 : BM * 128;
-    const uint16_t* base = q < 8 ? A + k * step_a : B + k * step_b;
-    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint16_t*>(base), 0, q < 8 ? bytes_a : bytes_b, 0x00020000);
-    uint4* to = (q < 8 ? stage64_a<S>() : stage64_b<S>()) + (wave * 8 + j) * 64;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, AWQ_LDS(to), 16, v[j & 1] + past + j * 1024, 0, 0,
-                                             0);
-  }
-};
-
-// The main loop's context with everything that the compiler has to know to be
-// uniform said so: else every copy is a loop over the lanes' resources (4096
-// tokens of 4096x11008: 165 instead of 150 us).
-template <class T>
-__device__ __forceinline__ const T* uniform(const T* p) {
-  const uint64_t u = reinterpret_cast<uint64_t>(p);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(u)),
-                 hi = __builtin_amdgcn_readfirstlane(uint32_t(u >> 32));
-  return reinterpret_cast<const T*>(uint64_t(hi) << 32 | lo);
-}
-__device__ __forceinline__ void w8_setup(GemmCtx64& c, const uint16_t* A, int64_t rows_a,
-                                         const uint16_t* B, int64_t rows_b, int64_t ld,
-                                         int64_t k) {
-  gemm_setup64(c, uniform(A), __builtin_amdgcn_readfirstlane(int(rows_a)), ld, uniform(B),
-               __builtin_amdgcn_readfirstlane(int(rows_b)), ld, k, false);
-  c.KT = __builtin_amdgcn_readfirstlane(c.KT);
-}
-__device__ __forceinline__ void panel_setup(PanelCtx& c, const uint16_t* A, int64_t rows_a,
-                                            int64_t step_a, const uint16_t* B, int64_t rows_b,
-                                            int64_t step_b, int steps) {
-  c.A = uniform(A);
-  c.B = uniform(B);
-  c.step_a = step_a;
-  c.step_b = step_b;
-  c.bytes_a = __builtin_amdgcn_readfirstlane(int(rows_a)) * 128;
-  c.bytes_b = __builtin_amdgcn_readfirstlane(int(rows_b)) * 128;
-  c.wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
-  c.KT = __builtin_amdgcn_readfirstlane(steps);
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int row = c.wave * 64 + 8 * j + (lane >> 3);
-    c.v[j] = (row - 8 * j) * 128 + ((lane & 7) ^ ((row >> 1) & 7)) * 16;
-  }
-}
 
 // A workgroup's tile and, of a cut one, its run (slot >= 0).
 struct W8Unit {
@@ -161,7 +102,7 @@ struct WaveTile {
   static constexpr int kChunks = COLS / 8;
   uint4* lds;
   __device__ __forceinline__ WaveTile(int wave)
-      : lds(wave == 0 ? s64A0 : wave == 1 ? s64A1 : wave == 2 ? s64B0 : s64B1) {}
+      : lds(wave == 0 ? ring0 : wave == 1 ? ring1 : wave == 2 ? ring2 : ring3) {}
   __device__ __forceinline__ uint4* at(int t, int chunk) const {
     return lds + t * kChunks + (chunk ^ (COLS == 64 ? (t >> 1) & 7 : t & 15));
   }

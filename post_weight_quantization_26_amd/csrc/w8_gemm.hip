@@ -1,4 +1,4 @@
-// 8-bit products of many tokens: the 256x256 main loop of gemm_core.h with
+// 8-bit products of many tokens: the 256x256 main loop of w8_ring.h with
 // v_mfma_i32_16x16x64_i8, whose operands have the size of 16 bits' 16x16x32 at
 // twice the multiplications. The main loop's A rows are output channels, so a
 // lane holds 4 consecutive outputs of a token and the epilogue (steps, bias or
@@ -18,32 +18,26 @@ void w8_gemm_kernel(const W8Product p, int tiles_t, int tiles_n) {
   constexpr int BC = GATED ? BM / 2 : BM;   // output channels of a tile
   const W8Unit unit = w8_unit<CUT>(p.cut, tiles_t, tiles_n);
   const int64_t t0 = int64_t(unit.tt) * BN, n0 = int64_t(unit.tn) * BC;
-  const int64_t ld = p.K / 2;               // codes in pairs
-  int kt0 = 0, kt1 = int(ld / BK64);
+  int kt0 = 0, kt1 = int(p.K / 128);
   if constexpr (CUT) w8_run(p.cut, unit, kt1, kt0, kt1);
-  const int64_t k0 = int64_t(kt0) * BK64, k1 = int64_t(kt1) * BK64;
-  const uint16_t* x = reinterpret_cast<const uint16_t*>(p.x) + t0 * ld + k0;
+  const int64_t k0 = int64_t(kt0) * 128;
   const int64_t rows_t = p.T - t0 < BN ? p.T - t0 : BN;
-  GemmCtx64 c;
+  RingCtx c;
+  c.wave = uniform(int(threadIdx.x >> 6));
+  c.b.set(p.x + t0 * p.K + k0, int(rows_t), int(p.K), c.wave * 64, 128, kt1 - kt0);
   if constexpr (GATED) {
     // wave w copies A rows 64w .. + 63: 64 channels from n0 + 64·(w / 2) of the
     // first layer (even w) or of the second
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t first = n0 + 64 * (w >> 1), last = p.N - 1;
-    const int64_t left = p.N - first;
-    const int64_t rows = left < 0 ? 0 : left < 64 ? left : 64;
-    const uint16_t* q = reinterpret_cast<const uint16_t*>(w & 1 ? p.u.q : p.w.q) +
-                        (first < p.N ? first : last) * ld + k0;
-    w8_setup(c, q, rows, x, rows_t, ld, k1 - k0);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) c.vbaseA[j] -= w * 64 * int(ld) * 2;
+    const int64_t first = n0 + 64 * (c.wave >> 1), left = p.N - first;
+    const int8_t* q = (c.wave & 1 ? p.u.q : p.w.q) + (left > 0 ? first : p.N - 1) * p.K + k0;
+    c.a.set(q, left < 0 ? 0 : left < 64 ? int(left) : 64, int(p.K), 0, 128,
+            kt1 - kt0);
   } else {
     const int64_t rows = p.N - n0 < BM ? p.N - n0 : BM;
-    w8_setup(c, reinterpret_cast<const uint16_t*>(p.w.q) + n0 * ld + k0, rows, x, rows_t, ld,
-             k1 - k0);
+    c.a.set(p.w.q + n0 * p.K + k0, int(rows), int(p.K), c.wave * 64, 128, kt1 - kt0);
   }
   floatx4 acc[8][8];
-  gemm_mainloop16_of<i8x16_t>(c, acc);
+  ring_mainloop<i8x16_t>(c, acc);
 
   const int lane = threadIdx.x & 63;
   const int wm = c.wave >> 1, wn = c.wave & 1;
