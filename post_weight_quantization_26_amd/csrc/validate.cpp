@@ -867,15 +867,15 @@ static bool w8_sizes_ok(int64_t T, int64_t N, int64_t K, int32_t layers) {
 
 // 256x256 tiles: time in us for rounds of 256 tiles and the last ones, whole or cut
 // into the runs that take least. Steps are slower the more CUs work, a round's ends
-// take 14 us, the runs' sums 0.035 us each and a launch.
+// take 10 us, the runs' sums 0.045 us each and a launch.
 static double w8_big_us(int64_t rows, int64_t T, int64_t steps, LoraCut& cut) {
   const int64_t tiles = ceil_div(T, 256) * ceil_div(rows, 256), rest = tiles % 256;
   const double s = double(steps);
   cut = LoraCut{};
-  double tail = rest ? 14 + s * (0.93 + 0.55 * double(rest) / 256) : 0;
+  double tail = rest ? 10 + s * (0.87 + 0.55 * double(rest) / 256) : 0;
   for (int64_t runs = 2; rest && runs <= std::min<int64_t>(256 / rest, steps / 2); ++runs) {
     const double units = double(rest * runs);
-    const double t = 12 + 0.035 * units + s / double(runs) * (0.93 + 0.55 * units / 256);
+    const double t = 14 + 0.045 * units + s / double(runs) * (0.87 + 0.55 * units / 256);
     if (t < tail) {
       tail = t;
       cut.runs = runs;
@@ -885,7 +885,7 @@ static double w8_big_us(int64_t rows, int64_t T, int64_t steps, LoraCut& cut) {
     cut.full = tiles - rest;
     cut.bytes = size_t(rest) * size_t(cut.runs) * 256 * 256 * 4;
   }
-  return double(tiles / 256) * (14 + 1.5 * s) + tail;
+  return double(tiles / 256) * (10 + 1.42 * s) + tail;
 }
 
 // Tile and runs of the contraction for a product of `rows` output channels, T
@@ -981,7 +981,8 @@ W8BackLayout w8_back_layout(int64_t T, int64_t N, int64_t K, int32_t layers) {
   // With a transposed layer (its codes read and written at about 4.4 bytes a ns)
   const double big = w8_big_us(K, T, l.C / 64, l.cut) + 5 + double(l.C) * double(K) * 3 / 4.4e6;
   // or from the codes: a wave's blocks of 32 rows at `alone` us where every CU has a
-  // workgroup at most, `full` where it has all it can hold
+  // workgroup at most, `full` where one has all it can hold, which the others wait for
+  // (with the mean over the CUs in its place the choices took 9% more on average)
   struct Shape {
     int t;
     int64_t slots;
@@ -995,8 +996,8 @@ W8BackLayout w8_back_layout(int64_t T, int64_t N, int64_t K, int32_t layers) {
     if (tiles > 8192 && least) continue;
     for (int64_t runs = 1; runs <= 12 && (runs == 1 || runs * 8 <= blocks); ++runs) {
       const int64_t units = tiles * runs;
-      const double load =
-          std::min(1.0, std::max(0.0, double(units - 256) / double(s.slots - 256)));
+      const double load = std::min(
+          1.0, double(ceil_div(units, 256) - 1) / double(s.slots / 256 - 1));   // of the fullest CU
       double us = 4 + double(ceil_div(units, s.slots)) * double(blocks) / double(4 * runs) *
                           (s.alone + (s.full - s.alone) * load);
       if (runs > 1) us += 4 + double(runs) * double(T) * double(K) * 8 / 4e6;
