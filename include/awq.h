@@ -488,8 +488,8 @@ awq_status awq_act_unpack8(const int8_t* codes, const float* steps, awq_dtype dt
  * float32 product rounded once to `dtype` (a value within a rounding of the
  * type's largest may come back as an infinity). X bf16, f16 or f32, K any up to
  * 65536, at most 2^34 elements; X, s, codes and steps aligned to their
- * elements (rows of a multiple of 8 values with 16-byte aligned buffers run
- * faster). Outputs must not overlap inputs. Neither synchronises. */
+ * elements (rows of a multiple of 8 values with 16-byte aligned buffers run a
+ * little faster). Outputs must not overlap inputs. Neither synchronises. */
 awq_status awq_quantize_rows8(const void* X, awq_dtype dtype, int64_t T, int64_t K,
                               const float* s, int8_t* codes, float* steps, void* stream);
 awq_status awq_dequantize_rows8(const int8_t* codes, const float* steps, awq_dtype dtype,
@@ -531,7 +531,7 @@ awq_status awq_layer_norm_backward(const void* dY, const void* X, const float* s
  * by wsteps_n, the bias (NULL: none; in `dtype`) is added, and the result is
  * rounded once to `dtype` (bf16 or f16). A step that is NaN makes its row or
  * column NaN. K a multiple of 128 below 131072 (the sum fits 32 bits with codes
- * down to -128), N any below 2^23, T any, N*K at most 2^34. codes, qweight, Y, G and U
+ * down to -128), N any below 2^23, T any below 2^22, N*K at most 2^34. codes, qweight, Y, G and U
  * 16-byte aligned, bias 2, steps 4. ws: at least awq_w8a8_workspace_bytes(T, N,
  * K, layers) bytes, 16-byte aligned (NULL where that is 0), layers 1, or 2 for
  * a gated pair. Does not synchronise.

@@ -890,12 +890,13 @@ static double w8_big_us(int64_t rows, int64_t T, int64_t steps, LoraCut& cut) {
 
 // Tile and runs of the contraction for a product of `rows` output channels, T
 // tokens and `steps` steps of 128 bytes, by an estimate in us of each choice: the
-// steps of the rounds it takes, 5 for a launch and, with runs, 3 and their sums'
-// bytes. Over random sizes the choice was within 6% of the best one on average.
-// us, chosen first: 64 tokens of 4096x11008 15.5 (128x32, 4 runs), 27 (1 run), 96
-// (256x256); 200 of 11008x4096 23 (128x64), 27 (128x32), 26 (128x128), 48; 800 of
-// 4096x11008 53 (128x128), 55 (128x64); 1600 78 (256x256 cut in 2), 98 (256x128),
-// 102 (128x128), 112 (128x64).
+// steps of the rounds it takes, 5 for a launch and, with runs, 2 for the other, 0.4 a
+// run and their sums' bytes. Over 36 sizes of 20 to 400 tokens the choice took 1% more
+// than the best one on average.
+// us, chosen first: 64 tokens of 4096x11008 15 to 18 (128x32, 4 runs), 27 (1 run), 26
+// (256x256, cut in 14); 200 of 11008x4096 23 (128x64), 27 (128x32), 26 (128x128), 32
+// (256x256, cut in 5); 800 of 4096x11008 56 (128x64), 53 (128x128), 55 (256x256, cut in
+// 4); 1600 80 (256x256, cut in 2), 98 (256x128), 102 (128x128), 112 (128x64).
 struct W8Tiling {
   bool big;
   int tile_n, tile_t;
@@ -924,7 +925,7 @@ static W8Tiling w8_tiling(int64_t rows, int64_t T, int64_t steps) {
       const double rounds = s.pairs ? std::max(1.0, double(units) / 256)
                                     : double(ceil_div(units, 256));
       double us = 5 + rounds * s.us * double(steps) / double(runs);
-      if (runs > 1) us += 3 + double(runs) * double(T) * double(rows) * 8 / 6e6;
+      if (runs > 1) us += 2 + double(runs) * (0.4 + double(T) * double(rows) * 8 / 3e6);
       if (us < least) {
         least = us;
         best.big = false;

@@ -87,7 +87,8 @@ hipError_t launch_mid(const W8Product& p, hipStream_t st) {
     w8_mid_kernel<F16, GATED, ACT, RA, TR, false><<<grid, 256, 0, st>>>(p, tiles_n, tiles_t);
     return hipGetLastError();
   }
-  if constexpr (RA == 128) w8_mid_kernel<F16, GATED, ACT, RA, TR, true><<<grid, 256, 0, st>>>(p, tiles_n, tiles_t);
+  if constexpr (RA == 128)
+    w8_mid_kernel<F16, GATED, ACT, RA, TR, true><<<grid, 256, 0, st>>>(p, tiles_n, tiles_t);
   else return hipErrorInvalidValue;   // runs are cut of tiles of 128 rows only
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

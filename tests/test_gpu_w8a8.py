@@ -160,7 +160,7 @@ def test_gated(api, dtype, act, T, N, K):
 # whole, all cut into runs, and the last ones cut behind 256 whole ones.
 FORMS = [(17, 16, 2048), (1500, 7, 2048), (4400, 1, 4096), (6000, 129, 128), (6000, 520, 128),
          (4400, 1048, 128), (4100, 3001, 2048), (1000, 2000, 8192), (4100, 4096, 4096),
-         (2050, 3718, 384), (4100, 1168, 6400)]
+         (2050, 3718, 384), (4100, 1168, 6400), (5372, 1, 14336), (33, 520, 4096)]
 # 256x256 tiles of 6 to 11 k-tiles: every number that the main loop's rounds leave over.
 FORMS += [(4000, 4090, k) for k in (768, 896, 1024, 1152, 1280, 1408)]
 
