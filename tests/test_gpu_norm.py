@@ -21,7 +21,8 @@ def api():
 
 SHAPES = [(1, 1), (3, 5), (9, 64), (5, 129), (300, 512), (4, 513), (7, 1000), (1100, 1024),
           (3, 1152), (2, 2048), (5, 2049), (300, 4096), (3, 4104), (513, 5003), (2, 8192), (3, 8193),
-          (2, 11008), (3, 16383), (300, 16384)]
+          (2, 11008), (3, 16383), (300, 16384), (5, 1030), (4, 2052), (300, 1997), (257, 3002),
+          (256, 3002), (2, 12)]
 
 
 def weights(K, dtype, wide, seed=5):

@@ -56,7 +56,7 @@ def close(got, ref, err, what):
 
 ROWS = [(1, 1), (3, 5), (5, 8), (2, 129), (7, 512), (4, 513), (6, 1000), (3, 1024), (2, 2048),
         (5, 2056), (33, 4096), (3, 4099), (2, 8192), (3, 8200), (2, 16384), (2, 20001), (2, 32768),
-        (2, 40000), (1, 65535), (2, 65536)]
+        (2, 40000), (1, 65535), (2, 65536), (5, 1030), (4, 2052), (6, 1997), (300, 3002), (2, 12)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
