@@ -76,7 +76,7 @@ __global__ __launch_bounds__(kRowThreads<W>) void norm_kernel(const Norm p) {
 //
 // Up to 8192 columns a lane holds 8 of them and a group has as many waves as that
 // takes, up to 16 (W): 8 waves of 16 columns a lane ran 1111 rows of 5000 in 30 us,
-// 10 waves of 8 in 18, both launches. WHOLE: K is a multiple of 8.
+// 10 waves of 8 in 17, both launches. WHOLE: K is a multiple of 8.
 template <int DT, int W, int V, bool WHOLE>
 __global__ __launch_bounds__(V == 4 ? 512 : kRowThreads<W>) void norm_back_kernel(const NormBack p) {
   __shared__ float2 red[2][16];

@@ -2,10 +2,11 @@
 // reductions shared by the row quantiser (rows8.hip) and the norms (norm.hip).
 //
 // W is 1 (a workgroup of 4 waves holds 4 rows, a wave each) or 16 (a workgroup is one
-// row, of as many waves as it takes, up to 16). A lane holds V pieces of 8 consecutive values, which one or two loads of
-// 16 bytes bring wherever the row starts: global memory takes them at any
-// element's address, and rows of odd lengths run nearly as fast as aligned ones.
-// Only a row's last piece, if it is not whole, is stored element by element.
+// row, of as many waves as it takes, up to 16). A lane holds V pieces of 8 consecutive
+// values, which one or two loads of 16 bytes bring wherever the row starts: global
+// memory takes them at any element's address, and rows of odd lengths run nearly as
+// fast as aligned ones. Only a row's last piece, if it is not whole, is stored element
+// by element.
 #pragma once
 
 #include "act8.h"
