@@ -26,11 +26,8 @@ void w8_gemm_kernel(const W8Product p, int tiles_t, int tiles_n) {
   c.wave = uniform(int(threadIdx.x >> 6));
   c.b.set(p.x + t0 * p.K + k0, int(rows_t), int(p.K), c.wave * 64, 128, kt1 - kt0);
   if constexpr (GATED) {
-    // wave w copies A rows 64w .. + 63: 64 channels from n0 + 64·(w / 2) of the
-    // first layer (even w) or of the second
-    const int64_t first = n0 + 64 * (c.wave >> 1), left = p.N - first;
-    const int8_t* q = (c.wave & 1 ? p.u.q : p.w.q) + (left > 0 ? first : p.N - 1) * p.K + k0;
-    c.a.set(q, left < 0 ? 0 : left < 64 ? int(left) : 64, int(p.K), 0, 128,
+    const PairRows rows = pair_rows(n0, c.wave, p.N);
+    c.a.set((c.wave & 1 ? p.u.q : p.w.q) + rows.first * p.K + k0, rows.valid, int(p.K), 0, 128,
             kt1 - kt0);
   } else {
     const int64_t rows = p.N - n0 < BM ? p.N - n0 : BM;

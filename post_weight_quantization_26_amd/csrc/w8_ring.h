@@ -18,6 +18,7 @@
 #pragma once
 
 #include "gemm_core.h"
+#include "w8_ring_range.h"
 
 namespace awq {
 namespace {
@@ -57,34 +58,29 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 struct RingSide {
   const char* at;
   int64_t next;
-  int bytes, shorter;   // from `at` to the end of the last valid row; less by a k-tile
+  RingRange range;
   int v[2], rows;       // the lane's offset in even and odd copies; bytes of 8 rows
-  int left;             // k-tiles
   // wave_row: the first row that the wave copies, from `first`
   __device__ __forceinline__ void set(const void* first, int valid, int row, int wave_row,
                                       int64_t to_next, int tiles) {
     at = uniform(static_cast<const char*>(first));
     next = to_next;
-    bytes = uniform(valid) * row;
-    shorter = to_next == 128 ? 128 : 0;   // within a row, or a panel of every row's 128
+    range = ring_range(uniform(valid), row, to_next, uniform(tiles));
     rows = 8 * row;
-    left = uniform(tiles);
-    const int lane = threadIdx.x & 63, r = lane >> 3;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)   // rows of 8 chunks as swz64 has them
-      v[j] = (wave_row + r) * row + ((lane & 7) ^ ((r >> 1) + 4 * j)) * 16;
+    for (int j = 0; j < 2; ++j) v[j] = ring_offset(wave_row, threadIdx.x & 63, j, row);
   }
   // copy j of the wave's 8: 8 rows into unit U
   template <int U>
   __device__ __forceinline__ void copy(int wave, int j) const {
     const __amdgpu_buffer_rsrc_t rs =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(at), 0, bytes, 0x00020000);
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(at), 0, range.bytes, 0x00020000);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, AWQ_LDS(ring_unit<U>() + (wave * 8 + j) * 64), 16,
                                              v[j & 1], j * rows, 0, 0);
   }
   __device__ __forceinline__ void advance() {
     at += next;
-    bytes = --left > 0 ? bytes - shorter : 0;
+    range.advance();
   }
 };
 struct RingCtx {
@@ -137,7 +133,7 @@ __device__ __forceinline__ void ring_mainloop(RingCtx& c, floatx4 (&acc)[8][8]) 
     rda[ks] = swz64((c.wave >> 1) * 128 + (lane & 15), 4 * ks + (lane >> 4));
     rdb[ks] = swz64((c.wave & 1) * 128 + (lane & 15), 4 * ks + (lane >> 4));
   }
-  int n = c.a.left;
+  int n = c.a.range.left;
 #pragma unroll
   for (int j = 0; j < 8; ++j) c.a.template copy<0>(c.wave, j);
   c.a.advance();

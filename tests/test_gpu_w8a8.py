@@ -186,6 +186,16 @@ def test_forms(api, T, N, K, pair):
     close(H, h, R.rounded(h, eh, dtype), "H")
 
 
+# 256x256 tiles of a pair whose last one holds channels for its first half only: whole,
+# the last ones cut, all cut.
+HALVES = [(1100, 4097, 2048), (2051, 4160, 4096), (1000, 2112, 8192)]
+
+
+@pytest.mark.parametrize("T,N,K", HALVES)
+def test_pairs_that_end_in_a_tile_s_first_half(api, T, N, K):
+    test_forms(api, T, 2 * N, K, True)
+
+
 @pytest.mark.parametrize("T", [3, 20, 300])
 def test_offsets_past_32_bits(api, T):
     """A layer of more than 2^32 bytes: its last channels, and its gradient."""

@@ -1,0 +1,54 @@
+"""CPU: the plans of the 8-bit products and which bytes their 256x256 main loop
+copies, from the same C++ that the library is built of."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+from post_weight_quantization_26_amd import build_lib
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+
+
+@pytest.fixture(scope="module")
+def host(tmp_path_factory):
+    out = str(tmp_path_factory.mktemp("w8_host") / "w8_host.so")
+    res = subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", build_lib.INCLUDE,
+                          "-I", build_lib.CSRC, os.path.join(HERE, "w8_host.cpp"),
+                          os.path.join(build_lib.CSRC, "validate.cpp"), "-o", out],
+                         capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr[-2000:]
+    return ctypes.CDLL(out)
+
+
+def ask(fn, n, *sizes):
+    out = (ctypes.c_int64 * n)()
+    fn(*(ctypes.c_int64(v) for v in sizes[:3]), *(ctypes.c_int32(v) for v in sizes[3:]), out)
+    return list(out)
+
+
+def in_order(got):
+    past, missed, stray = got
+    return past <= 0 and missed == 0 and stray == 0
+
+
+@pytest.mark.parametrize("layers", [1, 2])
+def test_every_edge_of_the_channels_stays_in_the_layer(host, layers):
+    """Every number of channels that a last tile can hold, one k-tile and several, the
+    contraction whole and in runs."""
+    for rest in range(256 // layers):
+        N = 512 + rest
+        for T, K, runs in ((257, 128, 1), (300, 640, 1), (511, 1152, 3)):
+            got = ask(host.w8_host_replay, 3, T, N, K, layers, runs)
+            assert in_order(got), (T, N, K, layers, runs, got)
+
+
+@pytest.mark.parametrize("T,N,K", [(2051, 11040, 4096), (2051, 4160, 11008), (300, 14368, 5120),
+                                   (4100, 2752, 4096), (4096, 6848, 4096), (8192, 28680, 8192)])
+def test_pairs_that_end_in_a_tile_s_first_half(host, T, N, K):
+    """Layers whose last tile of a pair has no channel for two of the four waves."""
+    form, _, _, _, _, runs, _ = ask(host.w8_host_plan, 7, T, N, K, 2)
+    assert form == 2
+    for r in {1, max(1, runs)}:
+        assert in_order(ask(host.w8_host_replay, 3, T, N, K, 2, r))
