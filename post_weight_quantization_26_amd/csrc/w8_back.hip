@@ -234,8 +234,10 @@ void w8_back_gemm_kernel(const W8Back p, int steps, int tiles_t, int tiles_k) {
   const int64_t panel_a = p.K * 64, panel_b = p.T * 64;
   RingCtx c;
   c.wave = uniform(int(threadIdx.x >> 6));
-  c.a.set(p.B + k0 * panel_a + o0 * 64, int(rows_o), 128, c.wave * 64, panel_a * 2, k1 - k0);
-  c.b.set(p.A + k0 * panel_b + t0 * 64, int(rows_t), 128, c.wave * 64, panel_b * 2, k1 - k0);
+  c.a.set(RingKind::kPanels, p.B + k0 * panel_a + o0 * 64, int(rows_o), 128, c.wave * 64,
+          panel_a * 2, k1 - k0);
+  c.b.set(RingKind::kPanels, p.A + k0 * panel_b + t0 * 64, int(rows_t), 128, c.wave * 64,
+          panel_b * 2, k1 - k0);
   floatx4 acc[8][8];
   ring_mainloop<f16x8_t>(c, acc);
   if (CUT && unit.slot >= 0) {

@@ -24,14 +24,15 @@ void w8_gemm_kernel(const W8Product p, int tiles_t, int tiles_n) {
   const int64_t rows_t = p.T - t0 < BN ? p.T - t0 : BN;
   RingCtx c;
   c.wave = uniform(int(threadIdx.x >> 6));
-  c.b.set(p.x + t0 * p.K + k0, int(rows_t), int(p.K), c.wave * 64, 128, kt1 - kt0);
+  c.b.set(RingKind::kRows, p.x + t0 * p.K + k0, int(rows_t), int(p.K), c.wave * 64, 128, kt1 - kt0);
   if constexpr (GATED) {
     const PairRows rows = pair_rows(n0, c.wave, p.N);
-    c.a.set((c.wave & 1 ? p.u.q : p.w.q) + rows.first * p.K + k0, rows.valid, int(p.K), 0, 128,
-            kt1 - kt0);
+    c.a.set(RingKind::kRows, (c.wave & 1 ? p.u.q : p.w.q) + rows.first * p.K + k0, rows.valid,
+            int(p.K), 0, 128, kt1 - kt0);
   } else {
     const int64_t rows = p.N - n0 < BM ? p.N - n0 : BM;
-    c.a.set(p.w.q + n0 * p.K + k0, int(rows), int(p.K), c.wave * 64, 128, kt1 - kt0);
+    c.a.set(RingKind::kRows, p.w.q + n0 * p.K + k0, int(rows), int(p.K), c.wave * 64, 128,
+            kt1 - kt0);
   }
   floatx4 acc[8][8];
   ring_mainloop<i8x16_t>(c, acc);

@@ -61,11 +61,12 @@ struct RingSide {
   RingRange range;
   int v[2], rows;       // the lane's offset in even and odd copies; bytes of 8 rows
   // wave_row: the first row that the wave copies, from `first`
-  __device__ __forceinline__ void set(const void* first, int valid, int row, int wave_row,
-                                      int64_t to_next, int tiles) {
+  // (a panel's length alone does not tell: one token's panels are 128 bytes, too)
+  __device__ __forceinline__ void set(RingKind kind, const void* first, int valid, int row,
+                                      int wave_row, int64_t to_next, int tiles) {
     at = uniform(static_cast<const char*>(first));
     next = to_next;
-    range = ring_range(uniform(valid), row, to_next, uniform(tiles));
+    range = ring_range(kind, uniform(valid), row, uniform(tiles));
     rows = 8 * row;
 #pragma unroll
     for (int j = 0; j < 2; ++j) v[j] = ring_offset(wave_row, threadIdx.x & 63, j, row);

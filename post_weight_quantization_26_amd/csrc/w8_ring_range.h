@@ -12,11 +12,13 @@ struct RingRange {
   int bytes, shorter, left;   // shorter: what a k-tile takes off
   constexpr void advance() { bytes = --left > 0 ? bytes - shorter : 0; }
 };
-// `valid` rows of `row` bytes, k-tiles to_next bytes apart.
-constexpr RingRange ring_range(int valid, int row, int64_t to_next, int tiles) {
-  // within a row, or a panel of every row's 128; an empty range stays empty: below 0 the
-  // hardware would take it for one of 4 GiB
-  return {valid * row, valid && to_next == 128 ? 128 : 0, tiles};
+// Where the next k-tile lies: 128 bytes on in every row, or in the next panel of every
+// row's 128 bytes, which is as long as this one.
+enum class RingKind { kRows, kPanels };
+// `valid` rows of `row` bytes.
+constexpr RingRange ring_range(RingKind kind, int valid, int row, int tiles) {
+  // an empty range stays empty: below 0 the hardware would take it for one of 4 GiB
+  return {valid * row, kind == RingKind::kRows && valid ? 128 : 0, tiles};
 }
 
 // A lane's 16 bytes in even (j = 0) and odd (1) copies of a wave, 8 rows each from row

@@ -339,6 +339,35 @@ def test_gradient_forms(api, T, N, K, pair):
     close(dX, ref, R.rounded(ref, err, dtype), "dX")
 
 
+# One token against a contraction so long that it takes the transposed layer.
+ONE_TOKEN = [(1, 150000, 128, 1), (1, 318000, 256, 1), (1, 80000, 128, 2), (1, 160000, 256, 2)]
+
+
+@pytest.mark.parametrize("T,N,K,layers", ONE_TOKEN)
+def test_gradient_of_one_token(api, T, N, K, layers):
+    """Terms of -1, 0 and 1, whose sums (a deviation of 460 at most, 2048 is fp16's last
+    whole number) have no rounding anywhere: every channel counts."""
+    gen = torch.Generator().manual_seed(N)
+
+    def whole(*shape):
+        return torch.randint(-1, 2, shape, generator=gen)
+
+    two = [(whole(N, K).to(torch.int8).cuda(), torch.full((N,), w, device="cuda"))
+           for w in (1.0, 2.0 ** -6)[:layers]]
+    dH = whole(T, N).half().cuda()
+    if layers == 1:
+        dX = api.w8a8_backward(dH, *two[0])
+        ref = npy(dH) @ npy(two[0][0])
+    else:
+        # silu at 64 is 64, its slope 1: exp(-64) is far below a step of 1
+        pre = torch.full((T, N), 64.0, dtype=torch.float16, device="cuda"), whole(T, N).half().cuda()
+        dX, dG, dU = api.w8a8_gated_backward(dH, pre, *two)
+        assert torch.equal(dG, dH * pre[1]) and torch.equal(dU, dH * 64)
+        ref = npy(dG) @ npy(two[0][0]) + npy(dH) @ npy(two[1][0])
+    assert np.abs(ref).max() <= 2048
+    assert np.array_equal(npy(dX), ref)
+
+
 @pytest.mark.parametrize("T", [30, 4100])
 def test_gradient_with_steps_off_16_bytes(api, T):
     """Steps and gradients of any alignment that the calls take."""

@@ -52,3 +52,24 @@ def test_pairs_that_end_in_a_tile_s_first_half(host, T, N, K):
     assert form == 2
     for r in {1, max(1, runs)}:
         assert in_order(ask(host.w8_host_replay, 3, T, N, K, 2, r))
+
+
+# One token and a few rows of dX against a long contraction: the fewest that take the
+# transposed layer, one layer and a pair.
+ONE_TOKEN = [(1, 150000, 128, 1), (1, 318000, 256, 1), (1, 80000, 128, 2), (1, 160000, 256, 2)]
+
+
+@pytest.mark.parametrize("T,N,K,layers", ONE_TOKEN)
+def test_gradient_of_one_token_reads_every_panel(host, T, N, K, layers):
+    few, _, _, _, runs, _ = ask(host.w8_host_back_plan, 6, T, N, K, layers)
+    assert not few and runs > 1
+    for r in (1, runs):
+        got = ask(host.w8_host_back_replay, 3, T, N, K, layers, r)
+        assert in_order(got), (r, got)
+
+
+def test_every_number_of_tokens_reads_its_panels(host):
+    for T in [*range(1, 70), 127, 128, 129, 255, 256, 257, 511, 512, 513]:
+        for K, runs in ((128, 1), (256, 1), (384, 3)):
+            got = ask(host.w8_host_back_replay, 3, T, 700, K, 1, runs)
+            assert in_order(got), (T, K, runs, got)

@@ -74,22 +74,43 @@ extern "C" void w8_host_replay(int64_t T, int64_t N, int64_t K, int32_t layers, 
       for (int64_t tt : edges(ceil_div(T, 256))) {
         const int64_t t0 = tt * 256;
         const int valid = int(std::min<int64_t>(T - t0, 256));
-        rep.operand(ring_range(valid, int(K), 128, k1 - k0), t0 * K + k0 * 128, 128, int(K),
-                    wave * 64, valid, T * K, k1 - k0);
+        rep.operand(ring_range(RingKind::kRows, valid, int(K), k1 - k0), t0 * K + k0 * 128, 128,
+                    int(K), wave * 64, valid, T * K, k1 - k0);
       }
       for (int64_t tn : edges(ceil_div(N, channels))) {
         const int64_t n0 = tn * channels;
         if (layers == 2) {
           const PairRows rows = pair_rows(n0, wave, N);
-          rep.operand(ring_range(rows.valid, int(K), 128, k1 - k0), rows.first * K + k0 * 128, 128,
-                      int(K), 0, rows.valid, N * K, k1 - k0);
+          rep.operand(ring_range(RingKind::kRows, rows.valid, int(K), k1 - k0),
+                      rows.first * K + k0 * 128, 128, int(K), 0, rows.valid, N * K, k1 - k0);
         } else {
           const int valid = int(std::min<int64_t>(N - n0, 256));
-          rep.operand(ring_range(valid, int(K), 128, k1 - k0), n0 * K + k0 * 128, 128, int(K),
-                      wave * 64, valid, N * K, k1 - k0);
+          rep.operand(ring_range(RingKind::kRows, valid, int(K), k1 - k0), n0 * K + k0 * 128, 128,
+                      int(K), wave * 64, valid, N * K, k1 - k0);
         }
       }
     }
+  }
+  answer(rep, out);
+}
+
+// A gradient through the transposed layer (w8_back.hip): both operands in panels of 64 of
+// the contraction, 128 bytes a row.
+extern "C" void w8_host_back_replay(int64_t T, int64_t N, int64_t K, int32_t layers, int32_t runs,
+                                    int64_t* out) {
+  const int64_t C = layers * ceil_div(N, 64) * 64;
+  const int steps = int(C / 64);
+  Replay rep;
+  for (int run = 0; run < runs; ++run) {
+    const int k0 = steps * run / runs, k1 = steps * (run + 1) / runs;
+    for (int wave = 0; wave < 4; ++wave)
+      for (int64_t rows : {K, T})
+        for (int64_t tile : edges(ceil_div(rows, 256))) {
+          const int64_t o0 = tile * 256, panel = rows * 128;
+          const int valid = int(std::min<int64_t>(rows - o0, 256));
+          rep.operand(ring_range(RingKind::kPanels, valid, 128, k1 - k0), k0 * panel + o0 * 128,
+                      panel, 128, wave * 64, valid, rows * C * 2, k1 - k0);
+        }
   }
   answer(rep, out);
 }
