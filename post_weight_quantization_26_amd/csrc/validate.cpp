@@ -995,7 +995,9 @@ W8BackLayout w8_back_layout(int64_t T, int64_t N, int64_t K, int32_t layers) {
   for (const Shape& s : shapes) {
     const int64_t tiles = (K / 128) * ceil_div(T, s.t);
     if (tiles > 8192 && least) continue;
+    if (!grid_fits(ceil_div(K / 128, 8) * 8 * ceil_div(T, s.t), 256)) continue;
     for (int64_t runs = 1; runs <= 12 && (runs == 1 || runs * 8 <= blocks); ++runs) {
+      if (runs > 1 && !grid_fits(ceil_div(T * K, 2048), 256)) break;   // the sums' launch
       const int64_t units = tiles * runs;
       const double load = std::min(
           1.0, double(ceil_div(units, 256) - 1) / double(s.slots / 256 - 1));   // of the fullest CU
@@ -1009,7 +1011,7 @@ W8BackLayout w8_back_layout(int64_t T, int64_t N, int64_t K, int32_t layers) {
       }
     }
   }
-  l.few = least < big;
+  l.few = least && least < big;
   l.a = take(size_t(l.few ? ceil_div(T, 16) * 16 : T) * size_t(l.C) * 2);
   l.e = take(size_t(T) * 4);
   if (l.few) {

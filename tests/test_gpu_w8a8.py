@@ -368,6 +368,18 @@ def test_gradient_of_one_token(api, T, N, K, layers):
     assert np.array_equal(npy(dX), ref)
 
 
+def test_gradient_of_millions_of_tokens(api):
+    """More 16-token tiles than one launch can hold."""
+    T, N, K = 3400000, 1, 9600
+    q, w = layer8(N, K, 5)
+    dY = randn(T, N, seed=9, dtype="f16")
+    dX = api.w8a8_backward(dY, q, w)
+    for part in (slice(0, 40), slice(1700000, 1700040), slice(T - 40, T)):
+        d = npy(dY[part])
+        ref, err = R.back_product([(d, np.zeros_like(d), npy(q), npy(w))])
+        close(dX[part], ref, R.rounded(ref, err, "f16"), "dX")
+
+
 @pytest.mark.parametrize("T", [30, 4100])
 def test_gradient_with_steps_off_16_bytes(api, T):
     """Steps and gradients of any alignment that the calls take."""

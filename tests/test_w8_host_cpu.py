@@ -2,6 +2,7 @@
 copies, from the same C++ that the library is built of."""
 import ctypes
 import os
+import random
 import subprocess
 
 import pytest
@@ -73,3 +74,23 @@ def test_every_number_of_tokens_reads_its_panels(host):
         for K, runs in ((128, 1), (256, 1), (384, 3)):
             got = ask(host.w8_host_back_replay, 3, T, 700, K, 1, runs)
             assert in_order(got), (T, K, runs, got)
+
+
+def test_gradient_grids_fit(host):
+    """Straight from the codes, of which a workgroup takes few tokens: a launch holds less
+    than 2^32 threads a dimension."""
+    def up(a, b):
+        return -(-a // b)
+
+    rng = random.Random(1)
+    sizes = [(1000000, 1, 65536, 1), (4122381, 1, 127232, 2), (3064641, 2, 10368, 2),
+             (2255534, 101, 14464, 1), ((1 << 22) - 1, 1, 130944, 1)]
+    sizes += [(int(2 ** rng.uniform(0, 22)), int(2 ** rng.uniform(0, 21)),
+               128 * int(2 ** rng.uniform(0, 9.99)), rng.choice((1, 2))) for _ in range(20000)]
+    for T, N, K, layers in sizes:
+        if N * K * layers > 1 << 34:
+            continue
+        few, tile_t, runs, _, _, _ = ask(host.w8_host_back_plan, 6, T, N, K, layers)
+        if few:
+            assert up(K // 128, 8) * 8 * up(T, tile_t) * 256 < 1 << 32, (T, N, K, layers, tile_t)
+            assert runs == 1 or up(T * K, 2048) * 256 < 1 << 32, (T, N, K, layers, runs)
