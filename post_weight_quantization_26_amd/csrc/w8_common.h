@@ -3,6 +3,7 @@
 
 #include "gemm_types.h"
 #include "w8.h"
+#include "w8_phi.h"
 
 namespace awq {
 namespace {
@@ -18,26 +19,21 @@ __device__ __forceinline__ intx4 mfma_16x16x64(intx4 a, intx4 b, intx4 c) {
 
 // act(g) and, for the gradient, its derivative. exp and the reciprocal are the
 // hardware's (1 ulp; the argument's rounding adds |g|·2^-23, all far below the
-// output's 2^-8 or 2^-11).
+// output's 2^-8 or 2^-11); below 2^-126 both give zero, so that silu ends at g = -87.3,
+// where it is -1e-36.
 constexpr int kSilu = 0, kGelu = 1;
 __device__ __forceinline__ float sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.f + __expf(-g));
 }
-// Φ(g) from e = exp(-g²/2). For g <= 0, Φ(g) / e = erfcx(|g| / √2) / 2 is smooth and
-// falls as 1 / |g|: t·Q(t) with t = 1 / (1 + 0.3·|g|), Q the polynomial of degree 7 of
-// least relative error over t in (0.18, 1], fitted by reweighted least squares: 1.6e-7.
-// The whole is within (1.5·g² + 14) of 2^-24, relative to the tail too, the 1.5·g² from
-// the exponent's argument. The library's erfc has branches that the gated epilogues pay
-// for: 18 us more for each round of 256 tiles.
+// Φ(g) from e = exp(-g²/2): a fit of Φ / e for g <= 0 (w8_phi.h). The whole is within
+// (1.5·g² + 14) of 2^-24, relative to the tail too down to float32's smallest normal
+// numbers, the 1.5·g² from the exponent's argument. The library's erfc has branches that
+// the gated epilogues pay for: 18 us more for each round of 256 tiles.
 __device__ __forceinline__ float normal_cdf(float g, float e) {
-  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(fabsf(g), 0.3f, 1.f));
-  float q = __builtin_fmaf(t, 0.0354241431f, -0.156160012f);
-  q = __builtin_fmaf(t, q, 0.204559252f);
-  q = __builtin_fmaf(t, q, -0.0520361029f);
-  q = __builtin_fmaf(t, q, 0.127692774f);
-  q = __builtin_fmaf(t, q, 0.100175679f);
-  q = __builtin_fmaf(t, q, 0.120712183f);
-  q = __builtin_fmaf(t, q, 0.119632013f);
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(fabsf(g), kPhiT, 1.f));
+  float q = kPhi[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) q = __builtin_fmaf(t, q, kPhi[i]);
   const float tail = e * (t * q);
   return g < 0.f ? tail : 1.f - tail;
 }

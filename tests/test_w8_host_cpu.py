@@ -5,7 +5,9 @@ import os
 import random
 import subprocess
 
+import numpy as np
 import pytest
+from scipy.special import erfcx
 
 from post_weight_quantization_26_amd import build_lib
 
@@ -94,3 +96,14 @@ def test_gradient_grids_fit(host):
         if few:
             assert up(K // 128, 8) * 8 * up(T, tile_t) * 256 < 1 << 32, (T, N, K, layers, tile_t)
             assert runs == 1 or up(T * K, 2048) * 256 < 1 << 32, (T, N, K, layers, runs)
+
+
+def test_gelu_s_fit(host):
+    """Relative error of the coefficients that the kernels hold, over every argument whose
+    exponential is a normal number: 1.25e-7 is stated, the references take 2^-22.5."""
+    x = np.linspace(0, 13.22, 1000001)   # exp(-13.22²/2) < 2^-126
+    y = np.empty_like(x)
+    as_double = ctypes.POINTER(ctypes.c_double)
+    host.w8_host_phi(x.ctypes.data_as(as_double), ctypes.c_int64(len(x)), y.ctypes.data_as(as_double))
+    off = np.abs(y / (erfcx(x / np.sqrt(2)) / 2) - 1).max()
+    assert off < 1.25e-7 < 2.0 ** -22.5

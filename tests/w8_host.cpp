@@ -5,6 +5,7 @@
 #include <cstring>
 
 #include "awq_internal.h"
+#include "w8_phi.h"
 #include "w8_ring_range.h"
 
 using namespace awq;
@@ -113,4 +114,14 @@ extern "C" void w8_host_back_replay(int64_t T, int64_t N, int64_t K, int32_t lay
         }
   }
   answer(rep, out);
+}
+
+// The fit of erfcx(x / √2) / 2 with its own coefficients, exactly evaluated.
+extern "C" void w8_host_phi(const double* x, int64_t n, double* y) {
+  for (int64_t i = 0; i < n; ++i) {
+    const double t = 1 / (1 + double(kPhiT) * x[i]);
+    double q = 0;
+    for (const float c : kPhi) q = q * t + double(c);
+    y[i] = t * q;
+  }
 }
