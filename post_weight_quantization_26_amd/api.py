@@ -412,6 +412,13 @@ def _out(t: Optional[torch.Tensor], shape, dtype, like: torch.Tensor, name: str)
     return t
 
 
+def _both(pair, name: str, of: str) -> None:
+    """Two buffers that are filled together: in place of a missing one a new one would be
+    filled and lost."""
+    if len(pair) != 2 or any(t is None for t in pair):
+        raise ValueError(f"{name} must be ({of}), both given")
+
+
 def _call(device: int, fn, *args) -> None:
     """One call of the library on the current stream of GPU number ``device``,
     which need not be the current GPU."""
@@ -653,6 +660,7 @@ def layer_norm(X: torch.Tensor, gamma: torch.Tensor, beta: Optional[torch.Tensor
     if stats is not None:
         _out(stats, (T, 2), torch.float32, X, "stats")
     if rows8 is not None:
+        _both(rows8, "rows8", "codes, steps")
         codes = _out(rows8[0], (T, K), torch.int8, X, "rows8 codes")
         steps = _out(rows8[1], (T,), torch.float32, X, "rows8 steps")
     _call(X.get_device(), L.lib().awq_layer_norm, X.data_ptr(), _dtype(X), T, K, gamma.data_ptr(),
@@ -775,6 +783,7 @@ def w8a8_gated_matmul(codes: torch.Tensor, steps: torch.Tensor, gate, up, dtype:
     H = _out(out, (T, N), dtype, codes, "out")
     G = U = None
     if pre is not None:
+        _both(pre, "pre", "G, U")
         G = _out(pre[0], (T, N), dtype, codes, "pre G")
         U = _out(pre[1], (T, N), dtype, codes, "pre U")
     at, nbytes, _keep = _w8_ws(ws, w8a8_workspace_bytes(T, N, K, 2), codes)

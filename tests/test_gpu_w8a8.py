@@ -610,3 +610,19 @@ def test_wrappers_refuse_shapes_and_types(api):
                  lambda: api.quantize_rows8(torch.zeros(1, 65537, dtype=bf, **dev))):
         with pytest.raises(L.AwqError):
             call()
+
+
+def test_buffers_filled_together_are_given_together(api):
+    """A missing one would be filled as a new buffer that no one gets."""
+    bf = torch.bfloat16
+    x, g = randn(4, 128, seed=1, dtype="bf16"), randn(128, seed=2, dtype="bf16")
+    q, s = rows(4, 128, 3)
+    w = layer8(16, 128, 4)
+    y = torch.empty(4, 16, dtype=bf, device="cuda")
+    for call in (lambda: api.layer_norm(x, g, rows8=(q, None)),
+                 lambda: api.layer_norm(x, g, rows8=(None, s)),
+                 lambda: api.layer_norm(x, g, rows8=(q,)),
+                 lambda: api.w8a8_gated_matmul(q, s, w, w, bf, pre=(y, None)),
+                 lambda: api.w8a8_gated_matmul(q, s, w, w, bf, pre=(None, y))):
+        with pytest.raises(ValueError, match="both"):
+            call()
