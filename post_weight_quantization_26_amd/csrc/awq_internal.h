@@ -281,6 +281,12 @@ awq_status check_act8(const char* name, const void* X, awq_dtype d, int64_t T, i
 // 8-bit rows, norms and products.
 constexpr int64_t kRows8MaxK = 65536;
 constexpr int64_t kNormMaxK = 16384;
+// Threads of a row in the row kernels (row_block.h), at most: a wave up to 1024 columns,
+// else the waves that 8 columns a lane take, up to 16.
+inline int64_t row_threads(int64_t K) {
+  const int64_t t = ceil_div(K, 512) * 64;
+  return K <= 1024 ? 64 : t < 1024 ? t : 1024;
+}
 constexpr int64_t kW8MaxK = (int64_t(1) << 17) - 1;   // 128·128·K fits an int32
 constexpr int64_t kW8MaxN = int64_t(1) << 23;         // 256 rows of outputs: 32-bit offsets
 constexpr int64_t kW8BackMaxN = int64_t(1) << 21;

@@ -765,7 +765,7 @@ bool all_aligned16(std::initializer_list<const void*> pointers) {
   return std::all_of(pointers.begin(), pointers.end(), aligned16);
 }
 
-// The row kernels take a workgroup of up to 1024 threads per row.
+// Up to 1024 columns a workgroup holds 4 rows, else one.
 static awq_status check_rows(const char* name, awq_dtype d, int64_t T, int64_t K, int64_t most) {
   if (!dtype_ok(d)) return set_error(AWQ_E_INVALID, "%s: unknown dtype %d", name, int(d));
   if (T < 1 || K < 1 || T > kMaxDim || K > kMaxDim)
@@ -776,8 +776,7 @@ static awq_status check_rows(const char* name, awq_dtype d, int64_t T, int64_t K
                      (long long)most);
   if (T * K > kMaxMatrixElems)
     return set_error(AWQ_E_UNSUPPORTED, "%s: T*K=%lld exceeds 2^34", name, (long long)(T * K));
-  const int64_t threads = K <= 1024 ? 64 : K <= 8192 ? 256 : K <= 16384 ? 512 : 1024;
-  if (!grid_fits(T + 3, threads))
+  if (!grid_fits(T + 3, row_threads(K)))
     return set_error(AWQ_E_UNSUPPORTED, "%s: T=%lld exceeds the grid", name, (long long)T);
   return AWQ_OK;
 }

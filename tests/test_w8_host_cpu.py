@@ -107,3 +107,15 @@ def test_gelu_s_fit(host):
     host.w8_host_phi(x.ctypes.data_as(as_double), ctypes.c_int64(len(x)), y.ctypes.data_as(as_double))
     off = np.abs(y / (erfcx(x / np.sqrt(2)) / 2) - 1).max()
     assert off < 1.25e-7 < 2.0 ** -22.5
+
+
+def test_row_grids_are_checked_with_the_threads_that_rows_take(host):
+    """512·V columns of a row fill V pieces of a wave; V 1 to 8 by the kernels' forms."""
+    fn = host.w8_host_row_threads
+    fn.restype = ctypes.c_int64
+    for K in [*range(1, 1200), *range(1200, 65537, 61), 8192, 8193, 16384, 16385, 32768, 32769, 65536]:
+        pieces = [v for v in (1, 2, 4, 8) if K <= 512 * 16 * v] if K > 1024 else []
+        most = max([64, *(-(-K // (512 * v)) * 64 for v in pieces)])
+        assert most <= fn(ctypes.c_int64(K)) <= 1024, K
+        # and no size within 2^34 elements is refused for it
+        assert K <= 1024 or (2 ** 34 // K + 3) * fn(ctypes.c_int64(K)) < 2 ** 32, K

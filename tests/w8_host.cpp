@@ -125,3 +125,5 @@ extern "C" void w8_host_phi(const double* x, int64_t n, double* y) {
     y[i] = t * q;
   }
 }
+
+extern "C" int64_t w8_host_row_threads(int64_t K) { return row_threads(K); }
