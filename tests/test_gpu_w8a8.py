@@ -196,6 +196,23 @@ def test_pairs_that_end_in_a_tile_s_first_half(api, T, N, K):
     test_forms(api, T, 2 * N, K, True)
 
 
+# The fewest tokens that the forms take, with the form that each size has to take.
+FEWEST = [(5, 264657, 256, 1, "128x32"), (5, 4013, 16896, 1, "128x32 runs"),
+          (33, 32186, 128, 1, "128x64"), (33, 8718, 9088, 1, "128x64 runs"),
+          (65, 30937, 512, 1, "128x128"), (65, 6389, 60288, 1, "128x128 runs"),
+          (65, 64611, 128, 1, "256x128"), (5, 530, 128512, 1, "all cut"),
+          (129, 59267, 2688, 1, "whole"), (5, 65757, 512, 2, "128x32"),
+          (5, 5073, 6656, 2, "128x32 runs"), (33, 14592, 128, 2, "128x64"),
+          (33, 2379, 10368, 2, "128x64 runs"), (65, 15663, 512, 2, "128x128"),
+          (65, 2586, 53760, 2, "128x128 runs"), (5, 1049987, 128, 2, "256x128"),
+          (5, 265, 127232, 2, "all cut"), (129, 74643, 4224, 2, "last cut")]
+
+
+@pytest.mark.parametrize("T,N,K,layers,form", FEWEST)
+def test_fewest_tokens_of_a_form(api, T, N, K, layers, form):
+    test_forms(api, T, N * layers, K, layers == 2)
+
+
 @pytest.mark.parametrize("T", [3, 20, 300])
 def test_offsets_past_32_bits(api, T):
     """A layer of more than 2^32 bytes: its last channels, and its gradient."""
@@ -337,6 +354,18 @@ def test_gradient_forms(api, T, N, K, pair):
     ref, err = R.back_product([(dg, edg, npy(gate[0]), npy(gate[1])),
                                (du, edu, npy(up[0]), npy(up[1]))])
     close(dX, ref, R.rounded(ref, err, dtype), "dX")
+
+
+FEWEST_BACK = [(17, 1, 17024, 1, "codes 32"), (17, 1643, 3328, 1, "codes 32 runs"),
+               (33, 1, 17408, 1, "codes 64"), (33, 3211, 3584, 1, "codes 64 runs"),
+               (385, 4781, 31744, 1, "whole"), (17, 1392, 1920, 2, "codes 32 runs"),
+               (33, 1636, 3200, 2, "codes 64 runs"), (387, 8979, 30336, 2, "whole"),
+               (395, 10363, 38912, 2, "last cut")]
+
+
+@pytest.mark.parametrize("T,N,K,layers,form", FEWEST_BACK)
+def test_fewest_tokens_of_a_gradient_s_form(api, T, N, K, layers, form):
+    test_gradient_forms(api, T, N, K, layers == 2)
 
 
 # One token against a contraction so long that it takes the transposed layer.

@@ -9,6 +9,7 @@ import numpy as np
 import pytest
 from scipy.special import erfcx
 
+import test_gpu_w8a8 as gpu
 from post_weight_quantization_26_amd import build_lib
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -119,3 +120,70 @@ def test_row_grids_are_checked_with_the_threads_that_rows_take(host):
         assert most <= fn(ctypes.c_int64(K)) <= 1024, K
         # and no size within 2^34 elements is refused for it
         assert K <= 1024 or (2 ** 34 // K + 3) * fn(ctypes.c_int64(K)) < 2 ** 32, K
+
+
+# ------------------------------------------------ the forms that the GPU tests reach
+
+def cut_form(full, runs):
+    return "whole" if not runs else "last cut" if full else "all cut"
+
+
+def product_form(host, T, N, K, layers):
+    kind, tile_n, tile_t, runs, full, cut_runs, _ = ask(host.w8_host_plan, 7, T, N, K, layers)
+    if kind == 0:
+        return "few"
+    if kind == 1:
+        return f"{tile_n}x{tile_t}" + (" runs" if runs > 1 else "")
+    return cut_form(full, cut_runs)
+
+
+def gradient_form(host, T, N, K, layers):
+    few, tile_t, runs, full, cut_runs, _ = ask(host.w8_host_back_plan, 6, T, N, K, layers)
+    return f"codes {tile_t}" + (" runs" if runs > 1 else "") if few else cut_form(full, cut_runs)
+
+
+CUTS = {"whole", "last cut", "all cut"}
+PRODUCT_FORMS = {"few", "128x32", "128x32 runs", "128x64", "128x64 runs", "128x128",
+                 "128x128 runs", "256x128"} | CUTS
+GRADIENT_FORMS = {f"codes {t}{r}" for t in (16, 32, 64) for r in ("", " runs")} | CUTS
+
+
+@pytest.mark.parametrize("layers", [1, 2])
+def test_sizes_of_the_gpu_tests_take_every_form(host, layers):
+    """What chooses a form is an estimate of its time: when that changes, so do the
+    sizes that reach a form."""
+    def halved(N):
+        return N // 2 if layers == 2 and N > 1 else N
+
+    took = {product_form(host, T, N, K, layers) for T, N, K in gpu.PRODUCTS}
+    took |= {product_form(host, T, halved(N), K, layers) for T, N, K in gpu.FORMS}
+    assert took == PRODUCT_FORMS
+    # every number of k-tiles that the 256x256 main loop's rounds of 5 leave over
+    assert {K // 128 % 5 for T, N, K in gpu.FORMS
+            if product_form(host, T, halved(N), K, layers) in CUTS} == set(range(5))
+    took = {gradient_form(host, *size, layers) for size in gpu.BACK + gpu.BACK_FORMS}
+    assert took == GRADIENT_FORMS
+
+
+def test_sizes_of_the_gpu_tests_take_the_forms_they_name(host):
+    for *size, form in gpu.FEWEST:
+        assert product_form(host, *size) == form, size
+    for *size, form in gpu.FEWEST_BACK:
+        assert gradient_form(host, *size) == form, size
+    for size in gpu.ONE_TOKEN:
+        assert gradient_form(host, *size) == "all cut", size
+    assert [product_form(host, *size, 2) for size in gpu.HALVES] == ["whole", "last cut", "all cut"]
+    assert all(N % 128 in range(1, 65) for _, N, _ in gpu.HALVES)
+
+
+@pytest.mark.parametrize("layers", [1, 2])
+def test_fewest_tokens_of_the_256x256_forms_stay_in_their_operands(host, layers):
+    sizes = [s[:3] for s in gpu.FEWEST if s[3] == layers and s[4] in CUTS]
+    for T, N, K in sizes:
+        runs = ask(host.w8_host_plan, 7, T, N, K, layers)[5]
+        for r in {1, max(1, runs)}:
+            assert in_order(ask(host.w8_host_replay, 3, T, N, K, layers, r)), (T, N, K, r)
+    for T, N, K in [s[:3] for s in gpu.FEWEST_BACK if s[3] == layers and s[4] in CUTS]:
+        runs = ask(host.w8_host_back_plan, 6, T, N, K, layers)[4]
+        for r in {1, max(1, runs)}:
+            assert in_order(ask(host.w8_host_back_replay, 3, T, N, K, layers, r)), (T, N, K, r)
