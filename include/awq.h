@@ -538,7 +538,8 @@ awq_status awq_layer_norm_backward(const void* dY, const void* X, const float* s
  *
  * awq_w8a8_gated_matmul takes two layers of one input (gate and up):
  *   H = act(G)·U,  act AWQ_ACT_SILU g / (1 + e^-g) or AWQ_ACT_GELU g·Phi(g),
- * G and U the products above in float32; H is rounded once. G and U [T, N]
+ * G and U the products above in float32; H is rounded once. Where e^g or e^(-g^2/2)
+ * is below 2^-126, act(g) of a negative g is 0. G and U [T, N]
  * (both NULL: not kept) receive them in `dtype`, for the gradient.
  *
  * Gradients with respect to the input, taken as the values that its 8-bit rows

@@ -797,7 +797,9 @@ def w8a8_backward(dY: torch.Tensor, qweight: torch.Tensor, wsteps: torch.Tensor,
                   ws: Optional[torch.Tensor] = None,
                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The gradient of w8a8_matmul with respect to the values that its 8-bit
-    rows stand for: dX [T, K] in dY's dtype from dY [T, N]."""
+    rows stand for: dX [T, K] in dY's dtype from dY [T, N]. dY times the steps
+    is rounded to fp16 under a power of two per row (2^-11 of a term), for
+    either dtype; sums are float32."""
     N, K, device = _rows8(qweight, wsteps, ("qweight", "wsteps"))
     _check_on(device, ("dY",), (dY,))
     if dY.dim() != 2 or dY.shape[1] != N:
@@ -815,7 +817,8 @@ def w8a8_gated_backward(dH: torch.Tensor, pre, gate, up, act: str = "silu",
     """The gradient of w8a8_gated_matmul: (dX [T, K], dG, dU [T, N]) in dH's
     dtype from dH [T, N] and the ``pre`` = (G, U) that the forward call kept; dX
     with respect to the values that the 8-bit rows stand for, dG and dU those
-    of the two products. ``out`` = (dX, dG, dU) gives the buffers."""
+    of the two products, which times the steps are rounded for dX as in
+    w8a8_backward. ``out`` = (dX, dG, dU) gives the buffers."""
     _dev(dH, "dH")
     device = dH.get_device()
     N, K = _pair(gate, up, None, device)

@@ -71,12 +71,15 @@ __global__ __launch_bounds__(kRowThreads<W>) void norm_kernel(const Norm p) {
 // its columns' sums of dy·xh and dy in registers, so dY and X are read once and
 // dX written once; the groups' sums go to `partial` (float32), which a second
 // launch adds up in a fixed order. A row's values are loaded one row ahead.
-// Bound by HBM for long batches (8192 rows of 8192: 84 us, 4.8 TB/s), by the chain
-// of a row's loads, sums and barrier for short ones.
+// Bound by HBM for long batches (8192 rows of 8192: 80 us, 5.0 TB/s, both launches), by
+// the chain of a row's loads, sums and barrier for short ones.
 //
 // Up to 8192 columns a lane holds 8 of them and a group has as many waves as that
 // takes, up to 16 (W): 8 waves of 16 columns a lane ran 1111 rows of 5000 in 30 us,
-// 10 waves of 8 in 17, both launches. WHOLE: K is a multiple of 8.
+// 10 waves of 8 in 17, both launches. Above 8192 columns a lane holds 32 (V = 4), which
+// for float32 do not fit its registers: 2000 rows of 16384 take 134 us (bf16 43); 16
+// waves of 16 a lane took 123 there, but 178 instead of 133 for 12001. WHOLE: K is a
+// multiple of 8.
 template <int DT, int W, int V, bool WHOLE>
 __global__ __launch_bounds__(V == 4 ? 512 : kRowThreads<W>) void norm_back_kernel(const NormBack p) {
   __shared__ float2 red[2][16];

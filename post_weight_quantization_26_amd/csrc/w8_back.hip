@@ -8,7 +8,10 @@
 // One fp16 product: the steps join the gradient in the operand A (one rounding),
 // the codes are exact fp16 numbers. A pair's two sums are one contraction of
 // twice the length. fp16 for bf16 gradients too: it keeps 3 bits more, and a
-// power of two per row takes the place of bf16's range. Launch 1 forms A; then
+// power of two per row takes the place of bf16's range. The rounding is 2^-11 of a term,
+// as large as fp16's of an output (dX's mean error 2.9e-4 instead of 2.1e-4); a second
+// operand of what the first one leaves would keep float32's terms at twice the matrix
+// work, most of the time of large calls. Launch 1 forms A; then
 //  * many tokens: launch 2 writes the codes' transpose as the fp16 operand of [K, C]
 //    and launch 3 is the 256x256 main loop of w8_ring.h;
 //  * fewer: w8_back_few.hip takes the codes as they are.
@@ -150,7 +153,8 @@ __global__ __launch_bounds__(1024) void w8_grad_rows_kernel(const W8Back p) {
   }
 }
 
-// The same for any N, element by element in two passes.
+// The same for any N, element by element in two passes (a pair's gradient of 4096 tokens
+// of 4096 inputs: 757 us for 11007 outputs, 650 for 11008).
 template <bool F16, bool GATED, int ACT>
 __global__ __launch_bounds__(256) void w8_grad_rows_any_kernel(const W8Back p) {
   const int64_t t = blockIdx.x;

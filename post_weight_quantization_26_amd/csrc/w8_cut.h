@@ -58,7 +58,8 @@ __device__ __forceinline__ W8Unit w8_unit(const W8Cut& cut, int tiles_t, int til
 // First and last + 1 of a run's k-tiles, of `steps`.
 __device__ __forceinline__ void w8_run(const W8Cut& cut, const W8Unit& u, int steps, int& k0,
                                        int& k1) {
-  k0 = u.slot < 0 ? 0 : steps * u.run / cut.runs;   // both below 2^15
+  // at most 2^16 steps (a pair's gradient, N below 2^21) and 256 runs
+  k0 = u.slot < 0 ? 0 : steps * u.run / cut.runs;
   k1 = u.slot < 0 ? steps : steps * (u.run + 1) / cut.runs;
 }
 
