@@ -77,9 +77,13 @@ __global__ __launch_bounds__(kRowThreads<W>) void norm_kernel(const Norm p) {
 // Up to 8192 columns a lane holds 8 of them and a group has as many waves as that
 // takes, up to 16 (W): 8 waves of 16 columns a lane ran 1111 rows of 5000 in 30 us,
 // 10 waves of 8 in 17, both launches. Above 8192 columns a lane holds 32 (V = 4), which
-// for float32 do not fit its registers: 2000 rows of 16384 take 134 us (bf16 43); 16
-// waves of 16 a lane took 123 there, but 178 instead of 133 for 12001. WHOLE: K is a
-// multiple of 8.
+// for float32 do not fit its registers: 2000 rows of 16384 take 122 us (bf16 44), of
+// 12001 99 (40); 16 waves of 16 a lane took 123 and 178. WHOLE: K is a multiple of 8.
+//
+// Only a lane's last piece can lie past a row's end: the others hold 512 columns for
+// V = 2, which begins at 513, and 1536 for each 2048 that K begins for V = 4, which begins
+// at 8193. That they are whole is known here spares their shifts (20000 rows of 777: 37
+// -> 30 us; 2000 of 12001: float32 135 -> 99, bf16 48 -> 40).
 template <int DT, int W, int V, bool WHOLE>
 __global__ __launch_bounds__(V == 4 ? 512 : kRowThreads<W>) void norm_back_kernel(const NormBack p) {
   __shared__ float2 red[2][16];
@@ -97,10 +101,12 @@ __global__ __launch_bounds__(V == 4 ? 512 : kRowThreads<W>) void norm_back_kerne
     if (r >= p.T) return;
     st = *reinterpret_cast<const float2*>(p.stats + 2 * r);
 #pragma unroll
-    for (int c = 0; c < V; ++c) {
-      rx[c].template load<W, WHOLE>(p.X, r * K, K, c, t);
-      ry[c].template load<W, WHOLE>(p.dY, r * K, K, c, t);
+    for (int c = 0; c < V - 1; ++c) {
+      rx[c].template load<W, true>(p.X, r * K, K, c, t);
+      ry[c].template load<W, true>(p.dY, r * K, K, c, t);
     }
+    rx[V - 1].template load<W, WHOLE, true>(p.X, r * K, K, V - 1, t);
+    ry[V - 1].template load<W, WHOLE>(p.dY, r * K, K, V - 1, t);
   };
   load(row);
   for (int par = 0; row < p.T; row += p.groups, par ^= 1) {
@@ -109,11 +115,19 @@ __global__ __launch_bounds__(V == 4 ? 512 : kRowThreads<W>) void norm_back_kerne
 #pragma unroll
     for (int c = 0; c < V; ++c) {
       float x[8], dy[8];
-      rx[c].template get<W, WHOLE>(K, c, t, x);
-      ry[c].template get<W, WHOLE>(K, c, t, dy);
+      if (c < V - 1) {
+        rx[c].template get<W, true>(K, c, t, x);
+        ry[c].template get<W, true>(K, c, t, dy);
+      } else {
+        rx[c].template get<W, WHOLE, true>(K, c, t, x);
+        ry[c].template get<W, WHOLE>(K, c, t, dy);
+      }
+      // past K, where d is 0, xh is one of the row's values or 0: -mean·r may be an
+      // infinity, and 0 times it NaN
+      const float m = c + 1 < V || row_col<W>(c, t) < K ? mean : 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        xh[c][e] = (x[e] - mean) * rstd;
+        xh[c][e] = (x[e] - m) * rstd;
         ag[c][e] = __builtin_fmaf(dy[e], xh[c][e], ag[c][e]);
         ab[c][e] += dy[e];
         d[c][e] = dy[e] * g[c][e];   // 0 past K

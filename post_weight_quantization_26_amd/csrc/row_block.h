@@ -64,7 +64,8 @@ __device__ __forceinline__ const char* element(const void* base, int64_t i) {
   return static_cast<const char*>(base) + i * (DT == 0 ? 4 : 2);
 }
 
-// A piece as loaded, columns past K zero. A row's last piece, if it is not whole, loads
+// A piece as loaded, columns past K zero (SAME: within a row's last piece, not whole, some
+// of its values again). A row's last piece, if it is not whole, loads
 // the row's last 8 elements and moves them down when they are read: element by element
 // the load itself would wait for its parts (1111 rows of 5003, gradient: 34 -> 31 us).
 template <int DT>
@@ -72,8 +73,8 @@ struct Piece {
   static constexpr int kWords = DT == 0 ? 8 : 4, kEach = 8 / kWords;   // elements a word
   uint32_t w[kWords];
 
-  // WHOLE: K is a multiple of 8
-  template <int W, bool WHOLE = false>
+  // WHOLE: the piece is within the row or past it as a whole
+  template <int W, bool WHOLE = false, bool SAME = false>
   __device__ __forceinline__ void load(const void* base, int64_t at, int K, int c, int t) {
     const int col = row_col<W>(c, t);
 #pragma unroll
@@ -81,10 +82,10 @@ struct Piece {
     if (!WHOLE && K < 8) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        if (col + e >= K) continue;
-        if constexpr (DT == 0) w[e] = static_cast<const uint32_t*>(base)[at + col + e];
-        else
-          w[e >> 1] |= uint32_t(static_cast<const uint16_t*>(base)[at + col + e]) << (16 * (e & 1));
+        if (SAME ? col >= K : col + e >= K) continue;
+        const int64_t i = at + (SAME && col + e >= K ? K - 1 : col + e);
+        if constexpr (DT == 0) w[e] = static_cast<const uint32_t*>(base)[i];
+        else w[e >> 1] |= uint32_t(static_cast<const uint16_t*>(base)[i]) << (16 * (e & 1));
       }
     } else if (col < K) {
       const char* p = element<DT>(base, at + (col + 8 <= K ? col : K - 8));
@@ -99,7 +100,7 @@ struct Piece {
     }
   }
 
-  template <int W, bool WHOLE = false>
+  template <int W, bool WHOLE = false, bool SAME = false>
   __device__ __forceinline__ void get(int K, int c, int t, float (&x)[8]) const {
     uint32_t u[kWords];
 #pragma unroll
@@ -109,7 +110,7 @@ struct Piece {
       if constexpr (kEach == 2) {
 #pragma unroll
         for (int i = 0; i < kWords; ++i) {
-          const uint32_t next = i + 1 < kWords ? u[i + 1] : 0;
+          const uint32_t next = i + 1 < kWords ? u[i + 1] : SAME ? u[i] : 0;
           u[i] = n & 1 ? __builtin_amdgcn_alignbit(next, u[i], 16) : u[i];
         }
       }
@@ -117,7 +118,7 @@ struct Piece {
       for (int step = 1; step < kWords; step *= 2)
 #pragma unroll
         for (int i = 0; i < kWords; ++i) {
-          const uint32_t next = i + step < kWords ? u[i + step] : 0;
+          const uint32_t next = i + step < kWords ? u[i + step] : SAME ? u[i] : 0;
           u[i] = n & (step * kEach) ? next : u[i];
         }
     }

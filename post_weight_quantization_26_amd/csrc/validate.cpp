@@ -821,8 +821,8 @@ awq_status check_norm(const void* X, awq_dtype d, int64_t T, int64_t K, const vo
 }
 
 // Row groups of the gradient, 8 waves a CU and all with the same number of rows: at 20
-// waves a CU 4000 rows of 5003 took 35 us instead of 31 and 20000 of 777 48 instead of
-// 38. At least 4 rows, while there are as many groups as CUs, so that a group's partial
+// waves a CU 4000 rows of 5003 took 36 us instead of 33 and 20000 of 777 51 instead of
+// 30. At least 4 rows, while there are as many groups as CUs, so that a group's partial
 // sums are a small part of them.
 NormBackLayout norm_back_layout(int64_t T, int64_t K) {
   NormBackLayout l{};

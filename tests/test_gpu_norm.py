@@ -133,6 +133,25 @@ def test_special_rows(api, dtype, K):
     assert (x8[0][2:4] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [12, 96, 100, 600, 1300, 5003, 8200, 9000, 12001])
+def test_gradient_of_rows_whose_mean_over_deviation_is_no_float32(api, dtype, K):
+    """Equal values far from 0 with a small eps: mean·r is infinite, (x - mean)·r is 0.
+    Lanes behind the row's end hold no x that the mean could be taken off."""
+    X = randn(3, K, seed=K, dtype=dtype)
+    X[1] = 2.0 ** 90
+    dY = randn(3, K, seed=K + 1, scale=0.3, dtype=dtype)
+    gamma, _, wd = weights(K, dtype, False)
+    stats = torch.empty(3, 2, device="cuda")
+    Y = api.layer_norm(X, gamma, eps=1e-30, stats=stats)
+    assert (Y[1] == 0).all() and stats[1, 0] == 2.0 ** 90 and abs(stats[1, 1] * 1e-15 - 1) < 1e-6
+    dX, dgamma, dbeta = api.layer_norm_backward(dY, X, stats, gamma)
+    r = R.norm_back(npy(dY), npy(X), npy(stats), npy(gamma), False)
+    close(dX, r[0], R.rounded(r[0], r[3], dtype), "dX")
+    close(dgamma, r[1], R.rounded(r[1], r[4], wd), "dgamma")
+    close(dbeta, r[2], R.rounded(r[2], r[5], wd), "dbeta")
+
+
 def test_unaligned_views(api):
     base = randn(20, 4100, seed=1, dtype="bf16").reshape(-1)
     K = 4096
